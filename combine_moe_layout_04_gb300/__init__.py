@@ -8,9 +8,14 @@ mirror the C-ABI declared in ``include/moe_layout.h``:
     synchronises), moe_stats_device, moe_dispatch, moe_combine, moe_status,
     moe_status_string, moe_layout_noalloc,
     moe_relay_layout, moe_dispatch_relay, moe_combine_relay (the Mode 2 relay),
-    moe_expert_groups, moe_dispatch_group, moe_combine_group (per-expert groups)
+    moe_expert_groups, moe_dispatch_group, moe_combine_group (per-expert groups),
+    moe_route, moe_route_backward (the router),
+    moe_expert_forward, moe_expert_backward_rows, moe_expert_backward_weights
+    (the experts' products), moe_combine_backward,
+    moe_quant4_row_scale_bytes, moe_quant4_weight_scale_bytes, moe_quant4_rows,
+    moe_quant4_weights, moe_expert_forward4 (the experts in 4 bits)
 
-``Problem`` and ``Layout`` are conveniences that build the C structs and
+``Problem``, ``Layout``, ``Routing`` and ``Experts`` are conveniences that build the C structs and
 allocate the caller-owned device buffers.  If the shared library has not been
 built, every call raises ``MoeLibraryMissing``; there is no fallback path.
 """
@@ -38,6 +43,9 @@ MOE_STATS_HEADER_WORDS = 32
 MOE_ST_STATUS = 0  # header word holding the device status bits
 MOE_FAULT_WAIT_TIMEOUT = 1
 MOE_MOVE_AUTO, MOE_MOVE_VECTOR, MOE_MOVE_BULK = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_LAYOUT_AUTO, MOE_LAYOUT_SPLIT, MOE_LAYOUT_FUSED, MOE_LAYOUT_TWO_KERNELS = 0, 1, 2, 3
 
 # Header word names in index order (include/moe_layout.h, MOE_ST_*).
@@ -55,7 +63,10 @@ EXPORTED = ("moe_workspace_bytes", "moe_layout", "moe_stats_words", "moe_stats",
             "moe_combine", "moe_status", "moe_status_string", "moe_layout_noalloc",
             "moe_move_faults", "moe_selftest_bounded_waits", "moe_dispatch_quant", "moe_swap_plan",
             "moe_relay_layout", "moe_dispatch_relay", "moe_combine_relay",
-            "moe_expert_groups", "moe_dispatch_group", "moe_combine_group")
+            "moe_expert_groups", "moe_dispatch_group", "moe_combine_group",
+            "moe_route", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
+            "moe_expert_backward_weights", "moe_combine_backward", "moe_quant4_row_scale_bytes",
+            "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4")
 
 
 class MoeLibraryMissing(RuntimeError):
@@ -137,6 +148,16 @@ class _RelayC(ctypes.Structure):
                 ("capacity", ctypes.c_int64)]
 
 
+class _RoutingC(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("logits_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
+
+
+class _ExpertsC(ctypes.Structure):
+    _fields_ = [("in_cols", ctypes.c_int32), ("out_cols", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("weights", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -182,6 +203,21 @@ def load_library(path: str = LIB_PATH):
     lib.moe_dispatch_group.restype = i
     lib.moe_combine_group.argtypes = [P, L, vp, vp, i32, i32, vp, vp, vp, vp, vp]
     lib.moe_combine_group.restype = i
+    G, X = ctypes.POINTER(_RoutingC), ctypes.POINTER(_ExpertsC)
+    bytes_out = ctypes.POINTER(ctypes.c_size_t)
+    for name, args in (("moe_route", [P, G, vp, vp, vp, vp, vp]),
+                       ("moe_route_backward", [P, G, vp, vp, vp, vp, vp]),
+                       ("moe_combine_backward", [P, L, vp, vp, vp, vp, vp, vp]),
+                       ("moe_expert_forward", [P, L, X, vp, vp, vp, vp]),
+                       ("moe_expert_backward_rows", [P, L, X, vp, vp, vp, vp]),
+                       ("moe_expert_backward_weights", [P, L, X, vp, vp, vp, vp]),
+                       ("moe_quant4_row_scale_bytes", [P, i32, bytes_out]),
+                       ("moe_quant4_weight_scale_bytes", [P, X, bytes_out]),
+                       ("moe_quant4_rows", [P, L, i32, vp, vp, vp, vp]),
+                       ("moe_quant4_weights", [P, X, vp, vp, vp]),
+                       ("moe_expert_forward4", [P, L, X, vp, vp, vp, vp, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
     lib.moe_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
     lib.moe_status.restype = i
     lib.moe_layout_noalloc.argtypes = [P, vp, L, vp]
@@ -290,6 +326,53 @@ class Relay:
     def c(self) -> _RelayC:
         return _RelayC(self.relay_pos.data_ptr(), self.relay_src.data_ptr(), self.slot_relay.data_ptr(),
                        self.capacity)
+
+
+@dataclass
+class Routing:
+    """How the router makes its gates (moe_routing in include/moe_layout.h)."""
+    score: int = MOE_SCORE_SOFTMAX
+    renormalise: bool = True
+    scale: float = 1.0
+
+    def c(self, logits) -> _RoutingC:
+        return _RoutingC(self.score, int(self.renormalise), self.scale,
+                         MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32)
+
+
+@dataclass
+class Experts:
+    """The experts of a layer (moe_experts in include/moe_layout.h): weights
+    bf16 [E, W, in_cols], or 4-bit codes [E, W, in_cols / 2] with their scale
+    blocks; W = out_cols, or 2 * out_cols (gate rows, then up rows) with
+    MOE_ACT_SWIGLU."""
+    in_cols: int
+    out_cols: int
+    weights: object = None
+    act: int = MOE_ACT_NONE
+    scales: object = None
+
+    @property
+    def weight_rows(self) -> int:
+        return 2 * self.out_cols if self.act == MOE_ACT_SWIGLU else self.out_cols
+
+    def c(self) -> _ExpertsC:
+        return _ExpertsC(self.in_cols, self.out_cols, self.act, 0, _ptr(self.weights), _ptr(self.scales))
+
+
+def _take(where: str, t, dtype: str, *shape):
+    """Address of a tensor argument that has to be dense, of one of the given
+    types and of the given shape (None: anything, -1: any size there)."""
+    if t is None:
+        return None
+    if hasattr(t, "is_contiguous"):
+        kind = str(t.dtype).replace("torch.", "")
+        sizes = tuple(t.shape)
+        fits = not shape or (len(sizes) == len(shape) and all(a in (-1, b) for a, b in zip(shape, sizes)))
+        if not t.is_contiguous() or kind not in dtype.split("|") or not fits:
+            raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {dtype} tensor {list(shape) or ''} is wanted, "
+                                            f"not {kind} {list(sizes)}")
+    return t.data_ptr()
 
 
 def _check(rc: int, where: str):
@@ -425,6 +508,133 @@ def moe_combine_group(problem: Problem, layout: Layout, ids, expert_group, group
                                             _ptr(expert_group), int(group), int(num_groups), _ptr(y),
                                             _ptr(weights), _ptr(acc), _ptr(out), _stream(stream)),
            "moe_combine_group")
+
+
+def moe_route(problem: Problem, routing: Routing, logits, ids, gates, bias=None, stream=None):
+    """ids and gates of every token's top-k experts from logits [T, E] (fp32 or bf16)."""
+    p, where = problem, "moe_route"
+    _check(load_library().moe_route(
+        ctypes.byref(p.c()), ctypes.byref(routing.c(logits)),
+        _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
+        _take(where, bias, "float32", p.num_experts), _take(where, ids, "int32", p.num_tokens, p.topk),
+        _take(where, gates, "float32", p.num_tokens, p.topk), _stream(stream)), where)
+
+
+def moe_route_backward(problem: Problem, routing: Routing, logits, ids, dgates, dlogits, stream=None):
+    """dlogits [T, E] (of the logits' type) from the gates' gradient."""
+    p, where = problem, "moe_route_backward"
+    at = _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts)
+    if getattr(logits, "dtype", None) != getattr(dlogits, "dtype", None):
+        raise MoeError(MOE_ERR_INVALID, f"{where}: dlogits has the logits' type")
+    _check(load_library().moe_route_backward(
+        ctypes.byref(p.c()), ctypes.byref(routing.c(logits)), at, _take(where, ids, "int32", p.num_tokens, p.topk),
+        _take(where, dgates, "float32", p.num_tokens, p.topk),
+        _take(where, dlogits, "float32|bfloat16", p.num_tokens, p.num_experts), _stream(stream)), where)
+
+
+def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy, dweights, stream=None):
+    """Gradients of moe_combine: dy [T*k, h] and dweights [T, k] from dout [T, h]."""
+    p, where = problem, "moe_combine_backward"
+    slots = p.num_tokens * p.topk
+    _check(load_library().moe_combine_backward(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take(where, dout, "bfloat16", p.num_tokens, p.hidden),
+        _take(where, y, "bfloat16", slots, p.hidden), _take(where, weights, "float32", p.num_tokens, p.topk),
+        _take(where, dy, "bfloat16", slots, p.hidden), _take(where, dweights, "float32", p.num_tokens, p.topk),
+        _stream(stream)), where)
+
+
+def _take_weights(where: str, p: Problem, x: Experts):
+    _take(where, x.weights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols)
+    return ctypes.byref(x.c())
+
+
+def moe_expert_forward(problem: Problem, layout: Layout, experts: Experts, rows, out, pre=None, stream=None):
+    """out [T*k, out_cols] = every receive row times its expert's weights, gated
+    with MOE_ACT_SWIGLU (pre [T*k, W] then receives what the gate is made of)."""
+    p, x, where = problem, experts, "moe_expert_forward"
+    slots = p.num_tokens * p.topk
+    _check(load_library().moe_expert_forward(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take_weights(where, p, x),
+        _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, pre, "bfloat16", slots, x.weight_rows),
+        _take(where, out, "bfloat16", slots, x.out_cols), _stream(stream)), where)
+
+
+def moe_expert_backward_rows(problem: Problem, layout: Layout, experts: Experts, dout, drows, pre=None, stream=None):
+    """drows [T*k, in_cols] = dout [T*k, W] times the experts' weights; with
+    pre [T*k, 2 * in_cols] (the rows were its gated halves) drows is pre's gradient."""
+    p, x, where = problem, experts, "moe_expert_backward_rows"
+    slots, wide = p.num_tokens * p.topk, x.in_cols * (1 if pre is None else 2)
+    _check(load_library().moe_expert_backward_rows(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take_weights(where, p, x),
+        _take(where, dout, "bfloat16", slots, x.weight_rows), _take(where, pre, "bfloat16", slots, wide),
+        _take(where, drows, "bfloat16", slots, wide), _stream(stream)), where)
+
+
+def moe_expert_backward_weights(problem: Problem, layout: Layout, experts: Experts, rows, dout, dweights, stream=None):
+    """dweights [E, W, in_cols] = per expert, the sum of dout[r]^T rows[r] over its rows."""
+    p, x, where = problem, experts, "moe_expert_backward_weights"
+    slots = p.num_tokens * p.topk
+    _check(load_library().moe_expert_backward_weights(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), ctypes.byref(x.c()),
+        _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, dout, "bfloat16", slots, x.weight_rows),
+        _take(where, dweights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols), _stream(stream)), where)
+
+
+def moe_quant4_row_scale_bytes(problem: Problem, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_quant4_row_scale_bytes(ctypes.byref(problem.c()), int(cols), ctypes.byref(n)),
+           "moe_quant4_row_scale_bytes")
+    return n.value
+
+
+def moe_quant4_weight_scale_bytes(problem: Problem, experts: Experts) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_quant4_weight_scale_bytes(ctypes.byref(problem.c()), ctypes.byref(experts.c()),
+                                                        ctypes.byref(n)), "moe_quant4_weight_scale_bytes")
+    return n.value
+
+
+def _take_bytes(where: str, t, size: int):
+    """Address of a dense uint8 tensor of at least `size` bytes."""
+    at = _take(where, t, "uint8")
+    if hasattr(t, "numel") and t.numel() < size:
+        raise MoeError(MOE_ERR_INVALID, f"{where}: {size} bytes of scale blocks are wanted, not {t.numel()}")
+    return at
+
+
+def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, stream=None):
+    """Receive rows bf16 [T*k, cols] to 4-bit codes [T*k, cols / 2] and scale blocks."""
+    p, where = problem, "moe_quant4_rows"
+    slots, cols = p.num_tokens * p.topk, 2 * int(codes.shape[1])
+    _check(load_library().moe_quant4_rows(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), cols, _take(where, rows, "bfloat16", slots, cols),
+        _take(where, codes, "uint8", slots, cols // 2),
+        _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, cols)), _stream(stream)), where)
+
+
+def moe_quant4_weights(problem: Problem, experts: Experts, codes, scales, stream=None):
+    """The experts' bf16 weights to 4-bit codes [E, W, in_cols / 2] and scale blocks."""
+    p, x, where = problem, experts, "moe_quant4_weights"
+    _check(load_library().moe_quant4_weights(
+        ctypes.byref(p.c()), _take_weights(where, p, x),
+        _take(where, codes, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2),
+        _take_bytes(where, scales, moe_quant4_weight_scale_bytes(p, x)), _stream(stream)), where)
+
+
+def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, codes, scales, out, pre=None, stream=None):
+    """moe_expert_forward from 4-bit rows (moe_quant4_rows) and 4-bit weights (experts.weights,
+    experts.scales of moe_quant4_weights); out and pre are bf16."""
+    p, x, where = problem, experts, "moe_expert_forward4"
+    slots = p.num_tokens * p.topk
+    _take(where, x.weights, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2)
+    if x.scales is not None:
+        _take_bytes(where, x.scales, moe_quant4_weight_scale_bytes(p, x))
+    _check(load_library().moe_expert_forward4(
+        ctypes.byref(p.c()), ctypes.byref(layout.c()), ctypes.byref(x.c()),
+        _take(where, codes, "uint8", slots, x.in_cols // 2),
+        _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, x.in_cols)),
+        _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),
+        _stream(stream)), where)
 
 
 def moe_status(workspace, stream=None):

@@ -3,6 +3,7 @@
 // inside an NVTX range of its own name.  The library allocates no memory and
 // keeps no state between calls (moe_noalloc.cu's fixed scratch array aside).
 
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -136,6 +137,68 @@ int code_of_status(uint32_t bits) {
     if (bits & (MOE_STATUS_PLACEMENT | MOE_STATUS_SRC_OFFSET)) return MOE_ERR_INVALID;
     if (bits & MOE_STATUS_RELAY_CAPACITY) return MOE_ERR_CAPACITY;
     return MOE_OK;
+}
+
+// The experts of a call; wide is the granularity of in_cols.
+int check_experts(const moe_experts* x, const Dims& d, int wide, moe::ExpertArgs* a) {
+    if (x == nullptr || x->reserved != 0) return MOE_ERR_INVALID;
+    if (x->act != MOE_ACT_NONE && x->act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID;
+    if (x->in_cols < 8 || x->in_cols > MOE_MAX_HIDDEN || x->in_cols % wide != 0) return MOE_ERR_INVALID;
+    if (x->out_cols < 8 || x->out_cols > MOE_MAX_HIDDEN || x->out_cols % 8 != 0) return MOE_ERR_INVALID;
+    *a = moe::ExpertArgs{};
+    a->R = d.T * d.k;
+    a->E = d.E;
+    a->K = x->in_cols;
+    a->N = x->out_cols;
+    a->glu = x->act == MOE_ACT_SWIGLU;
+    a->W = a->glu ? 2 * a->N : a->N;
+    if ((long long)a->E * a->W >= (1LL << 31)) return MOE_ERR_INVALID;
+    a->weights = x->weights;
+    a->weight_scales = x->scales;
+    return MOE_OK;
+}
+
+// The layout arrays the experts' products read.
+int check_expert_layout(const moe_layout_t* l, moe::ExpertArgs* a) {
+    if (l == nullptr || l->expert_count == nullptr || l->expert_offset == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(l->expert_count, 4) || !aligned(l->expert_offset, 4)) return MOE_ERR_ALIGN;
+    a->count = l->expert_count;
+    a->offset = l->expert_offset;
+    return MOE_OK;
+}
+
+int check_routing(const moe_problem* problem, const moe_routing* r, Dims* d, moe::RouteArgs* a) {
+    const int rc = check_problem(problem, d);
+    if (rc != MOE_OK) return rc;
+    if (r == nullptr) return MOE_ERR_INVALID;
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
+    if (r->logits_dtype != MOE_LOGITS_F32 && r->logits_dtype != MOE_LOGITS_BF16) return MOE_ERR_INVALID;
+    if (!std::isfinite(r->scale) || d->k > d->E) return MOE_ERR_INVALID;
+    for (int v : r->reserved)
+        if (v != 0) return MOE_ERR_INVALID;
+    *a = moe::RouteArgs{};
+    a->T = d->T;
+    a->k = d->k;
+    a->E = d->E;
+    a->score = r->score;
+    a->renorm = r->renormalise != 0;
+    a->bf16 = r->logits_dtype == MOE_LOGITS_BF16;
+    a->scale = r->scale;
+    return MOE_OK;
+}
+
+// Bytes of the scale blocks of `blocks` blocks of 128 rows, cols columns wide.
+size_t scale_block_bytes(size_t blocks, int cols) { return blocks * (((size_t)cols + 127) / 128) * 512; }
+
+// A launcher's result as a status code; nothing it throws (a lookup table that
+// cannot grow) leaves a C entry point.
+template <typename F>
+int guarded(F launch) noexcept {
+    try {
+        return cuda_status(launch());
+    } catch (...) {
+        return MOE_ERR_CUDA;
+    }
 }
 
 int64_t row_bytes(const Dims& d) {
@@ -437,6 +500,201 @@ int moe_combine_group(const moe_problem* problem, const moe_layout_t* layout, co
     const moe::GroupArgs ga{ids, expert_group, group, num_groups, d.E};
     return cuda_status(moe::launch_combine_group(m, ga, y, weights, acc, out,
                                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_route(const moe_problem* problem, const moe_routing* routing, const void* logits, const float* bias,
+              int32_t* ids, float* gates, moe_stream_t stream) {
+    MOE_NVTX("moe_route");
+    Dims d;
+    moe::RouteArgs a;
+    const int rc = check_routing(problem, routing, &d, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (logits == nullptr || ids == nullptr || gates == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(logits, a.bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
+        return MOE_ERR_ALIGN;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.gates = gates;
+    return guarded([&] { return moe::launch_route(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_route_backward(const moe_problem* problem, const moe_routing* routing, const void* logits,
+                       const int32_t* ids, const float* dgates, void* dlogits, moe_stream_t stream) {
+    MOE_NVTX("moe_route_backward");
+    Dims d;
+    moe::RouteArgs a;
+    const int rc = check_routing(problem, routing, &d, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (logits == nullptr || ids == nullptr || dgates == nullptr || dlogits == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(logits, a.bf16 ? 2 : 4) || !aligned(dlogits, a.bf16 ? 2 : 4) || !aligned(ids, 4) ||
+        !aligned(dgates, 4))
+        return MOE_ERR_ALIGN;
+    a.logits = logits;
+    a.ids = const_cast<int32_t*>(ids);
+    a.dgates = dgates;
+    a.dlogits = dlogits;
+    return guarded([&] { return moe::launch_route_backward(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_combine_backward(const moe_problem* problem, const moe_layout_t* layout, const void* dout, const void* y,
+                         const float* weights, void* dy, float* dweights, moe_stream_t stream) {
+    MOE_NVTX("moe_combine_backward");
+    Dims d;
+    const int rc = check_problem(problem, &d);
+    if (rc != MOE_OK) return rc;
+    if (layout == nullptr) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (layout->pos == nullptr || dout == nullptr || y == nullptr || weights == nullptr || dy == nullptr ||
+        dweights == nullptr)
+        return MOE_ERR_INVALID;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(weights, 4) ||
+        !aligned(dweights, 4) || !aligned(layout->pos, 4))
+        return MOE_ERR_ALIGN;
+    return guarded([&] {
+        return moe::launch_combine_backward(layout->pos, d.T, d.k, d.h, dout, y, weights, dy, dweights,
+                                            reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int moe_expert_forward(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                       const void* rows, void* pre, void* out, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_forward");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 8, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (pre != nullptr && !a.glu) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || rows == nullptr || out == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(rows, 16) || !aligned(pre, 16) || !aligned(out, 16))
+        return MOE_ERR_ALIGN;
+    a.rows = rows;
+    a.pre = pre;
+    a.out = out;
+    return guarded([&] { return moe::launch_expert_forward(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_expert_backward_rows(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                             const void* dout, const void* pre, void* drows, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_backward_rows");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 8, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || dout == nullptr || drows == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(dout, 16) || !aligned(pre, 16) || !aligned(drows, 16))
+        return MOE_ERR_ALIGN;
+    a.dout = dout;
+    a.pre_in = pre;
+    a.out = drows;
+    return guarded([&] { return moe::launch_expert_backward_rows(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_expert_backward_weights(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                                const void* rows, const void* dout, void* dweights, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_backward_weights");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 8, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (dweights == nullptr || (d.T > 0 && (rows == nullptr || dout == nullptr))) return MOE_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(dout, 16) || !aligned(dweights, 16)) return MOE_ERR_ALIGN;
+    a.rows = rows;
+    a.dout = dout;
+    a.out = dweights;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (d.T == 0) return cuda_status(cudaMemsetAsync(dweights, 0, 2 * (size_t)a.E * a.W * a.K, s));
+    return guarded([&] { return moe::launch_expert_backward_weights(a, s); });
+}
+
+int moe_quant4_row_scale_bytes(const moe_problem* problem, int32_t cols, size_t* bytes) {
+    MOE_NVTX("moe_quant4_row_scale_bytes");
+    Dims d;
+    const int rc = check_problem(problem, &d);
+    if (rc != MOE_OK) return rc;
+    if (bytes == nullptr || cols < 32 || cols > MOE_MAX_HIDDEN || cols % 32 != 0) return MOE_ERR_INVALID;
+    *bytes = scale_block_bytes((size_t)d.T * d.k / 128 + d.E, cols);
+    return MOE_OK;
+}
+
+int moe_quant4_weight_scale_bytes(const moe_problem* problem, const moe_experts* experts, size_t* bytes) {
+    MOE_NVTX("moe_quant4_weight_scale_bytes");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 32, &a);
+    if (rc != MOE_OK) return rc;
+    if (bytes == nullptr) return MOE_ERR_INVALID;
+    const int per = a.glu ? 64 : 128;
+    *bytes = scale_block_bytes((size_t)a.E * ((a.N + per - 1) / per), a.K);
+    return MOE_OK;
+}
+
+int moe_quant4_rows(const moe_problem* problem, const moe_layout_t* layout, int32_t cols, const void* rows,
+                    void* codes, void* scales, moe_stream_t stream) {
+    MOE_NVTX("moe_quant4_rows");
+    Dims d;
+    moe::ExpertArgs a{};
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK && (cols < 32 || cols > MOE_MAX_HIDDEN || cols % 32 != 0)) rc = MOE_ERR_INVALID;
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (rows == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_ALIGN;
+    a.R = d.T * d.k;
+    a.E = d.E;
+    a.K = cols;
+    a.rows = rows;
+    return guarded([&] { return moe::launch_quant4_rows(a, codes, scales, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_quant4_weights(const moe_problem* problem, const moe_experts* experts, void* codes, void* scales,
+                       moe_stream_t stream) {
+    MOE_NVTX("moe_quant4_weights");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 32, &a);
+    if (rc != MOE_OK) return rc;
+    if (a.weights == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_ALIGN;
+    return guarded([&] {
+        return moe::launch_quant4_weights(a, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int moe_expert_forward4(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                        const void* codes, const void* scales, void* pre, void* out, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_forward4");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 32, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (pre != nullptr && !a.glu) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || a.weight_scales == nullptr || codes == nullptr || scales == nullptr || out == nullptr)
+        return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(a.weight_scales, 16) || !aligned(codes, 16) || !aligned(scales, 16) ||
+        !aligned(pre, 16) || !aligned(out, 16))
+        return MOE_ERR_ALIGN;
+    a.rows = codes;
+    a.row_scales = scales;
+    a.pre = pre;
+    a.out = out;
+    return guarded([&] { return moe::launch_expert_forward4(a, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 int moe_status(const void* workspace, uint32_t* status_bits, moe_stream_t stream) {

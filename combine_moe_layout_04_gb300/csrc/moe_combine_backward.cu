@@ -1,0 +1,95 @@
+// moe_combine_backward.cu -- the gradient of the gate-weighted sum: expert
+// output rows and gates in one pass ("Balancing and Beyond", section 1).
+//
+//   dy[pos[t, j]] = bf16(w[t, j] dout[t]),  dw[t, j] = <dout[t], y[pos[t, j]]>
+//
+// HBM-bound: per token it reads one row and k rows and writes k rows, 4 flops
+// an element.  A block owns a token, so that dout is read once and the dot
+// products end in the block, in an order that only the sizes fix: every
+// thread takes the columns tid, tid + 256, ... of 8, then lanes, then warps.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSlots = 8;  // slots taken at a time (their loads are issued together)
+
+__device__ __forceinline__ float2 wide2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+__global__ void __launch_bounds__(kThreads)
+combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R, const uint4* __restrict__ dout,
+                        const uint4* __restrict__ y, const float* __restrict__ weights, uint4* __restrict__ dy,
+                        float* __restrict__ dweights) {
+    __shared__ float part[kWarps][kSlots];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+        int64_t row[kSlots];
+        float w[kSlots], acc[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+            const bool live = j0 + j < k;
+            const int r = live ? pos[t * k + j0 + j] : -1;
+            row[j] = r >= 0 && r < R ? (int64_t)r * nvec : -1;
+            w[j] = live ? weights[t * k + j0 + j] : 0.0f;
+            acc[j] = 0.0f;
+        }
+        for (int c = tid; c < nvec; c += kThreads) {
+            const uint4 d = dout[t * nvec + c];
+            uint4 v[kSlots];
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j)
+                if (row[j] >= 0) v[j] = ld_stream_v4(y + row[j] + c);
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j) {
+                if (row[j] < 0) continue;
+                const uint32_t yw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 g = wide2(dw[i]), x = wide2(yw[i]);
+                    acc[j] = fmaf(g.x, x.x, acc[j]);
+                    acc[j] = fmaf(g.y, x.y, acc[j]);
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(w[j] * g.x, w[j] * g.y);
+                    o[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                st_v4(dy + row[j] + c, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], s);
+            if (lane == 0) part[warp][j] = acc[j];
+        }
+        __syncthreads();
+        if (tid < kSlots && j0 + tid < k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) sum += part[i][tid];
+            dweights[t * k + j0 + tid] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_combine_backward(const int32_t* pos, int T, int k, int h, const void* dout, const void* y,
+                                    const float* weights, void* dy, float* dweights, cudaStream_t s) {
+    combine_backward_kernel<<<T, kThreads, 0, s>>>(pos, k, h / 8, T * k, static_cast<const uint4*>(dout),
+                                                   static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
+                                                   dweights);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

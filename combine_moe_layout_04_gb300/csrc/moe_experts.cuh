@@ -1,0 +1,65 @@
+// moe_experts.cuh -- what the experts' products and their 4-bit quantiser
+// share: the walk over ragged groups of receive rows.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// Rows of one expert, kept inside [0, R) whatever the layout holds.
+struct ExpertRows {
+    int first, count;
+};
+__device__ __forceinline__ ExpertRows expert_rows(const int32_t* count, const int32_t* offset, int e, int R) {
+    const int first = min(max(offset[e], 0), R);
+    return {first, min(max(count[e], 0), R - first)};
+}
+
+// base[e] = sum over e' < e of ceil(rows(e') / 128), base[E] the total: the
+// row blocks of the experts one after another.  All threads of the block call
+// it (a multiple of 32, at most 1024 threads); scratch holds 32 ints.
+__device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int32_t* offset, int E, int R, int* base,
+                                                int* scratch) {
+    const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (E + n - 1) / n;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e < E) sum += (expert_rows(count, offset, e, R).count + 127) >> 7;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int at = inc - sum;
+    for (int i = 0; i < warp; ++i) at += scratch[i];
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e < E) {
+            base[e] = at;
+            at += (expert_rows(count, offset, e, R).count + 127) >> 7;
+            if (e == E - 1) base[E] = at;
+        }
+    }
+    __syncthreads();
+}
+
+// The expert that owns row block b < base[E]: the last e with base[e] <= b.
+__device__ __forceinline__ int expert_of_block(const int* base, int E, int b) {
+    int lo = 0, hi = E;  // base[lo] <= b < base[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Byte of the scale of row i (of a block of 128) and group j (of 4).
+__host__ __device__ __forceinline__ int scale_byte(int i, int j) { return (i & 31) * 16 + (i >> 5) * 4 + j; }
+
+}  // namespace moe

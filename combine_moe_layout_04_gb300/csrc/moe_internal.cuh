@@ -162,6 +162,39 @@ struct RelayLayoutArgs {
     int T, k, H, P, cap;
 };
 
+// The experts' products of one call.
+struct ExpertArgs {
+    const int32_t* count;    // [E] rows of every expert
+    const int32_t* offset;   // [E+1] its first row
+    int R;                   // T * k receive rows
+    int E;
+    int K;                   // in_cols
+    int N;                   // out_cols
+    int W;                   // rows of an expert's weights: N, or 2 N with a gated activation
+    bool glu;
+    const void* rows;        // bf16 rows, or 4-bit codes
+    const void* row_scales;  // scale blocks of 4-bit rows
+    const void* weights;
+    const void* weight_scales;
+    const void* pre_in;      // backward through the activation: (g, u)
+    const void* dout;
+    void* pre;
+    void* out;
+};
+
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    const float* dgates;
+    int32_t* ids;
+    float* gates;
+    void* dlogits;
+    int T, k, E;
+    int score;
+    bool renorm, bf16;
+    float scale;
+};
+
 // ---- inline PTX helpers --------------------------------------------------
 
 __device__ __forceinline__ unsigned lanemask_lt() {
@@ -448,6 +481,16 @@ cudaError_t launch_expert_groups(const int32_t* e2r, int E, int R, int G, int32_
 cudaError_t read_move_faults(uint32_t* bits, cudaStream_t s);
 cudaError_t launch_swap_plan(const int32_t* count, const int32_t* e2r, int E, int R, int P, int tau,
                              int32_t* new_e2r, int32_t* swaps, cudaStream_t s);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_quant4_weights(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_combine_backward(const int32_t* pos, int T, int k, int h, const void* dout, const void* y,
+                                    const float* weights, void* dy, float* dweights, cudaStream_t s);
 cudaError_t run_wait_selftest(uint32_t* bits, cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,224 @@
+// moe_route.cu -- the router: top-k choice of the experts from their logits,
+// the gates, and the gradient of the gates ("Balancing and Beyond", section
+// 3.2: k distinct experts a token).
+//
+// One warp holds a token's E logits in registers (value i of lane l is expert
+// 32 i + l, so that a request covers consecutive logits) and finds the k
+// largest by k rounds of a warp maximum: over keys first, then over the lowest
+// index among the lanes that hold the maximum, which settles ties.  A key is
+// the logit as an unsigned integer in the same order, so a round is two
+// integer warp reductions; only the winning lane looks through its registers
+// again.  Lane j keeps choice j, so the gates are one value a lane.
+//
+// Softmax sums, sigmoids and gradients are fp32 throughout; bf16 logits widen
+// exactly, and a bf16 gradient is rounded once, when it is stored.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRouteThreads = 128;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr unsigned kTaken = 0, kNan = 1;  // below the key of every number, -infinity included
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void narrow(float* p, float v) { *p = v; }
+__device__ __forceinline__ void narrow(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// An unsigned integer that orders as the float does (-0 and +0 alike).
+__device__ __forceinline__ unsigned key_of(float v) {
+    if (isnan(v)) return kNan;
+    const unsigned u = __float_as_uint(v + 0.0f);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+
+// exp(v - top), with no weight for -infinity (the difference is NaN when top
+// is -infinity too).
+__device__ __forceinline__ float soft(float v, float top) { return v == -INFINITY ? 0.0f : expf(v - top); }
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// The logits of a token, V a lane; -infinity past E.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&l)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        l[i] = e < E ? widen(row[e]) : -INFINITY;
+    }
+}
+
+// A gate's weight before scale, lane j's for choice j, from its logit v; all:
+// every logit of the row.  Returns w, and in *s the sigmoid.
+template <int V>
+__device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all)[V], float v, bool on, float* s) {
+    if (a.score == MOE_SCORE_SOFTMAX) {
+        float top = on ? v : -INFINITY, sum;
+        if (a.renorm) {
+            top = warp_max(top);
+            sum = warp_sum(on ? soft(v, top) : 0.0f);
+        } else {
+            float mine = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) top = fmaxf(top, all[i]);
+            top = warp_max(top);
+#pragma unroll
+            for (int i = 0; i < V; ++i) mine += soft(all[i], top);
+            sum = warp_sum(mine);
+        }
+        return on && sum != 0.0f ? soft(v, top) / sum : 0.0f;
+    }
+    *s = on ? sigmoid(v) : 0.0f;
+    if (!a.renorm) return *s;
+    const float sum = warp_sum(*s);
+    return sum != 0.0f ? *s / sum : 0.0f;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    float l[V];
+    load_row<T, V>(static_cast<const T*>(a.logits) + (int64_t)t * a.E, a.E, lane, l);
+    unsigned key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        key[i] = e < a.E ? key_of(a.bias != nullptr ? l[i] + a.bias[e] : l[i]) : kTaken;
+    }
+    float mine = -INFINITY;  // logit of choice `lane`
+    int chosen = 0;
+    for (int j = 0; j < a.k; ++j) {
+        unsigned best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const unsigned top = __reduce_max_sync(kFull, best);
+        const unsigned id = __reduce_min_sync(kFull, best == top ? 32u * at + lane : 0xffffffffu);
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (id == 32u * i + lane) {
+                key[i] = kTaken;
+                v = l[i];
+            }
+        v = __shfl_sync(kFull, v, id & 31);
+        if (lane == j) {
+            mine = v;
+            chosen = (int)id;
+        }
+    }
+    const bool on = lane < a.k;
+    float s;
+    const float w = weight_of<V>(a, l, mine, on, &s);
+    if (on) {
+        a.ids[(int64_t)t * a.k + lane] = chosen;
+        a.gates[(int64_t)t * a.k + lane] = a.scale * w;
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.E;
+    const bool spread = a.score == MOE_SCORE_SOFTMAX && !a.renorm;  // every logit gets a gradient
+    float l[V];
+    if (spread) load_row<T, V>(row, a.E, lane, l);
+    int id = lane < a.k ? a.ids[(int64_t)t * a.k + lane] : -1;
+    const bool on = id >= 0 && id < a.E;
+    if (!on) id = -1;
+    const float v = on ? widen(row[id]) : -INFINITY;
+    const float g = on ? a.scale * a.dgates[(int64_t)t * a.k + lane] : 0.0f;
+    float s = 0.0f, grad;
+    const float w = weight_of<V>(a, l, v, on, &s);
+    const float mean = warp_sum(w * g);
+    if (spread) grad = w * g;
+    else if (a.score == MOE_SCORE_SOFTMAX) grad = w * (g - mean);
+    else if (a.renorm) grad = w * (1.0f - s) * (g - mean);
+    else grad = g * s * (1.0f - s);
+    float d[V];
+    if (spread) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+        top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += d[i] = soft(l[i], top);
+        sum = warp_sum(sum);
+        const float share = sum != 0.0f ? mean / sum : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= -share;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    }
+    for (int j = 0; j < a.k; ++j) {
+        const int e = __shfl_sync(kFull, id, j);
+        const float x = __shfl_sync(kFull, grad, j);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == 32 * i + lane) d[i] += x;
+    }
+    T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        if (e < a.E) narrow(out + e, d[i]);
+    }
+}
+
+template <typename T, int V>
+void launch(const RouteArgs& a, bool back, cudaStream_t s) {
+    constexpr int per = kRouteThreads / 32;
+    const dim3 grid((unsigned)((a.T + (int64_t)per - 1) / per));
+    if (back) route_backward_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
+    else route_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
+}
+
+// The registers a lane needs grow with E (at most 1024): powers of two keep
+// the unused ones below the used ones.
+template <typename T>
+cudaError_t pick(const RouteArgs& a, bool back, cudaStream_t s) {
+    if (a.E <= 32) launch<T, 1>(a, back, s);
+    else if (a.E <= 64) launch<T, 2>(a, back, s);
+    else if (a.E <= 128) launch<T, 4>(a, back, s);
+    else if (a.E <= 256) launch<T, 8>(a, back, s);
+    else if (a.E <= 512) launch<T, 16>(a, back, s);
+    else launch<T, 32>(a, back, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+    return a.bf16 ? pick<__nv_bfloat16>(a, false, s) : pick<float>(a, false, s);
+}
+
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s) {
+    return a.bf16 ? pick<__nv_bfloat16>(a, true, s) : pick<float>(a, true, s);
+}
+
+}  // namespace moe

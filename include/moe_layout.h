@@ -14,8 +14,11 @@
  *   host(r) = r / P,  local index li(r) = r % P,  H = R / P
  *   src(t)  = source rank of token t (tokens split over ranks 0..R_src-1)
  *
- * Call order per MoE layer: moe_layout -> (moe_stats) -> moe_dispatch ->
- * [experts] -> moe_combine.  All calls are asynchronous on the given stream;
+ * Call order per MoE layer: (moe_route ->) moe_layout -> (moe_stats) ->
+ * moe_dispatch -> experts (moe_expert_forward, or moe_quant4_rows and
+ * moe_expert_forward4) -> moe_combine; the way back is moe_combine_backward ->
+ * moe_expert_backward_weights and moe_expert_backward_rows -> moe_combine with
+ * unit weights (the gradient of a dispatch) and moe_route_backward.  All calls are asynchronous on the given stream;
  * only moe_stats, moe_status, moe_move_faults and moe_selftest_bounded_waits
  * synchronise it.  Every entry
  * point opens an NVTX range of its own name (header-only NVTX 3: free when no
@@ -437,6 +440,174 @@ int moe_combine_group(const moe_problem* problem, const moe_layout_t* layout, co
                       const int32_t* expert_group, int32_t group, int32_t num_groups, const void* y,
                       const float* weights, float* acc, void* out, moe_stream_t stream);
 
+/* ---- The router ------------------------------------------------------------
+ * "Balancing and Beyond", section 3.2: a token goes to k distinct experts,
+ * which the router chooses from one logit per expert, with a gate weight each.
+ *
+ *   score: what a gate is made of.
+ *     MOE_SCORE_SOFTMAX: softmax over the k chosen logits when renormalise is
+ *       not 0, else over all E logits;
+ *     MOE_SCORE_SIGMOID: 1 / (1 + exp(-logit)), divided by the sum of the
+ *       chosen ones when renormalise is not 0.
+ *   scale: every gate is multiplied by it (finite; 1 for none).
+ *   logits_dtype: MOE_LOGITS_F32 or MOE_LOGITS_BF16, of logits and dlogits. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_LOGITS_F32    0
+#define MOE_LOGITS_BF16   1
+typedef struct moe_routing {
+    int32_t score;
+    int32_t renormalise;
+    float scale;
+    int32_t logits_dtype;
+    int32_t reserved[4];          /* must be 0 */
+} moe_routing;
+
+/* Choice of the experts ("Balancing and Beyond", section 3.2: k distinct
+ * experts a token).  ids[t] = the k experts with the largest key, in falling
+ * order, equal keys by the lower index; key = logit, or logit + bias (one fp32
+ * addition) with a bias: the bias moves the choice only, never a gate.  A NaN
+ * key comes after every number, so the ids are always in range and distinct.
+ * gates as moe_routing says, in fp32 from the logits without bias.  A chosen
+ * logit of -infinity has weight 0, and a token whose chosen logits are all
+ * -infinity has gates 0; a NaN or +infinity that a gate is made of gives NaN.
+ *   logits: [T, E] fp32 or bf16; bias: fp32 [E] or NULL;
+ *   ids: int32 [T, k]; gates: fp32 [T, k]; k <= E. */
+int moe_route(const moe_problem* problem, const moe_routing* routing, const void* logits, const float* bias,
+              int32_t* ids, float* gates, moe_stream_t stream);
+
+/* Gradient of the gates with respect to the logits (the pages have
+ * no counterpart: they name training only by its traffic).  With a = scale *
+ * dgates and w the gates without scale, for the chosen i (0 elsewhere):
+ *   softmax over the chosen:  w_i (a_i - sum_j w_j a_j);
+ *   softmax over all E:       w_i ([i chosen] a_i - sum_j w_j a_j), every i;
+ *   sigmoid s:                a_i s_i (1 - s_i);
+ *   sigmoid, renormalised:    w_i (1 - s_i) (a_i - sum_j w_j a_j).
+ *   logits, ids: as moe_route took and gave them (an id out of [0, E)
+ *   contributes nothing); dgates: fp32 [T, k]; dlogits: [T, E] of the logits'
+ *   type, every value written. */
+int moe_route_backward(const moe_problem* problem, const moe_routing* routing, const void* logits,
+                       const int32_t* ids, const float* dgates, void* dlogits, moe_stream_t stream);
+
+/* ---- The experts' products ---------------------------------------------------
+ * The expert computation between dispatch and combine ("Balancing and Beyond",
+ * section 1 and Figure 1): one weight matrix per expert, and each expert's
+ * receive rows against its own.  Expert e owns the rows expert_offset[e] ..
+ * expert_offset[e] + expert_count[e] - 1 of the layout; the host never learns
+ * the counts.  Only those two arrays are read from the layout.
+ *
+ *   in_cols: columns of a receive row; out_cols: columns of a result row;
+ *   act: MOE_ACT_NONE, or MOE_ACT_SWIGLU: the weights hold a gate half and an
+ *     up half, and a result is silu(gate) * up, silu(g) = g / (1 + exp(-g));
+ *   weights: bf16 [E, W, in_cols] (codes [E, W, in_cols / 2] for the 4-bit
+ *     calls), W = out_cols or, with MOE_ACT_SWIGLU, 2 * out_cols: first the
+ *     gate rows, then the up rows;
+ *   scales: the 4-bit weights' scale blocks, else NULL.
+ * in_cols and out_cols: multiples of 8 in [8, 2^20]; in_cols a multiple of 32
+ * for the 4-bit calls.  E * W < 2^31.  Every array 16-byte aligned.
+ * Products are summed in fp32 and rounded once to bf16. */
+#define MOE_ACT_NONE   0
+#define MOE_ACT_SWIGLU 1
+typedef struct moe_experts {
+    int32_t in_cols;
+    int32_t out_cols;
+    int32_t act;
+    int32_t reserved;             /* must be 0 */
+    const void* weights;
+    const void* scales;
+} moe_experts;
+
+/* The experts' forward products ("Balancing and Beyond", section 1): for every
+ * receive row r of expert e, p = rows[r] W[e]^T and out[r] = p, or silu(g) * u
+ * of p = (g, u).
+ *   rows: bf16 [T*k, in_cols]; out: bf16 [T*k, out_cols];
+ *   pre: bf16 [T*k, W] that receives p (what the backward of the activation
+ *   reads) with MOE_ACT_SWIGLU, or NULL; must be NULL with MOE_ACT_NONE. */
+int moe_expert_forward(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                       const void* rows, void* pre, void* out, moe_stream_t stream);
+
+/* Gradient of the experts' products with respect to their rows (the pages
+ * have no counterpart).  dh = dout[r] W[e];
+ *   pre == NULL: drows[r] = dh, bf16 [T*k, in_cols];
+ *   pre = (g, u), bf16 [T*k, 2 * in_cols]: the rows were silu(g) * u, and
+ *     drows[r] = (dh u s (1 + g (1 - s)), dh g s), s = 1 / (1 + exp(-g)),
+ *     bf16 [T*k, 2 * in_cols]: the gradient of pre, without dh in between.
+ *   dout: bf16 [T*k, W]: the gradient of the products p (of pre, with
+ *   MOE_ACT_SWIGLU). */
+int moe_expert_backward_rows(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                             const void* dout, const void* pre, void* drows, moe_stream_t stream);
+
+/* Gradient of the experts' products with respect to their weights; the pages
+ * have no counterpart.  dweights[e] = sum over the expert's rows r of
+ * dout[r]^T rows[r], bf16 [E, W, in_cols]; zeros for an expert without rows.
+ * experts->weights is not read (it may be NULL).
+ *   rows: bf16 [T*k, in_cols]; dout: bf16 [T*k, W]. */
+int moe_expert_backward_weights(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                                const void* rows, const void* dout, void* dweights, moe_stream_t stream);
+
+/* Gradient of moe_combine ("Balancing and Beyond", section 1, defines the
+ * sum; the pages have no counterpart of its gradient):
+ *   dy[pos[t, j]] = bf16_rne(weights[t, j] * dout[t]),
+ *   dweights[t, j] = sum over the columns of dout[t] * y[pos[t, j]], fp32, in
+ *   an order that depends on the sizes only.
+ *   dout: bf16 [T, h]; y, dy: bf16 [T*k, h]; weights, dweights: fp32 [T, k].
+ * Row buffers 16-byte aligned.  Only pos is read from the layout; a position
+ * out of [0, T*k) is skipped (its dweights is 0). */
+int moe_combine_backward(const moe_problem* problem, const moe_layout_t* layout, const void* dout, const void* y,
+                         const float* weights, void* dy, float* dweights, moe_stream_t stream);
+
+/* ---- The experts' products in 4 bits ------------------------------------------
+ * Microscaled 4-bit floating point (OCP MX, MXFP4): along a row, every 32
+ * columns share one scale X = 2^(b - 127), held as the byte b (E8M0), and each
+ * column holds a code of E2M1 (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6).
+ *   b = max(0, biased exponent of the largest |x| of the 32, minus 2);
+ *   code = x / X (exact: a power of two) rounded to nearest, ties to even,
+ *   saturated at +-6;
+ *   an infinity or NaN among the 32: b = 255 (the scale is NaN), codes 0.
+ * Codes: two columns a byte, the even one in the low half.
+ * Scale blocks: 512 bytes hold the scales of 128 rows x 4 groups of 32
+ * columns, row i of the block and group j at byte (i % 32) * 16 + (i / 32) * 4
+ * + j; blocks run over the groups of a row first (ceil(cols / 128) of them),
+ * then over blocks of rows.  Groups past the last column hold 0.
+ *   weights: ceil(out_cols / 128) row blocks per expert; with MOE_ACT_SWIGLU
+ *     ceil(out_cols / 64), each of 64 gate rows and then their 64 up rows.
+ *   receive rows: every expert starts a row block of its own, in expert order:
+ *     row i of expert e is row i % 128 of block (i / 128) + sum over e' < e of
+ *     ceil(expert_count[e'] / 128).
+ * Rows of a block that no expert row fills are not written. */
+
+/* Bytes of scale blocks for the receive rows of a problem, cols columns wide:
+ * (T*k / 128 + E) * ceil(cols / 128) * 512 holds every layout (the pages
+ * have no counterpart).  cols: a multiple of 32 in [32, 2^20]. */
+int moe_quant4_row_scale_bytes(const moe_problem* problem, int32_t cols, size_t* bytes);
+
+/* Bytes of scale blocks for the experts' 4-bit weights (the pages have
+ * no counterpart). */
+int moe_quant4_weight_scale_bytes(const moe_problem* problem, const moe_experts* experts, size_t* bytes);
+
+/* Receive rows to microscaled 4-bit codes (the step below the FP8 conversion
+ * of "Balancing and Beyond", section 3.1).
+ *   rows: bf16 [T*k, cols]; codes: [T*k, cols / 2] bytes; scales: scale blocks
+ *   of moe_quant4_row_scale_bytes().  All 16-byte aligned.  Reads
+ *   expert_count and expert_offset of the layout. */
+int moe_quant4_rows(const moe_problem* problem, const moe_layout_t* layout, int32_t cols, const void* rows,
+                    void* codes, void* scales, moe_stream_t stream);
+
+/* The experts' bf16 weights to microscaled 4-bit codes, once per model; the
+ * pages have no counterpart.  experts describes the bf16 weights; codes:
+ * [E, W, in_cols / 2] bytes; scales: scale blocks of
+ * moe_quant4_weight_scale_bytes(). */
+int moe_quant4_weights(const moe_problem* problem, const moe_experts* experts, void* codes, void* scales,
+                       moe_stream_t stream);
+
+/* The experts' forward products from 4-bit rows and 4-bit weights;
+ * the pages have no counterpart (their rows stop at FP8).  As moe_expert_forward, on
+ * the values that codes and scales stand for; out and pre are bf16.
+ *   codes, scales: as moe_quant4_rows wrote them with the same layout;
+ *   experts->weights, experts->scales: as moe_quant4_weights wrote them. */
+int moe_expert_forward4(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                        const void* codes, const void* scales, void* pre, void* out, moe_stream_t stream);
+
 /* The pages have no counterpart: the status word is this library's way to
  * report data-dependent faults without faulting the GPU.
  * Waits for the stream, then reads the device status bits of the workspace
@@ -496,10 +667,11 @@ int moe_swap_plan(const moe_problem* problem, const moe_layout_t* layout, int32_
                   int32_t* new_expert_to_rank, int32_t* swaps, moe_stream_t stream);
 
 /* The pages have no counterpart (bounded waits of this library's movers).
- * Device faults of the row movers since the last call: bit
- * MOE_FAULT_WAIT_TIMEOUT is set when a bulk-copy pipeline of moe_dispatch or
- * moe_combine waited more than one second for its own copies, gave up, drained
- * them and returned (its output is then incomplete).  Waits for the stream,
+ * Device faults of the row movers and of the experts' products since the last
+ * call: bit MOE_FAULT_WAIT_TIMEOUT is set when a copy pipeline of
+ * moe_dispatch, moe_combine or an experts' product waited more than one second
+ * for its own copies, gave up, drained them and returned (its output is then
+ * incomplete).  Waits for the stream,
  * copies the bits to *bits and clears them. */
 #define MOE_FAULT_WAIT_TIMEOUT 0x1u
 int moe_move_faults(uint32_t* bits, moe_stream_t stream);

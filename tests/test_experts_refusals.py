@@ -1,0 +1,195 @@
+"""Arguments that the router's and the experts' calls refuse on the host,
+before anything is enqueued (no GPU needed)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from combine_moe_layout_04_gb300 import _build
+    _build.build()
+    import combine_moe_layout_04_gb300 as m
+    m.load_library()
+    return m
+
+
+class At:
+    """A pointer-shaped stand-in: the checks decide from the address alone."""
+
+    def __init__(self, addr, shape=()):
+        self.addr, self.shape = addr, shape
+
+    def data_ptr(self):
+        return self.addr
+
+
+GOOD, ODD = At(0x20000), At(0x20008)
+
+
+def _p(moe, **kw):
+    base = dict(num_tokens=256, hidden=1024, topk=2, num_experts=16, num_ranks=4, ranks_per_host=2)
+    base.update(kw)
+    return moe.Problem(**base)
+
+
+def _lay(moe, **kw):
+    lay = moe.Layout.__new__(moe.Layout)
+    for n in moe._LAYOUT_FIELDS:
+        setattr(lay, n, kw.get(n, At(0x10000)))
+    return lay
+
+
+def _refused(moe, code, call, *args, **kw):
+    with pytest.raises(moe.MoeError) as ei:
+        call(*args, **kw, stream=0)
+    assert ei.value.code == code
+
+
+def test_structs_match_the_header(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    import combine_moe_layout_04_gb300 as m
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    mirrors = {"moe_routing": m._RoutingC, "moe_experts": m._ExpertsC}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "moe_layout.h"', "int main(void) {"]
+    for name, cls in mirrors.items():
+        lines.append(f'printf("%zu ", sizeof({name}));')
+        lines += [f'printf("%zu ", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    src = tmp_path / "s.c"
+    src.write_text("\n".join(lines + ["return 0;", "}"]))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "s")], check=True)
+    got = [int(v) for v in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True).stdout.split()]
+    want = []
+    for cls in mirrors.values():
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+def test_route_refusals(moe):
+    r = moe.Routing()
+    for bad in (moe.Routing(score=2), moe.Routing(score=-1), moe.Routing(scale=float("nan")),
+                moe.Routing(scale=float("inf"))):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route, _p(moe), bad, GOOD, GOOD, GOOD)
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route_backward, _p(moe), bad, GOOD, GOOD, GOOD, GOOD)
+    few = _p(moe, num_experts=4, topk=5)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route, few, r, GOOD, GOOD, GOOD)
+    for args in ((None, GOOD, GOOD), (GOOD, None, GOOD), (GOOD, GOOD, None)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route, _p(moe), r, *args)
+    for args in ((None, GOOD, GOOD, GOOD), (GOOD, None, GOOD, GOOD), (GOOD, GOOD, None, GOOD), (GOOD, GOOD, GOOD, None)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route_backward, _p(moe), r, *args)
+    off = At(0x20002)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_route, _p(moe), r, off, GOOD, GOOD)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_route, _p(moe), r, GOOD, off, GOOD)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_route, _p(moe), r, GOOD, GOOD, GOOD, bias=off)
+    rc = r.c(GOOD)
+    rc.reserved[2] = 1
+    lib = moe.load_library()
+    assert lib.moe_route(ctypes.byref(_p(moe).c()), ctypes.byref(rc), 0x20000, None, 0x20000, 0x20000,
+                         None) == moe.MOE_ERR_INVALID
+    assert lib.moe_route(ctypes.byref(_p(moe).c()), None, 0x20000, None, 0x20000, 0x20000, None) == moe.MOE_ERR_INVALID
+    assert lib.moe_route(None, ctypes.byref(r.c(GOOD)), 0x20000, None, 0x20000, 0x20000, None) == moe.MOE_ERR_INVALID
+
+
+def _calls(moe, p, lay, x):
+    """Every expert call with good arguments, as (call, positional arguments)."""
+    return [(moe.moe_expert_forward, [p, lay, x, GOOD, GOOD]),
+            (moe.moe_expert_backward_rows, [p, lay, x, GOOD, GOOD]),
+            (moe.moe_expert_backward_weights, [p, lay, x, GOOD, GOOD, GOOD]),
+            (moe.moe_expert_forward4, [p, lay, x, GOOD, GOOD, GOOD])]
+
+
+@pytest.mark.parametrize("bad", [dict(in_cols=0), dict(in_cols=12), dict(in_cols=-8), dict(out_cols=4), dict(out_cols=20),
+                                 dict(in_cols=(1 << 20) + 32), dict(out_cols=(1 << 20) + 8), dict(act=2), dict(act=-1)])
+def test_expert_shapes_refused(moe, bad):
+    x = moe.Experts(**{**dict(in_cols=64, out_cols=64, weights=GOOD, scales=GOOD), **bad})
+    for call, args in _calls(moe, _p(moe), _lay(moe), x):
+        _refused(moe, moe.MOE_ERR_INVALID, call, *args)
+    with pytest.raises(moe.MoeError):
+        moe.moe_quant4_weight_scale_bytes(_p(moe), x)
+
+
+def test_expert_pointers_refused(moe):
+    p, lay, x = _p(moe), _lay(moe), moe.Experts(64, 64, GOOD, scales=GOOD)
+    for call, args in _calls(moe, p, lay, x):
+        for i in range(3, len(args)):
+            _refused(moe, moe.MOE_ERR_INVALID, call, *args[:i], None, *args[i + 1:])
+            _refused(moe, moe.MOE_ERR_ALIGN, call, *args[:i], ODD, *args[i + 1:])
+        if call is not moe.moe_expert_backward_weights:
+            _refused(moe, moe.MOE_ERR_INVALID, call, p, lay, moe.Experts(64, 64, None, scales=GOOD), *args[3:])
+            _refused(moe, moe.MOE_ERR_ALIGN, call, p, lay, moe.Experts(64, 64, ODD, scales=GOOD), *args[3:])
+        _refused(moe, moe.MOE_ERR_INVALID, call, p, _lay(moe, expert_count=At(None)), x, *args[3:])
+        _refused(moe, moe.MOE_ERR_INVALID, call, p, _lay(moe, expert_offset=At(None)), x, *args[3:])
+        _refused(moe, moe.MOE_ERR_INVALID, call, _p(moe, topk=0), lay, x, *args[3:])
+    # pre is what a gated activation leaves behind; 4-bit weights need scales and columns in blocks of 32
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward, p, lay, x, GOOD, GOOD, pre=GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward4, p, lay, moe.Experts(64, 64, GOOD), GOOD, GOOD, GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward4, p, lay, moe.Experts(72, 64, GOOD, scales=GOOD), GOOD, GOOD, GOOD)
+    # more weight rows than an int holds
+    many = moe.Experts(64, 1 << 20, GOOD, moe.MOE_ACT_SWIGLU)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward, _p(moe, num_experts=1024), lay, many, GOOD, GOOD)
+
+
+def test_quant4_sizes_and_refusals(moe):
+    p = _p(moe)
+    assert moe.moe_quant4_row_scale_bytes(p, 32) == (512 // 128 + 16) * 512
+    assert moe.moe_quant4_row_scale_bytes(p, 160) == (512 // 128 + 16) * 2 * 512
+    assert moe.moe_quant4_weight_scale_bytes(p, moe.Experts(160, 136)) == 16 * 2 * 2 * 512
+    assert moe.moe_quant4_weight_scale_bytes(p, moe.Experts(160, 136, act=moe.MOE_ACT_SWIGLU)) == 16 * 3 * 2 * 512
+    for cols in (0, 16, -32, 100, (1 << 20) + 32):
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_quant4_row_scale_bytes(p, cols)
+        assert ei.value.code == moe.MOE_ERR_INVALID
+    lay, codes = _lay(moe), At(0x30000, (512, 32))
+    for args in ((None, codes, GOOD), (GOOD, At(None, (512, 32)), GOOD), (GOOD, codes, None)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_rows, p, lay, *args)
+    for args in ((ODD, codes, GOOD), (GOOD, At(0x30004, (512, 32)), GOOD), (GOOD, codes, ODD)):
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_quant4_rows, p, lay, *args)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_rows, p, lay, GOOD, At(0x30000, (512, 20)), GOOD)
+    x = moe.Experts(64, 64, GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_weights, p, moe.Experts(64, 64), GOOD, GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_weights, p, moe.Experts(72, 64, GOOD), GOOD, GOOD)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_quant4_weights, p, x, ODD, GOOD)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_quant4_weights, p, x, GOOD, ODD)
+
+
+def test_combine_backward_refusals(moe):
+    p, lay = _p(moe), _lay(moe)
+    good = [GOOD] * 5
+    for i in range(5):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_combine_backward, p, lay, *good[:i], None, *good[i + 1:])
+    for i in (0, 1, 3):
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_combine_backward, p, lay, *good[:i], ODD, *good[i + 1:])
+    for i in (2, 4):
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_combine_backward, p, lay, *good[:i], At(0x20002), *good[i + 1:])
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_combine_backward, p, _lay(moe, pos=At(None)), *good)
+
+
+def test_binding_refuses_other_shapes_types_and_strides(moe):
+    """Tensors whose type, shape or strides are not the call's are refused by the binding."""
+    import torch
+    p, lay = _p(moe), _lay(moe)
+    x = moe.Experts(64, 32, torch.empty((16, 32, 64), dtype=torch.bfloat16))
+    rows, out = torch.empty((512, 64), dtype=torch.bfloat16), torch.empty((512, 32), dtype=torch.bfloat16)
+    for bad_rows, bad_out in ((rows.float(), out), (rows[:, :32], out), (rows[:511], out), (rows, out.half()),
+                              (torch.empty((64, 512), dtype=torch.bfloat16).T, out), (rows, out[:, :16])):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward, p, lay, x, bad_rows, bad_out)
+    wrong = moe.Experts(64, 32, torch.empty((16, 64, 64), dtype=torch.bfloat16))
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward, p, lay, wrong, rows, out)
+    scales = torch.empty(100, dtype=torch.uint8)
+    codes = torch.empty((512, 32), dtype=torch.uint8)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_rows, p, lay, rows, codes, scales)
+    logits = torch.empty((256, 16))
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route_backward, p, moe.Routing(), logits,
+             torch.empty((256, 2), dtype=torch.int32), torch.empty((256, 2)), logits.bfloat16())
+
+
+def test_no_tokens_is_no_work(moe):
+    p = _p(moe, num_tokens=0)
+    moe.moe_route(p, moe.Routing(), None, None, None, stream=0)
+    moe.moe_route_backward(p, moe.Routing(), None, None, None, None, stream=0)
+    moe.moe_combine_backward(p, _lay(moe), None, None, None, None, None, stream=0)
+    moe.moe_expert_forward(p, _lay(moe), moe.Experts(64, 64, None), None, None, stream=0)
