@@ -728,7 +728,12 @@ int moe_swap_plan(const moe_problem* problem, const moe_layout_t* layout, int32_
 int moe_move_faults(uint32_t* bits, moe_stream_t stream) {
     MOE_NVTX("moe_move_faults");
     if (bits == nullptr) return MOE_ERR_INVALID;
-    return cuda_status(moe::read_move_faults(bits, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t movers = 0, experts = 0;
+    int rc = cuda_status(moe::read_move_faults(&movers, s));
+    if (rc == MOE_OK) rc = cuda_status(moe::read_expert_faults(&experts, s));
+    if (rc == MOE_OK) *bits = movers | experts;
+    return rc;
 }
 
 int moe_selftest_bounded_waits(uint32_t* bits, moe_stream_t stream) {

@@ -1,0 +1,108 @@
+// moe_tc.cuh -- the Blackwell tensor-core instructions that the experts'
+// products use: tcgen05 matrix products with accumulators in tensor memory
+// (TMEM), fed from shared memory by tensor (TMA) copies.
+#pragma once
+
+#include <cuda.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace tc {
+
+// ---- tensor memory ---------------------------------------------------------
+
+// Columns of tensor memory for the CTA (a power of two, 32 .. 512); the whole
+// warp calls it, the address arrives at *slot in shared memory.
+__device__ __forceinline__ void alloc(uint32_t slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t at, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(at), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Arrives on a barrier when every tensor-core operation this thread issued before is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes (the lane quarter of warp % 4); wait_ld before use.
+__device__ __forceinline__ void ld32(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- operands --------------------------------------------------------------
+
+// Shared-memory matrix descriptor, less its start address: distances in bytes
+// between 64-element pieces of the other dimension (lead) and between groups
+// of 8 rows (stride); swizzle 2 = 128-byte, 0 = none.
+__host__ __device__ constexpr uint64_t descriptor(uint32_t lead, uint32_t stride, uint32_t swizzle) {
+    return ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | ((uint64_t)swizzle << 61);
+}
+__device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t smem) { return desc | (uint64_t)((smem >> 4) & 0x3fff); }
+
+// Rows of 128 bytes along the contraction (K-major), 128-byte swizzle: groups of 8 rows lie 1 KB apart.
+constexpr uint64_t kAlongK = descriptor(16, 1024, 2);
+// 64 x 64 boxes of bf16 whose rows run along the result (MN-major): boxes 8 KB apart, 8 contraction steps 1 KB.
+constexpr uint64_t kAcrossK = descriptor(8192, 1024, 2);
+// 32 rows x 16 bytes of scales, no swizzle: 8 rows are 128 bytes.
+constexpr uint64_t kScales = descriptor(0, 128, 0);
+
+// Instruction descriptor of a bf16 product with fp32 sums, M = 128.
+__host__ __device__ constexpr uint32_t instruction(int n, bool a_across, bool b_across) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// ... of an E2M1 product with E8M0 scales per 32; pair: which half of the four scales of a scale word.
+__host__ __device__ constexpr uint32_t instruction4(int n, uint32_t pair) {
+    return ((2 * pair) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24) |
+           ((2 * pair) << 29);
+}
+
+// D (+)= A B^T, 16 contraction steps.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add) : "memory");
+}
+// The same over 64 contraction steps of 4-bit codes, scales from tensor memory.
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t sa, uint32_t sb,
+                                     bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"(sa), "r"(sb), "r"((uint32_t)add) : "memory");
+}
+// A scale block's 512 bytes of 4 scales x 128 rows to 4 columns of tensor memory, for all four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t d, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(d), "l"(desc) : "memory");
+}
+
+// ---- tensor copies ---------------------------------------------------------
+
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
+}
+
+}  // namespace tc
+}  // namespace moe
