@@ -1,34 +1,38 @@
-// moe_experts.cu -- products grouped by expert over ragged receive rows
+// moe_experts.cu -- bf16 products grouped by expert over ragged receive rows
 // ("Balancing and Beyond", section 1: the experts between dispatch and
 // combine).
 //
-// One persistent kernel per product, one CTA an SM.  A tile is 128 rows of a
-// result (receive rows of one expert; for the weights' gradient 128 of an
-// expert's weight rows) by BN columns, and its sums stay in tensor memory.  Six
-// warps: one thread feeds a ring of shared-memory stages with tensor copies,
-// one thread issues the tensor-core products, four warps turn finished sums
-// into results while the next tile is already being computed (two tiles' sums
-// fit in tensor memory, except for 256 columns in 4 bits, whose scales share
-// it).
+// One persistent kernel per product, two CTAs (a pair) on one tile of sums.  The
+// weights take the 256 rows of the tensor core's product and the receive rows its
+// columns, because the columns can be any multiple of 16: an expert's rows are cut
+// into equal tiles of at most 256, and no more than 15 columns of a tile are
+// computed in vain, whether an expert has one row or thousands.
 //
-// Which operand runs along the contraction in memory decides the descriptor:
-//   forward            out  = rows  W^T   both along it
-//   gradient of rows   drows = dout W     W across it
-//   gradient of weights dW  = dout^T rows both across it (the rows are summed)
-// A stage is the same bytes in all three: 128 bytes along memory by 128 and BN
-// rows, 128-byte swizzle, fetched in boxes of 64 rows.
+//   forward             sums[feature][row]   = W rows^T       W, rows along the contraction
+//   gradient of rows    sums[column][row]    = W^T dout^T     W across it
+//   gradient of weights sums[column][w]      = rows^T dout    both across it (rows are summed)
+//
+// Six warps a CTA: one thread feeds a ring of shared-memory stages with tensor
+// copies (128 bytes along memory, 128-byte swizzle), one thread of the pair issues
+// the products, four warps turn finished sums into results while the next tile is
+// computed (two tiles' sums fit in tensor memory).  A result row runs along the
+// lanes of tensor memory, so the store half turns 32 columns at a time through
+// shared memory, in fp32: activations see unrounded sums, and a result row is
+// written 256 bytes at a time.
+//
+// With a gated activation the 128 weight rows of a CTA are 64 gate rows and the 64
+// up rows of the same features.
 //
 // Ragged groups.  The host knows only how many rows there are in all; every CTA
-// counts the row blocks of each expert from the layout's counts (a scan over at
-// most 1024 experts) and takes tiles blockIdx, blockIdx + grid, ... of that
-// list.  Within an expert row blocks go first, so that the CTAs that share a
-// piece of its weights run at the same time and it comes from HBM once.  Rows of
-// the next expert that a tile's box reaches into only make sums that nobody
-// stores; where rows are summed (weights' gradient) they are cleared in shared
-// memory first.
+// counts the row tiles of each expert from the layout's counts (a scan over at
+// most 1024 experts) and the pairs take tiles pair, pair + pairs, ... of that
+// list.  Within an expert row tiles go first, so that the pairs that share a piece
+// of its weights run at the same time and it comes from HBM once.  Columns of
+// neighbours that a copy reaches into only make sums that nobody stores; where
+// rows are summed (weights' gradient) they are cleared in shared memory first.
 //
-// Every wait is bounded.  A CTA whose wait gives up records a fault, waits for
-// its own copies and products, frees its tensor memory and returns.
+// Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
+// own copies and products, frees its tensor memory and returns.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,97 +46,102 @@ namespace {
 __device__ unsigned int g_expert_faults;
 constexpr uint64_t kWaitNs = 1000000000ull;
 
+constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2;
+constexpr int kThreads = 192;          // warp 0 copies, warp 1 multiplies, warps 2 .. 5 store
+constexpr int kHalf = 128;             // rows of the sums in one CTA
+constexpr int kColumns = 256;          // most columns of a tile
+constexpr int kStep = 64;              // contraction of a stage
+constexpr int kRowBytes = 2 * kStep;
+constexpr int kBoxBytes = 64 * kRowBytes;
+constexpr int kBytesA = kHalf * kRowBytes, kBytesB = kColumns / 2 * kRowBytes;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kStages = 6;
+constexpr int kTurn = 32;              // columns turned at a time
+constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
+constexpr int kSmem = kStages * kStageBytes + 4 * kTurn * kTurnPitch + 1024;  // 1024: alignment
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], done[2], free[2], last, tail;
+    uint32_t tmem;
+    int scratch[32];
+    int base[MOE_MAX_EXPERTS + 1];
+    ExpertRows rows[MOE_MAX_EXPERTS];
+};
+
+// Stage and phase of a ring of kStages.
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Receive rows or weights rows arrive in boxes of 8, 16, 32, 64 and 128 rows (kMaps maps): a tile's share is two boxes
+// at most, its largest power of two and the rest rounded up to one.
+constexpr int kMaps = 5;
+struct Maps {
+    CUtensorMap rows[kMaps];
+};
+
 // A bounded wait of a whole warp: it gives up together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs)) != 0;
 }
 
-constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
-constexpr int kThreads = 192;          // warp 0 copies, warp 1 multiplies, warps 2 .. 5 store
-constexpr int kTileRows = 128;
-constexpr int kRowBytes = 128;         // of a stage, along memory
-constexpr int kBoxRows = 64;
-constexpr int kBoxBytes = kBoxRows * kRowBytes;
-constexpr int kScaleBlock = 512;
-
-template <int OP, int BN>
-struct Shape {
-    static constexpr bool k4 = OP == kForward4;
-    static constexpr int kStep = k4 ? 2 * kRowBytes : 64;                 // contraction of a stage
-    static constexpr int kBytesA = kTileRows * kRowBytes, kBytesB = BN * kRowBytes;
-    static constexpr int kScaleBytes = k4 ? 2 * kScaleBlock * (1 + BN / 128) : 0;
-    static constexpr int kStageBytes = kBytesA + kBytesB + kScaleBytes;
-    static constexpr int kStages = BN == 256 ? 4 : 6;
-    static constexpr int kSums = k4 && BN == 256 ? 1 : 2;                 // tiles in tensor memory
-    static constexpr int kColumns = k4 ? 512 : 2 * BN;                    // of tensor memory
-    static constexpr uint32_t kScaleA = kSums * BN, kScaleB = kScaleA + 8;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;            // 1024: alignment
-};
-
-struct Shared {
-    uint64_t full[8], empty[8], done[2], free[2], last;
-    uint32_t tmem;
-    int scratch[32];
-    int base[MOE_MAX_EXPERTS + 1];
-};
-
-// One tile of a result.
+// One tile of sums.
 struct Tile {
     int e;        // expert
     int first;    // its first receive row
-    int m0, n0;   // first row and column of the tile, inside the expert's result
-    int rows;     // rows of the tile that exist
-    int block;    // row block, counted over the experts
-    int steps;    // stages of its contraction
+    int f0;       // first of the tile's features (result columns)
+    int m0, rows; // its result rows, inside the expert: receive rows, or weight rows
+    int n;        // rows, rounded up to the tensor core's columns
+    int length;   // of the contraction
 };
 
 struct Plan {
     int64_t tiles;
-    int across;   // tiles side by side
-    int length;   // contraction (0: the expert's rows)
-    int cols;     // columns of a result
+    int features;  // result columns
+    int wide;      // of them in a tile
+    int across;    // tiles of features
 };
 
-template <int OP, int BN, bool GLU>
+template <int OP, bool GLU>
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, const int* base) {
     Plan p;
-    p.cols = OP == kForward || OP == kForward4 ? a.N : a.K;
-    const int wide = GLU ? BN / 2 : BN;
-    p.across = (p.cols + wide - 1) / wide;
-    p.length = OP == kBackWeights ? 0 : OP == kBackRows ? a.W : a.K;
-    p.tiles = OP == kBackWeights ? (int64_t)a.E * ((a.W + kTileRows - 1) / kTileRows) * p.across
-                                 : (int64_t)base[a.E] * p.across;
+    p.features = OP == kForward ? a.N : a.K;
+    p.wide = GLU ? kHalf : 2 * kHalf;
+    p.across = (p.features + p.wide - 1) / p.wide;
+    p.tiles = (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns) : (int64_t)base[a.E]) * p.across;
     return p;
 }
 
-template <int OP, int BN, bool GLU>
-__device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, const int* base, int64_t i) {
-    constexpr int kStep = Shape<OP, BN>::kStep;
-    constexpr int wide = GLU ? BN / 2 : BN;
+template <int OP, bool GLU>
+__device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, const Shared& sh, int64_t i) {
     Tile t;
+    int down, j, total;
     if (OP == kBackWeights) {
-        const int down = (a.W + kTileRows - 1) / kTileRows;
+        down = (a.W + kColumns - 1) / kColumns;
         t.e = (int)(i / ((int64_t)down * p.across));
-        const int j = (int)(i - (int64_t)t.e * down * p.across);
-        const ExpertRows x = expert_rows(a.count, a.offset, t.e, a.R);
-        t.first = x.first;
-        t.m0 = (j % down) * kTileRows;
-        t.n0 = (j / down) * wide;
-        t.rows = min(kTileRows, a.W - t.m0);
-        t.block = x.count;
-        t.steps = (x.count + kStep - 1) / kStep;
-        return t;
+        j = (int)(i - (int64_t)t.e * down * p.across);
+    } else {
+        t.e = expert_of_block(sh.base, a.E, (int)(i / p.across));
+        down = sh.base[t.e + 1] - sh.base[t.e];
+        j = (int)(i - (int64_t)sh.base[t.e] * p.across);
     }
-    t.e = expert_of_block(base, a.E, (int)(i / p.across));
-    const int down = base[t.e + 1] - base[t.e];
-    const int j = (int)(i - (int64_t)base[t.e] * p.across);
-    const ExpertRows x = expert_rows(a.count, a.offset, t.e, a.R);
+    const ExpertRows x = sh.rows[t.e];
     t.first = x.first;
-    t.m0 = (j % down) * kTileRows;
-    t.n0 = (j / down) * wide;
-    t.rows = min(kTileRows, x.count - t.m0);
-    t.block = base[t.e] + j % down;
-    t.steps = (p.length + kStep - 1) / kStep;
+    t.length = OP == kBackWeights ? x.count : OP == kBackRows ? a.W : a.K;
+    total = OP == kBackWeights ? a.W : x.count;
+    // equal tiles, in sixteens
+    const int per = ((total + down - 1) / down + 15) & ~15;
+    t.m0 = (j % down) * per;
+    t.f0 = (j / down) * p.wide;
+    t.rows = min(per, total - t.m0);
+    t.n = (t.rows + 15) & ~15;
     return t;
 }
 
@@ -142,367 +151,322 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
 
-// 32 columns of a row from c, `left` of them inside the result (a multiple of 8).
-__device__ __forceinline__ void store32(__nv_bfloat16* row, int left, const float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < left)
-            st_v4(reinterpret_cast<uint4*>(row) + i,
-                  make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
-                             pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7])));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    st_v4(reinterpret_cast<uint4*>(p), make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
+                                                  pack2(v[6], v[7])));
 }
-__device__ __forceinline__ void load32(const __nv_bfloat16* row, int left, float (&v)[32]) {
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 x = ld_stream_v4(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (8 * i < left) x = ld_stream_v4(reinterpret_cast<const uint4*>(row) + i);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[8 * i + 2 * j] = low(w[j]);
-            v[8 * i + 2 * j + 1] = high(w[j]);
-        }
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void sums32(uint32_t at, float (&v)[32]) {
-    uint32_t r[32];
-    tc::ld32(at, r);
-    tc::wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+__device__ __forceinline__ void turned8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+// The 128 threads of the store half.
+__device__ __forceinline__ void store_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// A finished tile to its results; sums: tensor memory of this warp's lanes.
-template <int OP, int BN, bool GLU>
-__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, int row) {
-    const bool live = row < t.rows;
-    const int64_t r = OP == kBackWeights ? (int64_t)t.e * a.W + t.m0 + row : (int64_t)t.first + t.m0 + row;
-    if (GLU) {
-        // accumulator columns: 64 of the gate, their 64 of up, and so on
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r * a.N + t.n0;
-        __nv_bfloat16* pre = a.pre == nullptr ? nullptr : static_cast<__nv_bfloat16*>(a.pre) + r * a.W + t.n0;
-#pragma unroll 1
-        for (int c = 0; c < BN / 2 && t.n0 + c < a.N; c += 32) {
-            float g[32], u[32];
-            const uint32_t at = sums + (c >> 6) * 128 + (c & 63);
-            sums32(at, g);
-            sums32(at + 64, u);
-            const int left = live ? a.N - t.n0 - c : 0;
-            if (pre != nullptr) {
-                store32(pre + c, left, g);
-                store32(pre + a.N + c, left, u);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
-            store32(out + c, left, g);
-        }
-        return;
-    }
+// A finished tile to its results.  sums: tensor memory of this warp's lanes; cta: which half of the features; tid: of 128.
+template <int OP, bool GLU>
+__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
+                                           int cta, int tid) {
+    constexpr int kMine = GLU ? kHalf / 2 : kHalf;      // features of this CTA
+    constexpr int kEights = kMine / 8, kAtOnce = 128 / kEights;
+    const int f = t.f0 + cta * kMine + (tid % kEights) * 8;
+    const bool live = f < p.features;
     const bool through = OP == kBackRows && a.pre_in != nullptr;
-    const int64_t pitch = through ? 2 * (int64_t)p.cols : p.cols;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r * pitch + t.n0;
-    const __nv_bfloat16* pre = through ? static_cast<const __nv_bfloat16*>(a.pre_in) + r * pitch + t.n0 : nullptr;
-#pragma unroll 1
-    for (int c = 0; c < BN && t.n0 + c < p.cols; c += 32) {
-        const int left = live ? p.cols - t.n0 - c : 0;
-        float v[32];
-        if (OP == kBackWeights && t.steps == 0) {
+    const int64_t pitch = through ? 2 * (int64_t)p.features : p.features;
+    const int64_t r0 = OP == kBackWeights ? (int64_t)t.e * a.W + t.m0 : (int64_t)t.first + t.m0;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
+    for (int c = 0; c < t.rows; c += kTurn) {
+        uint32_t v[32];
+        tc::ld32(sums + c, v);
+        tc::wait_ld();
+        if (OP == kBackWeights && t.length == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        } else {
-            sums32(sums + c, v);
+            for (int i = 0; i < 32; ++i) v[i] = 0;
         }
-        if (through) {
-            float g[32], u[32];
-            load32(pre + c, left, g);
-            load32(pre + p.cols + c, left, u);
+        store_sync();  // the block before has been read
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float s = sigmoid(g[i]);
-                u[i] = v[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-                v[i] = v[i] * g[i] * s;
+        for (int i = 0; i < 32; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
+        store_sync();
+#pragma unroll
+        for (int i = 0; i < kTurn; i += kAtOnce) {
+            const int row = i + tid / kEights;
+            if (!live || c + row >= t.rows) continue;
+            const float* from = turn + row * kTurnPitch + (tid % kEights) * 8;
+            float x[8];
+            turned8(from, x);
+            const int64_t at = (c + row) * pitch;
+            if (GLU) {
+                float u[8];
+                turned8(from + kHalf / 2, u);
+                if (a.pre != nullptr) {
+                    __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(a.pre) + (r0 + c + row) * a.W + f;
+                    store8(pre, x);
+                    store8(pre + a.N, u);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = x[k] * sigmoid(x[k]) * u[k];
+                store8(out + at, x);
+            } else if (through) {
+                const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(a.pre_in) + (r0 + c + row) * pitch + f;
+                float g[8], u[8];
+                load8(pre, g);
+                load8(pre + p.features, u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float s = sigmoid(g[k]);
+                    u[k] = x[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
+                    x[k] = x[k] * g[k] * s;
+                }
+                store8(out + at, u);
+                store8(out + at + p.features, x);
+            } else {
+                store8(out + at, x);
             }
-            store32(out + c, left, u);
-            store32(out + p.cols + c, left, v);
-        } else {
-            store32(out + c, left, v);
         }
     }
 }
 
 // ---- the kernel ----------------------------------------------------------------
 
-template <int OP, int BN, bool GLU>
-__global__ void __launch_bounds__(kThreads, 1)
-product_kernel(const ExpertArgs a, const int box_rows, const __grid_constant__ CUtensorMap map_a,
-               const __grid_constant__ CUtensorMap map_b) {
-    using S = Shape<OP, BN>;
-    constexpr bool across_a = OP == kBackWeights, across_b = OP == kBackRows || OP == kBackWeights;
+// The weights (the rows, in the weights' gradient) come through map_a, the other operand through maps.
+template <int OP, bool GLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+pair_kernel(const ExpertArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ Maps maps) {
+    constexpr bool across_a = OP != kForward, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
-    const uint32_t stages = (smem_u32(dynamic) + 1023u) & ~1023u;
+    const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
+    const uint32_t stages = smem_u32(dynamic) + skip;
+    float* turn = reinterpret_cast<float*>(dynamic + skip + kStages * kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto full = [&](int s) { return smem_u32(&sh.full[s]); };
-    auto empty = [&](int s) { return smem_u32(&sh.empty[s]); };
-    auto stage_at = [&](int s) { return stages + (uint32_t)s * S::kStageBytes; };
+    const int cta = (int)tc::cta_of_pair();
+    const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 2);   // both CTAs' copies arrive on the first CTA's
+            mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.done[i]), 1);
-            mbar_init(smem_u32(&sh.free[i]), 128);
+            mbar_init(smem_u32(&sh.free[i]), 2 * 4);
         }
         mbar_init(smem_u32(&sh.last), 1);
+        mbar_init(smem_u32(&sh.tail), 1);
         fence_mbar_init();
-        tc::prefetch_map(&map_a);
-        tc::prefetch_map(&map_b);
     }
-    if (warp == 1) tc::alloc(smem_u32(&sh.tmem), S::kColumns);
-    if (OP != kBackWeights) scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch);
+    if (warp == 0 && lane < kMaps) tc::prefetch_map(&maps.rows[lane]);
+    if (warp == 0 && lane == kMaps) tc::prefetch_map(&map_a);
+    if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 2 * kColumns);
+    scan_row_blocks<kColumns>(a.count, a.offset, a.E, a.R, sh.base, sh.scratch, sh.rows);
     tc::fence_before_sync();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    const Plan p = make_plan<OP, BN, GLU>(a, sh.base);
+    const Plan p = make_plan<OP, GLU>(a, sh.base);
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     bool ok = true;
-    int64_t issued = 0;  // stages
-    if (warp == 0 && lane == 0) {
-        const int groups = (a.K + 127) >> 7;                                  // of scales along a row
-        const int per = GLU ? 64 : 128;
-        const int wblocks = (a.N + per - 1) / per;
-        for (int64_t i = blockIdx.x; i < p.tiles && ok; i += gridDim.x) {
-            const Tile t = tile_at<OP, BN, GLU>(a, p, sh.base, i);
-            const int boxes_a = across_a ? (t.rows + kBoxRows - 1) / kBoxRows : (t.rows + box_rows - 1) / box_rows;
-            const int bytes_a = across_a ? boxes_a * kBoxBytes : boxes_a * box_rows * kRowBytes;
-            // boxes of B that hold a column of the result; with a gate every other box is of the up half
-            const int pieces = min((p.cols - t.n0 + kBoxRows - 1) / kBoxRows, GLU ? BN / 128 : BN / kBoxRows);
-            const int boxes_b = GLU ? 2 * pieces : pieces;
-            for (int kb = 0; kb < t.steps; ++kb) {
-                const int s = (int)(issued % S::kStages);
-                if (!mbar_wait_bounded(empty(s), (uint32_t)((issued / S::kStages) & 1) ^ 1u, kWaitNs)) {
+    Ring ring;
+    int issued = 0;  // stages, up to kStages
+    // where the sums are over rows, the whole warp works on an expert's last stage; else one thread does it all
+    if (warp == 0 && (OP == kBackWeights || lane == 0)) {
+        const uint32_t full0 = tc::in_first(full);
+        uint32_t tails = 0;
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            const int half = t.n / 2;                                        // columns of B in this CTA
+            const int fa = t.f0 + cta * (GLU ? kHalf / 2 : kHalf);            // its first feature
+            const int boxes_a = GLU ? 2 : min(max((p.features - fa + 63) / 64, 0), 2);
+            // B along the contraction: the box of the largest power of two, and one for the rest
+            int rows0 = 64, rows1 = half > 64 ? 64 : 0;
+            const CUtensorMap *map0 = &maps.rows[0], *map1 = map0;
+            if (!across_b) {
+                const int top = 31 - __clz(half);
+                rows0 = 1 << top;
+                map0 = &maps.rows[top - 3];
+                const int rest = half - rows0;
+                rows1 = 0;
+                if (rest > 0) {
+                    const int up = rest <= 8 ? 3 : 32 - __clz(rest - 1);
+                    rows1 = 1 << up;
+                    map1 = &maps.rows[up - 3];
+                }
+            }
+            const uint32_t bytes = boxes_a * kBoxBytes + (rows0 + rows1) * kRowBytes;
+            const int b0 = (OP == kBackWeights ? 0 : t.first) + t.m0 + cta * half;
+            for (int k0 = 0; k0 < t.length; k0 += kStep) {
+                const bool got = mbar_wait_bounded(empty + 8 * ring.stage, ring.phase ^ 1u, kWaitNs);
+                if (OP == kBackWeights ? !__all_sync(0xffffffffu, got) : !got) {
                     ok = false;
                     break;
                 }
-                const uint32_t sa = stage_at(s), sb = sa + S::kBytesA, bar = full(s);
-                int bytes_s = 0, pair = 0, wb0 = 0, wbn = 0;
-                if (S::k4) {
-                    pair = min(2, groups - 2 * kb) * kScaleBlock;
-                    wb0 = t.n0 / per;
-                    wbn = min(BN / 128, wblocks - wb0);
-                    bytes_s = pair * (1 + wbn);
+                const uint32_t sa = stages + (uint32_t)ring.stage * kStageBytes, sb = sa + kBytesA;
+                const int left = t.length - k0;
+                // rows past the expert's last that would be summed: this CTA waits for the stage itself and clears them
+                const bool clear = OP == kBackWeights && left < kStep && (left & 15) != 0;
+                if (lane == 0) {
+                    const uint32_t bar = clear ? smem_u32(&sh.tail) : full0 + 8 * ring.stage;
+                    tc::arrive_expect_cluster(bar, bytes);
+                    if (OP == kBackWeights) {
+                        if (boxes_a > 0) tc::load2_pair(sa, &map_a, fa, t.first + k0, bar);
+                        if (boxes_a > 1) tc::load2_pair(sa + kBoxBytes, &map_a, fa + 64, t.first + k0, bar);
+                        tc::load2_pair(sb, map0, b0, t.first + k0, bar);
+                        if (rows1 > 0) tc::load2_pair(sb + kBoxBytes, map0, b0 + 64, t.first + k0, bar);
+                    } else {
+                        if (boxes_a > 0) {
+                            if (OP == kBackRows) tc::load3_pair(sa, &map_a, fa, k0, t.e, bar);
+                            else tc::load3_pair(sa, &map_a, k0, fa, t.e, bar);
+                        }
+                        if (boxes_a > 1) {
+                            if (OP == kBackRows) tc::load3_pair(sa + kBoxBytes, &map_a, fa + 64, k0, t.e, bar);
+                            else tc::load3_pair(sa + kBoxBytes, &map_a, k0, fa + (GLU ? a.N : 64), t.e, bar);
+                        }
+                        tc::load2_pair(sb, map0, k0, b0, bar);
+                        if (rows1 > 0) tc::load2_pair(sb + rows0 * kRowBytes, map1, k0, b0 + rows0, bar);
+                    }
                 }
-                mbar_arrive_expect_tx(bar, bytes_a + boxes_b * kBoxBytes + bytes_s);
-                if (across_a) {
-                    for (int j = 0; j < boxes_a; ++j)
-                        tc::load2(sa + j * kBoxBytes, &map_a, t.m0 + j * 64, t.first + kb * 64, bar);
-                } else {
-                    for (int j = 0; j < boxes_a; ++j)
-                        tc::load2(sa + j * box_rows * kRowBytes, &map_a, kb * (S::k4 ? kRowBytes : 64),
-                                  t.first + t.m0 + j * box_rows, bar);
+                if (clear) {
+                    __syncwarp();
+                    if (!warp_wait(smem_u32(&sh.tail), tails++ & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int from = left * 8, to = ((left + 15) & ~15) * 8;  // 16-byte pieces of a box
+                    for (int b = 0; b < kStageBytes / kBoxBytes; ++b)
+                        for (int j = from + lane; j < to; j += 32)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                                         :: "r"(sa + b * kBoxBytes + j * 16), "r"(0u) : "memory");
+                    asm volatile("fence.proxy.async;" ::: "memory");  // also for the first CTA's products
+                    __syncwarp();
+                    if (lane == 0) tc::arrive_cluster(full0 + 8 * ring.stage);
                 }
-                for (int j = 0; j < boxes_b; ++j) {
-                    if (OP == kBackWeights)
-                        tc::load2(sb + j * kBoxBytes, &map_b, t.n0 + j * 64, t.first + kb * 64, bar);
-                    else if (OP == kBackRows)
-                        tc::load3(sb + j * kBoxBytes, &map_b, t.n0 + j * 64, kb * 64, t.e, bar);
-                    else
-                        tc::load3(sb + j * kBoxBytes, &map_b, kb * (S::k4 ? kRowBytes : 64),
-                                  GLU ? t.n0 + (j >> 1) * 64 + (j & 1) * a.N : t.n0 + j * 64, t.e, bar);
-                }
-                if (S::k4) {
-                    const uint32_t ss = sb + S::kBytesB;
-                    const int block = min(t.block, a.R / 128 + a.E - 1);
-                    bulk_g2s(ss, static_cast<const uint8_t*>(a.row_scales) +
-                                     ((int64_t)block * groups + 2 * kb) * kScaleBlock, pair, bar);
-                    for (int j = 0; j < wbn; ++j)
-                        bulk_g2s(ss + (1 + j) * 2 * kScaleBlock,
-                                 static_cast<const uint8_t*>(a.weight_scales) +
-                                     (((int64_t)t.e * wblocks + wb0 + j) * groups + 2 * kb) * kScaleBlock, pair, bar);
-                }
-                ++issued;
+                ring.next();
+                issued = min(issued + 1, kStages);
             }
         }
-    } else if (warp == 1) {
-        int64_t taken = 0;
+    } else if (warp == 1 && cta == 0 && lane == 0) {
         int n = 0;
-        for (int64_t i = blockIdx.x; i < p.tiles && ok; i += gridDim.x, ++n) {
-            const Tile t = tile_at<OP, BN, GLU>(a, p, sh.base, i);
-            const int length = OP == kBackWeights ? t.block : p.length;
-            const int half = n % S::kSums;
-            const uint32_t sums = tmem + half * BN;
-            if (!warp_wait(smem_u32(&sh.free[half]), (uint32_t)((n / S::kSums) & 1) ^ 1u)) {
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            const uint32_t sums = tmem + (n & 1) * kColumns;
+            const uint32_t instr = tc::instruction_pair(t.n, across_a, across_b);
+            if (!mbar_wait_bounded(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u, kWaitNs)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            for (int kb = 0; kb < t.steps; ++kb) {
-                const int s = (int)(taken % S::kStages);
-                if (!warp_wait(full(s), (uint32_t)((taken / S::kStages) & 1))) {
+            for (int k0 = 0; k0 < t.length; k0 += kStep) {
+                if (!mbar_wait_bounded(full + 8 * ring.stage, ring.phase, kWaitNs)) {
                     ok = false;
                     break;
                 }
-                ++taken;
                 tc::fence_after_sync();
-                const uint32_t sa = stage_at(s), sb = sa + S::kBytesA;
-                constexpr int kMma = S::k4 ? 64 : 16;                         // contraction of an instruction
-                const int left = min(S::kStep, length - kb * S::kStep);
-                const int count = (left + kMma - 1) / kMma;
-                if (OP == kBackWeights && left % kMma != 0) {
-                    // rows past the expert's last are another expert's: clear the ones that would be summed
-                    const int n0 = left * 8, n1 = count * kMma * 8;           // 16-byte pieces of a box
-                    for (int b = 0; b < (S::kBytesA + S::kBytesB) / kBoxBytes; ++b)
-                        for (int j = n0 + lane; j < n1; j += 32)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
-                                         :: "r"(sa + b * kBoxBytes + j * 16), "r"(0u) : "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    if (S::k4) {
-                        const uint32_t ss = sb + S::kBytesB;
-                        for (int g = 0; 2 * g < count; ++g) {
-                            tc::copy_scales(tmem + S::kScaleA + 4 * g, tc::at(tc::kScales, ss + g * kScaleBlock));
+                const uint32_t sa = stages + (uint32_t)ring.stage * kStageBytes;
+                const uint64_t da = tc::at(across_a ? tc::kAcrossK : tc::kAlongK, sa);
+                const uint64_t db = tc::at(across_b ? tc::kAcrossK : tc::kAlongK, sa + kBytesA);
+                const int count = (min(kStep, t.length - k0) + 15) / 16;
 #pragma unroll
-                            for (int j = 0; j < BN / 128; ++j)
-                                tc::copy_scales(tmem + S::kScaleB + g * (BN / 32) + 4 * j,
-                                                tc::at(tc::kScales, ss + ((1 + j) * 2 + g) * kScaleBlock));
-                        }
-                        for (int k = 0; k < count; ++k)
-                            tc::mma4(sums, tc::at(tc::kAlongK, sa + k * 32), tc::at(tc::kAlongK, sb + k * 32),
-                                     tc::instruction4(BN, k & 1), tmem + S::kScaleA + 4 * (k >> 1),
-                                     tmem + S::kScaleB + (k >> 1) * (BN / 32), kb > 0 || k > 0);
-                    } else {
-                        for (int k = 0; k < count; ++k) {
-                            const uint64_t da = across_a ? tc::at(tc::kAcrossK, sa + k * 2048)
-                                                         : tc::at(tc::kAlongK, sa + k * 32);
-                            const uint64_t db = across_b ? tc::at(tc::kAcrossK, sb + k * 2048)
-                                                         : tc::at(tc::kAlongK, sb + k * 32);
-                            tc::mma(sums, da, db, tc::instruction(BN, across_a, across_b), kb > 0 || k > 0);
-                        }
-                    }
-                    tc::commit(empty(s));
-                }
-                __syncwarp();
+                for (int k = 0; k < kStep / 16; ++k)
+                    if (k < count)
+                        tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
+                                     k0 > 0 || k > 0);
+                tc::commit_pair(empty + 8 * ring.stage);
+                ring.next();
             }
-            if (ok && lane == 0) tc::commit(smem_u32(&sh.done[half]));
-            __syncwarp();
+            if (ok) tc::commit_pair(smem_u32(&sh.done[n & 1]));
         }
         // whatever was issued is done before tensor memory is freed
-        if (lane == 0) tc::commit(smem_u32(&sh.last));
-        __syncwarp();
-        ok = warp_wait(smem_u32(&sh.last), 0) && ok;
+        tc::commit_pair(smem_u32(&sh.last));
+        ok = mbar_wait_bounded(smem_u32(&sh.last), 0, kWaitNs) && ok;
     } else if (warp >= 2) {
         const int quarter = warp & 3;
         int n = 0;
-        for (int64_t i = blockIdx.x; i < p.tiles; i += gridDim.x, ++n) {
-            const Tile t = tile_at<OP, BN, GLU>(a, p, sh.base, i);
-            const int half = n % S::kSums;
-            if (!warp_wait(smem_u32(&sh.done[half]), (uint32_t)((n / S::kSums) & 1))) {
+        for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            // the four warps go on or give up together: they meet at barriers of their own below
+            const bool got = mbar_wait_bounded(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1), kWaitNs);
+            int all;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all) : "r"((int)got) : "memory");
+            if (!all) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            store_tile<OP, BN, GLU>(a, p, t, tmem + half * BN + ((uint32_t)(quarter * 32) << 16), quarter * 32 + lane);
+            store_tile<OP, GLU>(a, p, t, tmem + (n & 1) * kColumns + ((uint32_t)(quarter * 32) << 16), turn, cta,
+                                quarter * 32 + lane);
             tc::fence_before_sync();
-            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(&sh.free[half])) : "memory");
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
         }
     }
     if (!ok && lane == 0) atomicOr(&g_expert_faults, MOE_FAULT_WAIT_TIMEOUT);
     __syncwarp();
-    // no copy of this CTA is in flight when it ends (each was waited for by its reader unless a wait gave up)
-    if (warp == 0 && lane == 0)
-        for (int64_t i = max((int64_t)0, issued - S::kStages); i < issued; ++i)
-            mbar_wait_bounded(full((int)(i % S::kStages)), (uint32_t)((i / S::kStages) & 1), kWaitNs);
+    // no copy of this pair is in flight when it ends (each was waited for by its reader unless a wait gave up)
+    if (warp == 0 && cta == 0 && lane == 0)
+        for (; issued > 0; --issued) {
+            if (ring.stage-- == 0) {
+                ring.stage = kStages - 1;
+                ring.phase ^= 1u;
+            }
+            mbar_wait_bounded(full + 8 * ring.stage, ring.phase, kWaitNs);
+        }
     tc::fence_before_sync();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tc::dealloc(tmem, S::kColumns);
+    if (warp == 1) tc::dealloc_pair(tmem, 2 * kColumns);
 }
 
-// ---- host side ---------------------------------------------------------------------
-
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once (no link against the driver library).
-Encode encoder() {
-    static const Encode fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<Encode>(p);
-    }();
-    return fn;
-}
-
-// [depth][rows][cols] of bf16 (or of bytes), dense, in boxes of box_rows x 128 bytes with 128-byte swizzle; what a
-// box reaches past the end reads as zeros.
-bool make_map(CUtensorMap* map, const void* data, bool bytes, int64_t cols, int64_t rows, int64_t depth, int box_rows) {
-    const Encode encode = encoder();
-    if (encode == nullptr) return false;
-    const cuuint64_t size = bytes ? 1 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-    const cuuint64_t pitch[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)(kRowBytes / size), (cuuint32_t)box_rows, 1};
-    const cuuint32_t step[3] = {1, 1, 1};
-    return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
-                  const_cast<void*>(data), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int OP, int BN, bool GLU>
-cudaError_t launch(const ExpertArgs& a, int box_rows, cudaStream_t s) {
-    using S = Shape<OP, BN>;
-    CUtensorMap ma, mb;
+template <int OP, bool GLU>
+cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
+    CUtensorMap ma;
+    Maps mb{};
     bool ok;
-    if (OP == kForward4)
-        ok = make_map(&ma, a.rows, true, a.K / 2, a.R, 0, box_rows) &&
-             make_map(&mb, a.weights, true, a.K / 2, a.W, a.E, kBoxRows);
-    else if (OP == kBackWeights)
-        ok = make_map(&ma, a.dout, false, a.W, a.R, 0, kBoxRows) && make_map(&mb, a.rows, false, a.K, a.R, 0, kBoxRows);
-    else
-        ok = make_map(&ma, OP == kForward ? a.rows : a.dout, false, OP == kForward ? a.K : a.W, a.R, 0, box_rows) &&
-             make_map(&mb, a.weights, false, a.K, a.W, a.E, kBoxRows);
+    if (OP == kBackWeights) {
+        ok = tc::make_map(&ma, a.rows, false, a.K, a.R, 0, 64) && tc::make_map(&mb.rows[0], a.dout, false, a.W, a.R, 0, 64);
+    } else {
+        ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, 64);
+        for (int i = 0; i < kMaps; ++i)
+            ok = ok && tc::make_map(&mb.rows[i], OP == kForward ? a.rows : a.dout, false, OP == kForward ? a.K : a.W, a.R,
+                                    0, 8 << i);
+    }
     if (!ok) return cudaErrorInvalidValue;
-    auto* kern = product_kernel<OP, BN, GLU>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), S::kSmem);
+    auto* kern = pair_kernel<OP, GLU>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
     if (e != cudaSuccess) return e;
-    // no more CTAs than there can be tiles
-    const int cols = OP == kForward || OP == kForward4 ? a.N : a.K;
-    const int wide = GLU ? BN / 2 : BN;
-    const int64_t across = (cols + wide - 1) / wide;
-    const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kTileRows - 1) / kTileRows)
-                                                       : a.R / kTileRows + (int64_t)(a.E < a.R ? a.E : a.R));
-    const int sms = device_sm_count();
-    kern<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, S::kSmem, s>>>(a, box_rows, ma, mb);
+    // no more pairs than there can be tiles
+    const int64_t features = OP == kForward ? a.N : a.K, wide = GLU ? kHalf : 2 * kHalf;
+    const int64_t across = (features + wide - 1) / wide;
+    const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
+                                                       : a.R / kColumns + (int64_t)(a.E < a.R ? a.E : a.R));
+    const int64_t pairs = device_sm_count() / 2;
+    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem, s>>>(a, ma, mb);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s) {
-    return a.glu ? launch<kForward, 256, true>(a, kBoxRows, s) : launch<kForward, 256, false>(a, kBoxRows, s);
+    return a.glu ? launch<kForward, true>(a, s) : launch<kForward, false>(a, s);
 }
-cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s) {
-    return launch<kBackRows, 256, false>(a, kBoxRows, s);
-}
+cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s) { return launch<kBackRows, false>(a, s); }
 cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s) {
-    return launch<kBackWeights, 256, false>(a, kBoxRows, s);
-}
-cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
-    return a.glu ? launch<kForward4, 256, true>(a, kBoxRows, s) : launch<kForward4, 256, false>(a, kBoxRows, s);
+    return launch<kBackWeights, false>(a, s);
 }
 
 cudaError_t read_expert_faults(uint32_t* bits, cudaStream_t stream) {

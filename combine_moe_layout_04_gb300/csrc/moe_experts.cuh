@@ -15,17 +15,22 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t* count, const in
     return {first, min(max(count[e], 0), R - first)};
 }
 
-// base[e] = sum over e' < e of ceil(rows(e') / 128), base[E] the total: the
+// base[e] = sum over e' < e of ceil(rows(e') / BLOCK), base[E] the total: the
 // row blocks of the experts one after another.  All threads of the block call
 // it (a multiple of 32, at most 1024 threads); scratch holds 32 ints.
+// keep: where not NULL, receives every expert's rows.
+template <int BLOCK>
 __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int32_t* offset, int E, int R, int* base,
-                                                int* scratch) {
+                                                int* scratch, ExpertRows* keep = nullptr) {
     const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (E + n - 1) / n;
     int sum = 0;
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
-        if (e < E) sum += (expert_rows(count, offset, e, R).count + 127) >> 7;
+        if (e >= E) continue;
+        const ExpertRows x = expert_rows(count, offset, e, R);
+        sum += (x.count + BLOCK - 1) / BLOCK;
+        if (keep != nullptr) keep[e] = x;
     }
     int inc = sum;
 #pragma unroll
@@ -41,7 +46,7 @@ __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int3
         const int e = tid * per + i;
         if (e < E) {
             base[e] = at;
-            at += (expert_rows(count, offset, e, R).count + 127) >> 7;
+            at += (expert_rows(count, offset, e, R).count + BLOCK - 1) / BLOCK;
             if (e == E - 1) base[E] = at;
         }
     }
