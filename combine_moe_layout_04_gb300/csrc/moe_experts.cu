@@ -5,17 +5,17 @@
 // One persistent kernel per product, two CTAs (a pair) on one tile of sums.  The
 // weights take the 256 rows of the tensor core's product and the receive rows its
 // columns, because the columns can be any multiple of 16: an expert's rows are cut
-// into equal tiles of at most 256, and no more than 15 columns of a tile are
-// computed in vain, whether an expert has one row or thousands.
+// into equal tiles, and no more than 15 columns of a tile are computed in vain,
+// whether an expert has one row or thousands.
 //
 //   forward             sums[feature][row]   = W rows^T       W, rows along the contraction
 //   gradient of rows    sums[column][row]    = W^T dout^T     W across it
 //   gradient of weights sums[column][w]      = rows^T dout    both across it (rows are summed)
 //
-// Six warps a CTA: one thread feeds a ring of shared-memory stages with tensor
-// copies (128 bytes along memory, 128-byte swizzle), one thread of the pair issues
-// the products, four warps turn finished sums into results while the next tile is
-// computed (two tiles' sums fit in tensor memory).  A result row runs along the
+// Ten warps a CTA: one feeds a ring of shared-memory stages with tensor copies (128
+// bytes along memory, 128-byte swizzle), one of the pair issues the products, two
+// groups of four turn finished sums into results while the next tile is computed
+// (two tiles' sums of 256 columns fit in tensor memory).  A result row runs along the
 // lanes of tensor memory, so the store half turns 32 columns at a time through
 // shared memory, in fp32: activations see unrounded sums, and a result row is
 // written 256 bytes at a time.
@@ -34,6 +34,7 @@
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
 
+#include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,21 +45,20 @@ namespace moe {
 namespace {
 
 __device__ unsigned int g_expert_faults;
-constexpr uint64_t kWaitNs = 1000000000ull;
 
 constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2;
-constexpr int kThreads = 192;          // warp 0 copies, warp 1 multiplies, warps 2 .. 5 store
+constexpr int kThreads = 320;          // warp 0 copies, warp 1 multiplies, two groups of four warps store
 constexpr int kHalf = 128;             // rows of the sums in one CTA
-constexpr int kColumns = 256;          // most columns of a tile
+constexpr int kColumns = 256;          // of one half of tensor memory; a wide tile takes both halves
 constexpr int kStep = 64;              // contraction of a stage
 constexpr int kRowBytes = 2 * kStep;
 constexpr int kBoxBytes = 64 * kRowBytes;
-constexpr int kBytesA = kHalf * kRowBytes, kBytesB = kColumns / 2 * kRowBytes;
-constexpr int kStageBytes = kBytesA + kBytesB;
-constexpr int kStages = 6;
+constexpr int kBytesA = kHalf * kRowBytes;
+constexpr int kRingBytes = 180 * 1024;
+constexpr int kStages = 12;            // most stages in flight
 constexpr int kTurn = 32;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
-constexpr int kSmem = kStages * kStageBytes + 4 * kTurn * kTurnPitch + 1024;  // 1024: alignment
+constexpr int kSmem = kRingBytes + 2 * 4 * kTurn * kTurnPitch + 1024;  // 1024: alignment
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], last, tail;
@@ -68,28 +68,54 @@ struct Shared {
     ExpertRows rows[MOE_MAX_EXPERTS];
 };
 
-// Stage and phase of a ring of kStages.
+// How a launch cuts rows and shared memory: a tile has at most `columns` columns,
+// and shared memory holds `stages` stages of `bytes` (16 KB of one operand and
+// half the columns of the other).
+struct Cut {
+    int columns, stages, bytes;
+};
+
+// Where in the ring of stages a thread is.
 struct Ring {
-    int stage = 0;
+    int stage = 0, at = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == kStages) {
-            stage = 0;
+    __device__ __forceinline__ void next(const Cut& cut) {
+        at += cut.bytes;
+        if (++stage == cut.stages) {
+            stage = at = 0;
             phase ^= 1u;
         }
     }
 };
 
-// Receive rows or weights rows arrive in boxes of 8, 16, 32, 64 and 128 rows (kMaps maps): a tile's share is two boxes
-// at most, its largest power of two and the rest rounded up to one.
+// Receive rows arrive in boxes of 8, 16, 32, 64 and 128 rows (kMaps maps): a tile's share is two boxes at most for
+// each of its halves, the largest power of two and the rest rounded up to one.
 constexpr int kMaps = 5;
 struct Maps {
     CUtensorMap rows[kMaps];
 };
+struct Boxes {
+    int rows0, rows1;                  // rows1 == 0: one box
+    const CUtensorMap *map0, *map1;
+    __device__ __forceinline__ int bytes() const { return (rows0 + rows1) * kRowBytes; }
+};
+__device__ __forceinline__ Boxes boxes_of(const Maps& maps, int rows) {
+    Boxes b{0, 0, &maps.rows[0], &maps.rows[0]};
+    if (rows == 0) return b;
+    const int top = 31 - __clz(rows), rest = rows - (1 << top);
+    b.rows0 = 1 << top;
+    b.map0 = &maps.rows[top - 3];
+    if (rest > 0) {
+        const int up = rest <= 8 ? 3 : 32 - __clz(rest - 1);
+        b.rows1 = 1 << up;
+        b.map1 = &maps.rows[up - 3];
+    }
+    return b;
+}
 
 // A bounded wait of a whole warp: it gives up together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs)) != 0;
+    return __all_sync(0xffffffffu, wait_second(bar, parity)) != 0;
 }
 
 // One tile of sums.
@@ -98,7 +124,7 @@ struct Tile {
     int first;    // its first receive row
     int f0;       // first of the tile's features (result columns)
     int m0, rows; // its result rows, inside the expert: receive rows, or weight rows
-    int n;        // rows, rounded up to the tensor core's columns
+    int n, more;  // rows, rounded up to the tensor core's columns: up to 256, and a wide tile's others
     int length;   // of the contraction
 };
 
@@ -141,7 +167,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, cons
     t.m0 = (j % down) * per;
     t.f0 = (j / down) * p.wide;
     t.rows = min(per, total - t.m0);
-    t.n = (t.rows + 15) & ~15;
+    const int n = (t.rows + 15) & ~15;
+    t.n = min(n, kColumns);
+    t.more = n - t.n;
     return t;
 }
 
@@ -166,49 +194,55 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void turned8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 8 floats of a turned row; lanes 4 .. 7 of every 8 read their halves the other way round, so that 8 lanes cover all banks.
+__device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p + (swap ? 4 : 0));
+    const float4 b = *reinterpret_cast<const float4*>(p + (swap ? 0 : 4));
+    v[0] = swap ? b.x : a.x; v[1] = swap ? b.y : a.y; v[2] = swap ? b.z : a.z; v[3] = swap ? b.w : a.w;
+    v[4] = swap ? a.x : b.x; v[5] = swap ? a.y : b.y; v[6] = swap ? a.z : b.z; v[7] = swap ? a.w : b.w;
 }
-// The 128 threads of the store half.
-__device__ __forceinline__ void store_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The 128 threads of a store group (barriers 1 and 2).
+__device__ __forceinline__ void store_sync(int group) { asm volatile("bar.sync %0, 128;" :: "r"(1 + group) : "memory"); }
 
-// A finished tile to its results.  sums: tensor memory of this warp's lanes; cta: which half of the features; tid: of 128.
+// Rows m0 .. m0 + rows of a finished tile to their results: the store groups take blocks of 32 columns of the sums in
+// turn, each through its own block of shared memory, and fetch the next one while they write.  sums: tensor memory of
+// this warp's lanes; cta: which half of the features; tid: of 128.
 template <int OP, bool GLU>
-__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
-                                           int cta, int tid) {
+__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, int m0, int rows,
+                                           uint32_t sums, float* turn, int cta, int group, int tid) {
     constexpr int kMine = GLU ? kHalf / 2 : kHalf;      // features of this CTA
     constexpr int kEights = kMine / 8, kAtOnce = 128 / kEights;
     const int f = t.f0 + cta * kMine + (tid % kEights) * 8;
     const bool live = f < p.features;
+    const bool swap = (tid & 4) != 0;
     const bool through = OP == kBackRows && a.pre_in != nullptr;
     const int64_t pitch = through ? 2 * (int64_t)p.features : p.features;
-    const int64_t r0 = OP == kBackWeights ? (int64_t)t.e * a.W + t.m0 : (int64_t)t.first + t.m0;
+    const int64_t r0 = OP == kBackWeights ? (int64_t)t.e * a.W + m0 : (int64_t)t.first + m0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
-    for (int c = 0; c < t.rows; c += kTurn) {
-        uint32_t v[32];
-        tc::ld32(sums + c, v);
+    uint32_t v[32];
+    if (group * kTurn < rows) tc::ld32(sums + group * kTurn, v);
+    for (int c = group * kTurn; c < rows; c += 2 * kTurn) {
         tc::wait_ld();
         if (OP == kBackWeights && t.length == 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0;
         }
-        store_sync();  // the block before has been read
+        store_sync(group);  // the block before has been read
 #pragma unroll
         for (int i = 0; i < 32; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
-        store_sync();
+        store_sync(group);
+        if (c + 2 * kTurn < rows) tc::ld32(sums + c + 2 * kTurn, v);
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
-            if (!live || c + row >= t.rows) continue;
+            if (!live || c + row >= rows) continue;
             const float* from = turn + row * kTurnPitch + (tid % kEights) * 8;
             float x[8];
-            turned8(from, x);
+            turned8(from, swap, x);
             const int64_t at = (c + row) * pitch;
             if (GLU) {
                 float u[8];
-                turned8(from + kHalf / 2, u);
+                turned8(from + kHalf / 2, swap, u);
                 if (a.pre != nullptr) {
                     __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(a.pre) + (r0 + c + row) * a.W + f;
                     store8(pre, x);
@@ -239,37 +273,43 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
 
 // ---- the kernel ----------------------------------------------------------------
 
+// Whether the weights' 128 rows of a CTA come in one box.
+template <int OP, bool GLU>
+constexpr bool kOneBox = OP == kForward && !GLU;
+
 // The weights (the rows, in the weights' gradient) come through map_a, the other operand through maps.
 template <int OP, bool GLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-pair_kernel(const ExpertArgs a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ Maps maps) {
+pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ Maps maps) {
     constexpr bool across_a = OP != kForward, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
     const uint32_t stages = smem_u32(dynamic) + skip;
-    float* turn = reinterpret_cast<float*>(dynamic + skip + kStages * kStageBytes);
+    float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = (int)tc::cta_of_pair();
     const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < cut.stages; ++i) {
             mbar_init(full + 8 * i, 2);   // both CTAs' copies arrive on the first CTA's
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.done[i]), 1);
-            mbar_init(smem_u32(&sh.free[i]), 2 * 4);
+            mbar_init(smem_u32(&sh.free[i]), 2 * 8);
         }
         mbar_init(smem_u32(&sh.last), 1);
         mbar_init(smem_u32(&sh.tail), 1);
         fence_mbar_init();
     }
-    if (warp == 0 && lane < kMaps) tc::prefetch_map(&maps.rows[lane]);
+    if (warp == 0 && lane < (across_b ? 1 : kMaps)) tc::prefetch_map(&maps.rows[lane]);
     if (warp == 0 && lane == kMaps) tc::prefetch_map(&map_a);
     if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 2 * kColumns);
-    scan_row_blocks<kColumns>(a.count, a.offset, a.E, a.R, sh.base, sh.scratch, sh.rows);
+    scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch,
+                    [&](int rows) { return (rows + cut.columns - 1) / cut.columns; }, sh.rows);
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();
@@ -279,52 +319,41 @@ pair_kernel(const ExpertArgs a, const __grid_constant__ CUtensorMap map_a, const
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     bool ok = true;
-    Ring ring;
-    int issued = 0;  // stages, up to kStages
-    // where the sums are over rows, the whole warp works on an expert's last stage; else one thread does it all
-    if (warp == 0 && (OP == kBackWeights || lane == 0)) {
+    if (warp == 0) {
         const uint32_t full0 = tc::in_first(full);
         uint32_t tails = 0;
+        Ring ring;
+        int flying = 0;                // stages issued, up to all of them
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const int half = t.n / 2;                                        // columns of B in this CTA
+            const int half = t.n / 2, half1 = t.more / 2;                    // columns of B in this CTA
             const int fa = t.f0 + cta * (GLU ? kHalf / 2 : kHalf);            // its first feature
-            const int boxes_a = GLU ? 2 : min(max((p.features - fa + 63) / 64, 0), 2);
-            // B along the contraction: the box of the largest power of two, and one for the rest
-            int rows0 = 64, rows1 = half > 64 ? 64 : 0;
-            const CUtensorMap *map0 = &maps.rows[0], *map1 = map0;
-            if (!across_b) {
-                const int top = 31 - __clz(half);
-                rows0 = 1 << top;
-                map0 = &maps.rows[top - 3];
-                const int rest = half - rows0;
-                rows1 = 0;
-                if (rest > 0) {
-                    const int up = rest <= 8 ? 3 : 32 - __clz(rest - 1);
-                    rows1 = 1 << up;
-                    map1 = &maps.rows[up - 3];
-                }
-            }
-            const uint32_t bytes = boxes_a * kBoxBytes + (rows0 + rows1) * kRowBytes;
+            // A in one box of 128 rows (forward without a gate) or two of 64
+            const int boxes_a = GLU ? 2 : kOneBox<OP, GLU> ? fa < p.features
+                                                           : min(max((p.features - fa + 63) / 64, 0), 2);
+            // (across the contraction: boxes of 64 columns of the one map there is)
+            const Boxes b = across_b ? Boxes{64, half > 64 ? 64 : 0, &maps.rows[0], &maps.rows[0]} : boxes_of(maps, half);
+            const Boxes c = boxes_of(maps, half1);
+            const uint32_t bytes = boxes_a * (kOneBox<OP, GLU> ? 2 : 1) * kBoxBytes + b.bytes() + c.bytes();
             const int b0 = (OP == kBackWeights ? 0 : t.first) + t.m0 + cta * half;
+            const int c0 = t.first + t.m0 + t.n + cta * half1;
             for (int k0 = 0; k0 < t.length; k0 += kStep) {
-                const bool got = mbar_wait_bounded(empty + 8 * ring.stage, ring.phase ^ 1u, kWaitNs);
-                if (OP == kBackWeights ? !__all_sync(0xffffffffu, got) : !got) {
+                if (!warp_wait(empty + 8 * ring.stage, ring.phase ^ 1u)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sa = stages + (uint32_t)ring.stage * kStageBytes, sb = sa + kBytesA;
+                const uint32_t sa = stages + ring.at, sb = sa + kBytesA;
                 const int left = t.length - k0;
                 // rows past the expert's last that would be summed: this CTA waits for the stage itself and clears them
                 const bool clear = OP == kBackWeights && left < kStep && (left & 15) != 0;
-                if (lane == 0) {
+                if (tc::elect_one()) {
                     const uint32_t bar = clear ? smem_u32(&sh.tail) : full0 + 8 * ring.stage;
                     tc::arrive_expect_cluster(bar, bytes);
                     if (OP == kBackWeights) {
                         if (boxes_a > 0) tc::load2_pair(sa, &map_a, fa, t.first + k0, bar);
                         if (boxes_a > 1) tc::load2_pair(sa + kBoxBytes, &map_a, fa + 64, t.first + k0, bar);
-                        tc::load2_pair(sb, map0, b0, t.first + k0, bar);
-                        if (rows1 > 0) tc::load2_pair(sb + kBoxBytes, map0, b0 + 64, t.first + k0, bar);
+                        tc::load2_pair(sb, b.map0, b0, t.first + k0, bar);
+                        if (b.rows1 > 0) tc::load2_pair(sb + kBoxBytes, b.map0, b0 + 64, t.first + k0, bar);
                     } else {
                         if (boxes_a > 0) {
                             if (OP == kBackRows) tc::load3_pair(sa, &map_a, fa, k0, t.e, bar);
@@ -332,104 +361,150 @@ pair_kernel(const ExpertArgs a, const __grid_constant__ CUtensorMap map_a, const
                         }
                         if (boxes_a > 1) {
                             if (OP == kBackRows) tc::load3_pair(sa + kBoxBytes, &map_a, fa + 64, k0, t.e, bar);
-                            else tc::load3_pair(sa + kBoxBytes, &map_a, k0, fa + (GLU ? a.N : 64), t.e, bar);
+                            else tc::load3_pair(sa + kBoxBytes, &map_a, k0, fa + a.N, t.e, bar);
                         }
-                        tc::load2_pair(sb, map0, k0, b0, bar);
-                        if (rows1 > 0) tc::load2_pair(sb + rows0 * kRowBytes, map1, k0, b0 + rows0, bar);
+                        tc::load2_pair(sb, b.map0, k0, b0, bar);
+                        if (b.rows1 > 0) tc::load2_pair(sb + b.rows0 * kRowBytes, b.map1, k0, b0 + b.rows0, bar);
+                        const uint32_t sc = sb + b.bytes();
+                        if (c.rows0 > 0) tc::load2_pair(sc, c.map0, k0, c0, bar);
+                        if (c.rows1 > 0) tc::load2_pair(sc + c.rows0 * kRowBytes, c.map1, k0, c0 + c.rows0, bar);
                     }
                 }
+                __syncwarp();
                 if (clear) {
-                    __syncwarp();
                     if (!warp_wait(smem_u32(&sh.tail), tails++ & 1)) {
                         ok = false;
                         break;
                     }
                     const int from = left * 8, to = ((left + 15) & ~15) * 8;  // 16-byte pieces of a box
-                    for (int b = 0; b < kStageBytes / kBoxBytes; ++b)
+                    for (int k = 0; k < cut.bytes / kBoxBytes; ++k)
                         for (int j = from + lane; j < to; j += 32)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
-                                         :: "r"(sa + b * kBoxBytes + j * 16), "r"(0u) : "memory");
+                                         :: "r"(sa + k * kBoxBytes + j * 16), "r"(0u) : "memory");
                     asm volatile("fence.proxy.async;" ::: "memory");  // also for the first CTA's products
                     __syncwarp();
                     if (lane == 0) tc::arrive_cluster(full0 + 8 * ring.stage);
                 }
-                ring.next();
-                issued = min(issued + 1, kStages);
+                ring.next(cut);
+                flying = min(flying + 1, cut.stages);
             }
         }
-    } else if (warp == 1 && cta == 0 && lane == 0) {
-        int n = 0;
-        for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
-            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const uint32_t sums = tmem + (n & 1) * kColumns;
-            const uint32_t instr = tc::instruction_pair(t.n, across_a, across_b);
-            if (!mbar_wait_bounded(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u, kWaitNs)) {
-                ok = false;
-                break;
+        // no copy of this pair is in flight when it ends: its readers have waited for them, unless a wait gave up
+        if (cta == 0)
+            for (; flying > 0; --flying) {
+                if (ring.stage-- == 0) {
+                    ring.stage = cut.stages - 1;
+                    ring.phase ^= 1u;
+                }
+                warp_wait(full + 8 * ring.stage, ring.phase);
             }
+    } else if (warp == 1 && cta == 0) {
+        Ring ring;
+        int n = 0;                     // halves of tensor memory taken so far
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            const bool wide = !across_b && t.more > 0;
+            const int bytes_b = wide ? kHalf * kRowBytes : 0;                 // a wide tile's first half is full
+            const uint32_t sums = tmem + (n & 1) * kColumns, sums1 = tmem + ((n & 1) ^ 1) * kColumns;
+            const uint32_t instr = tc::instruction_pair(t.n, across_a, across_b);
+            const uint32_t instr1 = tc::instruction_pair(t.more, across_a, across_b);
+            ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
+            if (ok && wide)
+                ok = warp_wait(smem_u32(&sh.free[(n + 1) & 1]), (uint32_t)(((n + 1) >> 1) & 1) ^ 1u);
+            if (!ok) break;
             tc::fence_after_sync();
             for (int k0 = 0; k0 < t.length; k0 += kStep) {
-                if (!mbar_wait_bounded(full + 8 * ring.stage, ring.phase, kWaitNs)) {
+                if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                const uint32_t sa = stages + (uint32_t)ring.stage * kStageBytes;
+                const uint32_t sa = stages + ring.at;
                 const uint64_t da = tc::at(across_a ? tc::kAcrossK : tc::kAlongK, sa);
                 const uint64_t db = tc::at(across_b ? tc::kAcrossK : tc::kAlongK, sa + kBytesA);
                 const int count = (min(kStep, t.length - k0) + 15) / 16;
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kStep / 16; ++k)
-                    if (k < count)
-                        tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
-                                     k0 > 0 || k > 0);
-                tc::commit_pair(empty + 8 * ring.stage);
-                ring.next();
+                    for (int k = 0; k < kStep / 16; ++k)
+                        if (k < count)
+                            tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
+                                         k0 > 0 || k > 0);
+                    if (wide) {
+                        const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + bytes_b);
+#pragma unroll
+                        for (int k = 0; k < kStep / 16; ++k)
+                            if (k < count) tc::mma_pair(sums1, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
+                    }
+                    tc::commit_pair(empty + 8 * ring.stage);
+                }
+                __syncwarp();
+                ring.next(cut);
             }
-            if (ok) tc::commit_pair(smem_u32(&sh.done[n & 1]));
+            if (!ok) break;
+            if (tc::elect_one()) {
+                tc::commit_pair(smem_u32(&sh.done[n & 1]));
+                if (wide) tc::commit_pair(smem_u32(&sh.done[(n + 1) & 1]));
+            }
+            __syncwarp();
+            n += wide ? 2 : 1;
         }
         // whatever was issued is done before tensor memory is freed
-        tc::commit_pair(smem_u32(&sh.last));
-        ok = mbar_wait_bounded(smem_u32(&sh.last), 0, kWaitNs) && ok;
+        if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last));
+        __syncwarp();
+        ok = warp_wait(smem_u32(&sh.last), 0) && ok;
     } else if (warp >= 2) {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
-        for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            // the four warps go on or give up together: they meet at barriers of their own below
-            const bool got = mbar_wait_bounded(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1), kWaitNs);
-            int all;
-            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                         "bar.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                         : "=r"(all) : "r"((int)got) : "memory");
-            if (!all) {
-                ok = false;
-                break;
+            for (int m = 0; m < t.rows; m += kColumns, ++n) {
+                // the four warps of a group go on or give up together: they meet at a barrier of their own below
+                const bool got = wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1));
+                int all;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                             "bar.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                             : "=r"(all) : "r"((int)got), "r"(1 + group) : "memory");
+                if (!all) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                store_tile<OP, GLU>(a, p, t, t.m0 + m, min(kColumns, t.rows - m),
+                                    tmem + (n & 1) * kColumns + ((uint32_t)(quarter * 32) << 16), mine, cta,
+                                    group, quarter * 32 + lane);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
             }
-            tc::fence_after_sync();
-            store_tile<OP, GLU>(a, p, t, tmem + (n & 1) * kColumns + ((uint32_t)(quarter * 32) << 16), turn, cta,
-                                quarter * 32 + lane);
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
         }
     }
     if (!ok && lane == 0) atomicOr(&g_expert_faults, MOE_FAULT_WAIT_TIMEOUT);
     __syncwarp();
-    // no copy of this pair is in flight when it ends (each was waited for by its reader unless a wait gave up)
-    if (warp == 0 && cta == 0 && lane == 0)
-        for (; issued > 0; --issued) {
-            if (ring.stage-- == 0) {
-                ring.stage = kStages - 1;
-                ring.phase ^= 1u;
-            }
-            mbar_wait_bounded(full + 8 * ring.stage, ring.phase, kWaitNs);
-        }
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
     if (warp == 1) tc::dealloc_pair(tmem, 2 * kColumns);
+}
+
+// The cut of a launch, from the mean rows of an expert (a is all the host knows of them).  A tile that takes all rows of
+// its expert reads the weights once, and the narrower it is the more stages are in flight: 2 rows an expert (64 experts,
+// 7168 -> 2 x 2048) take 528 us with 64 columns, 548 with 256, 588 with 512; 128 rows take 677 us cut at 64 columns and
+// 582 us cut at 256.  Up to 256 columns one tile's sums are written while the next is computed.  A wide tile (both
+// halves of tensor memory) gives that up and still wins where it saves a second tile: 272 rows take 718 us cut at 320
+// columns and 854 us cut at 256, 360 rows (32 experts) 421 us at 384 and 474 us at 256; but 1040 rows, which four wide
+// tiles or five narrow ones hold, take 658 us cut at 320 and 582 us cut at 256 (2048 <- 7168, 32 experts).  Routing
+// spreads an expert's rows by about the square root of their mean; 3.5 of that hold almost all experts.
+template <int OP>
+Cut make_cut(const ExpertArgs& a) {
+    const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
+    Cut cut{kColumns, 0, 0};
+    if (OP != kBackWeights)
+        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 256 ? 256 : most <= 320 ? 320 : most <= 448 ? 384 : 256;
+    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes;
+    cut.stages = kRingBytes / cut.bytes < kStages ? kRingBytes / cut.bytes : kStages;
+    return cut;
 }
 
 template <int OP, bool GLU>
@@ -440,7 +515,7 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     if (OP == kBackWeights) {
         ok = tc::make_map(&ma, a.rows, false, a.K, a.R, 0, 64) && tc::make_map(&mb.rows[0], a.dout, false, a.W, a.R, 0, 64);
     } else {
-        ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, 64);
+        ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
         for (int i = 0; i < kMaps; ++i)
             ok = ok && tc::make_map(&mb.rows[i], OP == kForward ? a.rows : a.dout, false, OP == kForward ? a.K : a.W, a.R,
                                     0, 8 << i);
@@ -449,13 +524,14 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     auto* kern = pair_kernel<OP, GLU>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
     if (e != cudaSuccess) return e;
+    const Cut cut = make_cut<OP>(a);
     // no more pairs than there can be tiles
     const int64_t features = OP == kForward ? a.N : a.K, wide = GLU ? kHalf : 2 * kHalf;
     const int64_t across = (features + wide - 1) / wide;
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
-                                                       : a.R / kColumns + (int64_t)(a.E < a.R ? a.E : a.R));
+                                                       : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem, s>>>(a, ma, mb);
+    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem, s>>>(a, cut, ma, mb);
     return cudaGetLastError();
 }
 

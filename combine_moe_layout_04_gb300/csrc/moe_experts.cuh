@@ -6,6 +6,20 @@
 
 namespace moe {
 
+// Waits for a barrier phase, giving up after a second.  The clock is read only
+// once in 1024 tries: reading it costs more than a stage of a product lasts.
+__device__ __forceinline__ bool wait_second(uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 1023u) == 0u) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > 1000000000ull) return false;
+        }
+    }
+}
+
 // Rows of one expert, kept inside [0, R) whatever the layout holds.
 struct ExpertRows {
     int first, count;
@@ -15,13 +29,15 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t* count, const in
     return {first, min(max(count[e], 0), R - first)};
 }
 
-// base[e] = sum over e' < e of ceil(rows(e') / BLOCK), base[E] the total: the
-// row blocks of the experts one after another.  All threads of the block call
-// it (a multiple of 32, at most 1024 threads); scratch holds 32 ints.
-// keep: where not NULL, receives every expert's rows.
-template <int BLOCK>
+__host__ __device__ __forceinline__ int blocks_of_128(int rows) { return (rows + 127) >> 7; }
+
+// base[e] = sum over e' < e of blocks(rows of e'), base[E] the total: the row
+// blocks of the experts one after another.  All threads of the block call it (a
+// multiple of 32, at most 1024 threads); scratch holds 32 ints.  keep: where
+// not NULL, receives every expert's rows.
+template <typename F>
 __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int32_t* offset, int E, int R, int* base,
-                                                int* scratch, ExpertRows* keep = nullptr) {
+                                                int* scratch, F blocks, ExpertRows* keep = nullptr) {
     const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (E + n - 1) / n;
     int sum = 0;
@@ -29,7 +45,7 @@ __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int3
         const int e = tid * per + i;
         if (e >= E) continue;
         const ExpertRows x = expert_rows(count, offset, e, R);
-        sum += (x.count + BLOCK - 1) / BLOCK;
+        sum += blocks(x.count);
         if (keep != nullptr) keep[e] = x;
     }
     int inc = sum;
@@ -46,7 +62,7 @@ __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int3
         const int e = tid * per + i;
         if (e < E) {
             base[e] = at;
-            at += (expert_rows(count, offset, e, R).count + BLOCK - 1) / BLOCK;
+            at += blocks(expert_rows(count, offset, e, R).count);
             if (e == E - 1) base[E] = at;
         }
     }

@@ -40,11 +40,10 @@ namespace moe {
 namespace {
 
 __device__ unsigned int g_expert4_faults;
-constexpr uint64_t kWaitNs = 1000000000ull;
 
 // A bounded wait of a whole warp: it gives up together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitNs)) != 0;
+    return __all_sync(0xffffffffu, wait_second(bar, parity)) != 0;
 }
 
 constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
@@ -265,7 +264,7 @@ product_kernel(const ExpertArgs a, const int box_rows, const __grid_constant__ C
         tc::prefetch_map(&map_b);
     }
     if (warp == 1) tc::alloc(smem_u32(&sh.tmem), S::kColumns);
-    if (OP != kBackWeights) scan_row_blocks<128>(a.count, a.offset, a.E, a.R, sh.base, sh.scratch);
+    if (OP != kBackWeights) scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch, blocks_of_128);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -287,7 +286,7 @@ product_kernel(const ExpertArgs a, const int box_rows, const __grid_constant__ C
             const int boxes_b = GLU ? 2 * pieces : pieces;
             for (int kb = 0; kb < t.steps; ++kb) {
                 const int s = (int)(issued % S::kStages);
-                if (!mbar_wait_bounded(empty(s), (uint32_t)((issued / S::kStages) & 1) ^ 1u, kWaitNs)) {
+                if (!wait_second(empty(s), (uint32_t)((issued / S::kStages) & 1) ^ 1u)) {
                     ok = false;
                     break;
                 }
@@ -420,7 +419,7 @@ product_kernel(const ExpertArgs a, const int box_rows, const __grid_constant__ C
     // no copy of this CTA is in flight when it ends (each was waited for by its reader unless a wait gave up)
     if (warp == 0 && lane == 0)
         for (int64_t i = max((int64_t)0, issued - S::kStages); i < issued; ++i)
-            mbar_wait_bounded(full((int)(i % S::kStages)), (uint32_t)((i / S::kStages) & 1), kWaitNs);
+            wait_second(full((int)(i % S::kStages)), (uint32_t)((i / S::kStages) & 1));
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

@@ -69,7 +69,7 @@ __device__ __forceinline__ void quantise256(const uint4* row, uint32_t* codes, u
 __global__ void __launch_bounds__(kThreads)
 quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     __shared__ int base[MOE_MAX_EXPERTS + 1], scratch[32];
-    scan_row_blocks<128>(a.count, a.offset, a.E, a.R, base, scratch);
+    scan_row_blocks(a.count, a.offset, a.E, a.R, base, scratch, blocks_of_128);
     const int block = blockIdx.x;
     if (block >= base[a.E]) return;
     const int e = expert_of_block(base, a.E, block);

@@ -26,6 +26,10 @@ COUNTS = {
     "one row": [0, 0, 1, 0],
     "tile edges": [1, 127, 128, 129, 0, 255, 256, 257],
     "skewed": [0, 3, 700, 0, 16, 17, 64, 1, 0],
+    "a little over a tile": [257, 272, 300, 0, 320, 321, 255, 290],
+    "a tile and a half": [384, 360, 385, 350, 400, 0, 391],
+    "some dozens": [40, 64, 65, 33, 50, 0, 17],
+    "about a hundred": [90, 104, 128, 129, 72, 0, 100],
     "few each": [2, 1, 0, 3, 1, 1, 2, 0, 0, 1, 4, 1, 0, 1, 2, 1],
 }
 # (in_cols, out_cols): multiples of 8 that fill no tile, one tile, several
