@@ -729,11 +729,10 @@ int moe_move_faults(uint32_t* bits, moe_stream_t stream) {
     MOE_NVTX("moe_move_faults");
     if (bits == nullptr) return MOE_ERR_INVALID;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t movers = 0, experts = 0, experts4 = 0;
+    uint32_t movers = 0, experts = 0;
     int rc = cuda_status(moe::read_move_faults(&movers, s));
     if (rc == MOE_OK) rc = cuda_status(moe::read_expert_faults(&experts, s));
-    if (rc == MOE_OK) rc = cuda_status(moe::read_expert4_faults(&experts4, s));
-    if (rc == MOE_OK) *bits = movers | experts | experts4;
+    if (rc == MOE_OK) *bits = movers | experts;
     return rc;
 }
 

@@ -46,19 +46,30 @@ namespace {
 
 __device__ unsigned int g_expert_faults;
 
-constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2;
+constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
 constexpr int kThreads = 320;          // warp 0 copies, warp 1 multiplies, two groups of four warps store
 constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // of one half of tensor memory; a wide tile takes both halves
-constexpr int kStep = 64;              // contraction of a stage
-constexpr int kRowBytes = 2 * kStep;
+constexpr int kRowBytes = 128;         // of a stage, along memory
+template <int OP>
+constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : kRowBytes / 2;  // its contraction
 constexpr int kBoxBytes = 64 * kRowBytes;
 constexpr int kBytesA = kHalf * kRowBytes;
-constexpr int kRingBytes = 180 * 1024;
+template <int OP>
+constexpr int kRingBytes = (OP == kForward4 ? 170 : 180) * 1024;
 constexpr int kStages = 12;            // most stages in flight
 constexpr int kTurn = 32;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
-constexpr int kSmem = kRingBytes + 2 * 4 * kTurn * kTurnPitch + 1024;  // 1024: alignment
+constexpr int kTurnBytes = 4 * kTurn * kTurnPitch;
+template <int OP>                      // 1024: alignment; in 4 bits also the experts' first scale blocks
+constexpr int kSmem = kRingBytes<OP> + 2 * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
+
+// 4-bit stages end with the scales of 256 codes: 1 KB (two scale blocks along a row) of the weights' 128 rows and of
+// every 128 receive rows the tile touches; the products take them from tensor memory behind the sums, where a tile has
+// at most 192 columns for their sake.
+constexpr int kScaleBlock = 512, kScaleBytes = 3 * 2 * kScaleBlock;
+constexpr int kColumns4 = 192;
+constexpr uint32_t kScalesA = kColumns + kColumns4, kScalesB = kScalesA + 8;
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], last, tail;
@@ -92,7 +103,7 @@ struct Ring {
 // each of its halves, the largest power of two and the rest rounded up to one.
 constexpr int kMaps = 5;
 struct Maps {
-    CUtensorMap rows[kMaps];
+    CUtensorMap rows[kMaps], weight_scales, row_scales;
 };
 struct Boxes {
     int rows0, rows1;                  // rows1 == 0: one box
@@ -138,7 +149,7 @@ struct Plan {
 template <int OP, bool GLU>
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, const int* base) {
     Plan p;
-    p.features = OP == kForward ? a.N : a.K;
+    p.features = OP == kForward || OP == kForward4 ? a.N : a.K;
     p.wide = GLU ? kHalf : 2 * kHalf;
     p.across = (p.features + p.wide - 1) / p.wide;
     p.tiles = (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns) : (int64_t)base[a.E]) * p.across;
@@ -162,8 +173,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, cons
     t.first = x.first;
     t.length = OP == kBackWeights ? x.count : OP == kBackRows ? a.W : a.K;
     total = OP == kBackWeights ? a.W : x.count;
-    // equal tiles, in sixteens
-    const int per = ((total + down - 1) / down + 15) & ~15;
+    // equal tiles, in sixteens (in 4 bits by half blocks of scales)
+    constexpr int kUnit = OP == kForward4 ? 64 : 16;
+    const int per = ((total + down - 1) / down + kUnit - 1) / kUnit * kUnit;
     t.m0 = (j % down) * per;
     t.f0 = (j / down) * p.wide;
     t.rows = min(per, total - t.m0);
@@ -275,19 +287,20 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
 
 // Whether the weights' 128 rows of a CTA come in one box.
 template <int OP, bool GLU>
-constexpr bool kOneBox = OP == kForward && !GLU;
+constexpr bool kOneBox = (OP == kForward || OP == kForward4) && !GLU;
 
 // The weights (the rows, in the weights' gradient) come through map_a, the other operand through maps.
 template <int OP, bool GLU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
-    constexpr bool across_a = OP != kForward, across_b = OP == kBackWeights;
+    constexpr bool k4 = OP == kForward4, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
     const uint32_t stages = smem_u32(dynamic) + skip;
-    float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes);
+    float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes<OP>);
+    int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + 2 * kTurnBytes);  // [E + 1], in 4 bits
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = (int)tc::cta_of_pair();
     const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
@@ -307,9 +320,11 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     }
     if (warp == 0 && lane < (across_b ? 1 : kMaps)) tc::prefetch_map(&maps.rows[lane]);
     if (warp == 0 && lane == kMaps) tc::prefetch_map(&map_a);
+    if (k4 && warp == 0 && lane >= 8 && lane < 10) tc::prefetch_map(lane == 8 ? &maps.weight_scales : &maps.row_scales);
     if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 2 * kColumns);
     scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch,
                     [&](int rows) { return (rows + cut.columns - 1) / cut.columns; }, sh.rows);
+    if (k4) scan_row_blocks(a.count, a.offset, a.E, a.R, blocks, sh.scratch, blocks_of_128);
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();
@@ -334,10 +349,16 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             // (across the contraction: boxes of 64 columns of the one map there is)
             const Boxes b = across_b ? Boxes{64, half > 64 ? 64 : 0, &maps.rows[0], &maps.rows[0]} : boxes_of(maps, half);
             const Boxes c = boxes_of(maps, half1);
-            const uint32_t bytes = boxes_a * (kOneBox<OP, GLU> ? 2 : 1) * kBoxBytes + b.bytes() + c.bytes();
+            uint32_t bytes = boxes_a * (kOneBox<OP, GLU> ? 2 : 1) * kBoxBytes + b.bytes() + c.bytes();
+            // scale blocks: rows of 512 bytes, `groups` to a block of rows
+            const int groups = (a.K + 127) >> 7, per = GLU ? 64 : 128, wblocks = (a.N + per - 1) / per;
+            const int scaled = k4 ? ((t.m0 & 127) + t.n + 127) >> 7 : 0;      // blocks of receive rows
+            const int wrow = k4 ? (t.e * wblocks + min(fa / per, wblocks - 1)) * groups : 0;
+            const int rrow = k4 ? (blocks[t.e] + (t.m0 >> 7)) * groups : 0;
+            if (k4) bytes += (1 + scaled) * 2 * kScaleBlock;
             const int b0 = (OP == kBackWeights ? 0 : t.first) + t.m0 + cta * half;
             const int c0 = t.first + t.m0 + t.n + cta * half1;
-            for (int k0 = 0; k0 < t.length; k0 += kStep) {
+            for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
                 if (!warp_wait(empty + 8 * ring.stage, ring.phase ^ 1u)) {
                     ok = false;
                     break;
@@ -345,7 +366,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 const uint32_t sa = stages + ring.at, sb = sa + kBytesA;
                 const int left = t.length - k0;
                 // rows past the expert's last that would be summed: this CTA waits for the stage itself and clears them
-                const bool clear = OP == kBackWeights && left < kStep && (left & 15) != 0;
+                const bool clear = OP == kBackWeights && left < kStep<OP> && (left & 15) != 0;
                 if (tc::elect_one()) {
                     const uint32_t bar = clear ? smem_u32(&sh.tail) : full0 + 8 * ring.stage;
                     tc::arrive_expect_cluster(bar, bytes);
@@ -355,19 +376,29 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         tc::load2_pair(sb, b.map0, b0, t.first + k0, bar);
                         if (b.rows1 > 0) tc::load2_pair(sb + kBoxBytes, b.map0, b0 + 64, t.first + k0, bar);
                     } else {
+                        const int x = k4 ? k0 / 2 : k0;                       // along memory
                         if (boxes_a > 0) {
                             if (OP == kBackRows) tc::load3_pair(sa, &map_a, fa, k0, t.e, bar);
-                            else tc::load3_pair(sa, &map_a, k0, fa, t.e, bar);
+                            else tc::load3_pair(sa, &map_a, x, fa, t.e, bar);
                         }
                         if (boxes_a > 1) {
                             if (OP == kBackRows) tc::load3_pair(sa + kBoxBytes, &map_a, fa + 64, k0, t.e, bar);
-                            else tc::load3_pair(sa + kBoxBytes, &map_a, k0, fa + a.N, t.e, bar);
+                            else tc::load3_pair(sa + kBoxBytes, &map_a, x, fa + a.N, t.e, bar);
                         }
-                        tc::load2_pair(sb, b.map0, k0, b0, bar);
-                        if (b.rows1 > 0) tc::load2_pair(sb + b.rows0 * kRowBytes, b.map1, k0, b0 + b.rows0, bar);
-                        const uint32_t sc = sb + b.bytes();
-                        if (c.rows0 > 0) tc::load2_pair(sc, c.map0, k0, c0, bar);
-                        if (c.rows1 > 0) tc::load2_pair(sc + c.rows0 * kRowBytes, c.map1, k0, c0 + c.rows0, bar);
+                        tc::load2_pair(sb, b.map0, x, b0, bar);
+                        if (b.rows1 > 0) tc::load2_pair(sb + b.rows0 * kRowBytes, b.map1, x, b0 + b.rows0, bar);
+                        if (k4) {
+                            const uint32_t ss = sa + cut.bytes - kScaleBytes;
+                            const int g = k0 >> 7;
+                            tc::load2_pair(ss, &maps.weight_scales, 0, wrow + g, bar);
+                            tc::load2_pair(ss + 2 * kScaleBlock, &maps.row_scales, 0, rrow + g, bar);
+                            if (scaled > 1)
+                                tc::load2_pair(ss + 4 * kScaleBlock, &maps.row_scales, 0, rrow + groups + g, bar);
+                        } else {
+                            const uint32_t sc = sb + b.bytes();
+                            if (c.rows0 > 0) tc::load2_pair(sc, c.map0, k0, c0, bar);
+                            if (c.rows1 > 0) tc::load2_pair(sc + c.rows0 * kRowBytes, c.map1, k0, c0 + c.rows0, bar);
+                        }
                     }
                 }
                 __syncwarp();
@@ -403,17 +434,18 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         int n = 0;                     // halves of tensor memory taken so far
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const bool wide = !across_b && t.more > 0;
+            const bool wide = !across_b && !k4 && t.more > 0;
             const int bytes_b = wide ? kHalf * kRowBytes : 0;                 // a wide tile's first half is full
             const uint32_t sums = tmem + (n & 1) * kColumns, sums1 = tmem + ((n & 1) ^ 1) * kColumns;
-            const uint32_t instr = tc::instruction_pair(t.n, across_a, across_b);
-            const uint32_t instr1 = tc::instruction_pair(t.more, across_a, across_b);
+            // the instruction of the tile and, for a wide one, of its other columns; in 4 bits for either half of a scale word
+            const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0) : tc::instruction_pair(t.n, across_a, across_b);
+            const uint32_t instr1 = k4 ? tc::instruction4_pair(t.n, 1) : tc::instruction_pair(t.more, across_a, across_b);
             ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
             if (ok && wide)
                 ok = warp_wait(smem_u32(&sh.free[(n + 1) & 1]), (uint32_t)(((n + 1) >> 1) & 1) ^ 1u);
             if (!ok) break;
             tc::fence_after_sync();
-            for (int k0 = 0; k0 < t.length; k0 += kStep) {
+            for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
                 if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
                     ok = false;
                     break;
@@ -422,17 +454,36 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 const uint32_t sa = stages + ring.at;
                 const uint64_t da = tc::at(across_a ? tc::kAcrossK : tc::kAlongK, sa);
                 const uint64_t db = tc::at(across_b ? tc::kAcrossK : tc::kAlongK, sa + kBytesA);
-                const int count = (min(kStep, t.length - k0) + 15) / 16;
-                if (tc::elect_one()) {
+                constexpr int kOne = k4 ? 64 : 16;                            // contraction of an instruction
+                const int count = (min(kStep<OP>, t.length - k0) + kOne - 1) / kOne;
+                if (k4 && tc::elect_one()) {
+                    const uint32_t ss = sa + cut.bytes - kScaleBytes;
 #pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k)
+                    for (int g = 0; g < 2; ++g) {
+                        tc::copy_scales_pair(tmem + kScalesA + 4 * g, tc::at(tc::kScales, ss + g * kScaleBlock));
+                        tc::copy_scales_pair(tmem + kScalesB + 8 * g, tc::at(tc::kScales, ss + (2 + g) * kScaleBlock));
+                        if ((t.m0 & 127) + t.n > 128)
+                            tc::copy_scales_pair(tmem + kScalesB + 8 * g + 4,
+                                                 tc::at(tc::kScales, ss + (4 + g) * kScaleBlock));
+                    }
+                    // a tile that starts in the middle of a scale block starts two columns of 32 rows later
+                    const uint32_t sb4 = tmem + kScalesB + ((t.m0 & 127) >> 5);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < count)
+                            tc::mma4_pair(sums, da + k * 2, db + k * 2, k & 1 ? instr1 : instr,
+                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 8 * (k >> 1), k0 > 0 || k > 0);
+                    tc::commit_pair(empty + 8 * ring.stage);
+                } else if (!k4 && tc::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
                         if (k < count)
                             tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
                                          k0 > 0 || k > 0);
                     if (wide) {
                         const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + bytes_b);
 #pragma unroll
-                        for (int k = 0; k < kStep / 16; ++k)
+                        for (int k = 0; k < 4; ++k)
                             if (k < count) tc::mma_pair(sums1, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
                     }
                     tc::commit_pair(empty + 8 * ring.stage);
@@ -500,10 +551,12 @@ template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
     Cut cut{kColumns, 0, 0};
-    if (OP != kBackWeights)
+    if (OP == kForward4)
+        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : kColumns4;
+    else if (OP != kBackWeights)
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 256 ? 256 : most <= 320 ? 320 : most <= 448 ? 384 : 256;
-    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes;
-    cut.stages = kRingBytes / cut.bytes < kStages ? kRingBytes / cut.bytes : kStages;
+    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? kScaleBytes : 0);
+    cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
     return cut;
 }
 
@@ -514,6 +567,12 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     bool ok;
     if (OP == kBackWeights) {
         ok = tc::make_map(&ma, a.rows, false, a.K, a.R, 0, 64) && tc::make_map(&mb.rows[0], a.dout, false, a.W, a.R, 0, 64);
+    } else if (OP == kForward4) {
+        const int64_t groups = (a.K + 127) / 128, per = GLU ? 64 : 128;
+        ok = tc::make_map(&ma, a.weights, true, a.K / 2, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64) &&
+             tc::make_scale_map(&mb.weight_scales, a.weight_scales, a.E * ((a.N + per - 1) / per) * groups) &&
+             tc::make_scale_map(&mb.row_scales, a.row_scales, (a.R / 128 + a.E) * groups);
+        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K / 2, a.R, 0, 8 << i);
     } else {
         ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
         for (int i = 0; i < kMaps; ++i)
@@ -522,16 +581,16 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
     auto* kern = pair_kernel<OP, GLU>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem<OP>);
     if (e != cudaSuccess) return e;
     const Cut cut = make_cut<OP>(a);
     // no more pairs than there can be tiles
-    const int64_t features = OP == kForward ? a.N : a.K, wide = GLU ? kHalf : 2 * kHalf;
+    const int64_t features = OP == kForward || OP == kForward4 ? a.N : a.K, wide = GLU ? kHalf : 2 * kHalf;
     const int64_t across = (features + wide - 1) / wide;
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem, s>>>(a, cut, ma, mb);
+    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem<OP>, s>>>(a, cut, ma, mb);
     return cudaGetLastError();
 }
 
@@ -543,6 +602,10 @@ cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s) {
 cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s) { return launch<kBackRows, false>(a, s); }
 cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s) {
     return launch<kBackWeights, false>(a, s);
+}
+
+cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
+    return a.glu ? launch<kForward4, true>(a, s) : launch<kForward4, false>(a, s);
 }
 
 cudaError_t read_expert_faults(uint32_t* bits, cudaStream_t stream) {

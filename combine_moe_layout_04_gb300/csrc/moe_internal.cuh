@@ -480,7 +480,6 @@ cudaError_t launch_combine_group(const MoveArgs& m, const GroupArgs& ga, const v
 cudaError_t launch_expert_groups(const int32_t* e2r, int E, int R, int G, int32_t* group, cudaStream_t s);
 cudaError_t read_move_faults(uint32_t* bits, cudaStream_t s);
 cudaError_t read_expert_faults(uint32_t* bits, cudaStream_t s);
-cudaError_t read_expert4_faults(uint32_t* bits, cudaStream_t s);
 cudaError_t launch_swap_plan(const int32_t* count, const int32_t* e2r, int E, int R, int P, int tau,
                              int32_t* new_e2r, int32_t* swaps, cudaStream_t s);
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);

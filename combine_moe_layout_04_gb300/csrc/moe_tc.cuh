@@ -22,23 +22,8 @@ __device__ __forceinline__ bool elect_one() {
 
 // ---- tensor memory ---------------------------------------------------------
 
-// Columns of tensor memory for the CTA (a power of two, 32 .. 512); the whole
-// warp calls it, the address arrives at *slot in shared memory.
-__device__ __forceinline__ void alloc(uint32_t slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void dealloc(uint32_t at, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(at), "r"(cols) : "memory");
-}
-
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Arrives on a barrier when every tensor-core operation this thread issued before is done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-}
 
 // 32 columns of this warp's 32 lanes (the lane quarter of warp % 4); wait_ld before use.
 __device__ __forceinline__ void ld32(uint32_t at, uint32_t (&v)[32]) {
@@ -71,45 +56,8 @@ constexpr uint64_t kAcrossK = descriptor(8192, 1024, 2);
 // 32 rows x 16 bytes of scales, no swizzle: 8 rows are 128 bytes.
 constexpr uint64_t kScales = descriptor(0, 128, 0);
 
-// Instruction descriptor of a bf16 product with fp32 sums, M = 128.
-__host__ __device__ constexpr uint32_t instruction(int n, bool a_across, bool b_across) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-// ... of an E2M1 product with E8M0 scales per 32; pair: which half of the four scales of a scale word.
-__host__ __device__ constexpr uint32_t instruction4(int n, uint32_t pair) {
-    return ((2 * pair) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24) |
-           ((2 * pair) << 29);
-}
-
-// D (+)= A B^T, 16 contraction steps.
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add) : "memory");
-}
-// The same over 64 contraction steps of 4-bit codes, scales from tensor memory.
-__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t sa, uint32_t sb,
-                                     bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"(sa), "r"(sb), "r"((uint32_t)add) : "memory");
-}
-// A scale block's 512 bytes of 4 scales x 128 rows to 4 columns of tensor memory, for all four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t d, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(d), "l"(desc) : "memory");
-}
-
 // ---- tensor copies ---------------------------------------------------------
 
-__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
-}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
 }
@@ -120,6 +68,8 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 // and half the columns of B in its shared memory and 128 rows of the sums in its
 // tensor memory; one thread of the first CTA issues.
 
+// Columns of tensor memory in both CTAs (a power of two, 32 .. 512): a whole warp
+// of each calls it, the address arrives at *slot in its own shared memory.
 __device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(slot), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -127,19 +77,38 @@ __device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
 __device__ __forceinline__ void dealloc_pair(uint32_t at, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(at), "r"(cols) : "memory");
 }
-// Arrives on the barrier at this address in both CTAs.
+// Arrives on the barrier at this address in both CTAs when every tensor-core operation this thread issued before is done.
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
+// Instruction descriptor of a bf16 product with fp32 sums: 256 rows, n columns (a multiple of 16).
 __host__ __device__ constexpr uint32_t instruction_pair(int n, bool a_across, bool b_across) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_across ? 1u : 0u) << 15) | ((b_across ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((256u >> 4) << 24);
 }
+// ... of an E2M1 product with E8M0 scales per 32; half: which two of the four scales of a scale word.
+__host__ __device__ constexpr uint32_t instruction4_pair(int n, uint32_t half) {
+    return ((2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24) |
+           ((2 * half) << 29);
+}
+// D (+)= A B^T, 16 contraction steps.
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"((uint32_t)add) : "memory");
+}
+// The same over 64 contraction steps of 4-bit codes, scales from tensor memory.
+__device__ __forceinline__ void mma4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t sa, uint32_t sb,
+                                          bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(instr), "r"(sa), "r"(sb), "r"((uint32_t)add) : "memory");
+}
+// A scale block's 512 bytes of 4 scales x 128 rows to 4 columns of tensor memory, for all four lane quarters; in both
+// CTAs, each from its own shared memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t d, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(d), "l"(desc) : "memory");
 }
 // Copies into this CTA's shared memory that complete on a barrier of either CTA of the pair.
 __device__ __forceinline__ void load2_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -204,6 +173,17 @@ inline bool make_map(CUtensorMap* map, const void* data, bool bytes, int64_t col
     return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
                   const_cast<void*>(data), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [rows] of 512 bytes (scale blocks), two rows a box, as they are.
+inline bool make_scale_map(CUtensorMap* map, const void* data, int64_t rows) {
+    const Encode encode = encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, pitch[1] = {512};
+    const cuuint32_t box[2] = {128, 2}, step[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(data), dims, pitch, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
