@@ -238,10 +238,17 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's own lookup of a device's current stream, without a Stream object around it
+
+
 def _stream(stream) -> Optional[int]:
-    import torch
+    global _raw_stream
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -336,7 +343,7 @@ class Routing:
     scale: float = 1.0
 
     def c(self, logits) -> _RoutingC:
-        return _RoutingC(self.score, int(self.renormalise), self.scale,
+        return _RoutingC(self.score, bool(self.renormalise), self.scale,
                          MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32)
 
 
@@ -360,19 +367,28 @@ class Experts:
         return _ExpertsC(self.in_cols, self.out_cols, self.act, 0, _ptr(self.weights), _ptr(self.scales))
 
 
-def _take(where: str, t, dtype: str, *shape):
-    """Address of a tensor argument that has to be dense, of one of the given
-    types and of the given shape (None: anything, -1: any size there)."""
-    if t is None:
-        return None
-    if hasattr(t, "is_contiguous"):
-        kind = str(t.dtype).replace("torch.", "")
-        sizes = tuple(t.shape)
-        fits = not shape or (len(sizes) == len(shape) and all(a in (-1, b) for a, b in zip(shape, sizes)))
-        if not t.is_contiguous() or kind not in dtype.split("|") or not fits:
-            raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {dtype} tensor {list(shape) or ''} is wanted, "
-                                            f"not {kind} {list(sizes)}")
-    return t.data_ptr()
+class _Kinds(dict):
+    """The torch types of names joined by "|", looked up once."""
+
+    def __missing__(self, kinds: str):
+        import torch
+        found = self[kinds] = tuple(getattr(torch, n) for n in kinds.split("|"))
+        return found
+
+
+_KINDS = _Kinds()
+
+
+def _take(where: str, t, kinds: str, *shape):
+    """Address of a tensor argument that has to be dense, of one of these types
+    and (where given) of this shape."""
+    try:
+        if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # NULL, or an object with nothing but an address
+        return None if t is None else t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {kinds} tensor {list(shape) or ''} is wanted, not "
+                                    f"{t.dtype} {list(t.shape)} with strides {list(t.stride())}")
 
 
 def _check(rc: int, where: str):

@@ -24,15 +24,13 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
 
-// 256 columns of a row, c0 + 8 lane on this lane (cols: a multiple of 32).
-// Codes go to the row's codes, scales to the 4-byte words of the row's place in
-// the scale blocks: word g of the row is at sc + 512 g.
-__device__ __forceinline__ void quantise256(const uint4* row, uint32_t* codes, uint8_t* sc, int c0, int cols,
-                                            int lane) {
+constexpr int kPiece = 1024;  // columns of a row a warp takes: four loads of 256 in flight
+
+// 256 columns of a row, c0 + 8 lane on this lane (cols: a multiple of 32), already loaded (v; 0 past the end).  Codes go
+// to the row's codes, scales to the 4-byte words of the row's place in the scale blocks: word g of the row is at sc + 512 g.
+__device__ __forceinline__ void quantise256(uint4 v, uint32_t* codes, uint8_t* sc, int c0, int cols, int lane) {
     const int c = c0 + 8 * lane;
     const bool live = c < cols;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (live) v = ld_stream_v4(row + (c >> 3));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     // magnitudes as integers order as the floats do; bf16 is the upper half
     uint32_t top = 0;
@@ -47,21 +45,30 @@ __device__ __forceinline__ void quantise256(const uint4* row, uint32_t* codes, u
     uint32_t out = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 x = make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
+        const float2 x = make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv);
         const uint32_t two = __nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest);
         out |= two << (8 * i);
     }
     if (live) codes[c >> 3] = bad ? 0u : out;
-    // lanes 0 and 16 gather the four scales of their 128 columns; past the last column the scale byte is 0
-    const int head = lane & 16;
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t s = __shfl_sync(kFull, live ? b : 0u, head + 4 * j);
-        word |= s << (8 * j);
-    }
-    const int col = c0 + 8 * head;
+    // the four scales of 128 columns meet in their first lane (0 and 16); past the last column the scale byte is 0
+    uint32_t word = live ? b : 0u;
+    word |= __shfl_down_sync(kFull, word, 4) << 8;
+    word |= __shfl_down_sync(kFull, word, 8) << 16;
+    const int col = c0 + 8 * (lane & 16);
     if ((lane & 15) == 0 && col < cols) *reinterpret_cast<uint32_t*>(sc + (int64_t)(col >> 7) * 512) = word;
+}
+
+// Columns c0 .. c0 + 1024 of a row (bf16) to its codes and scales.
+__device__ __forceinline__ void quantise_piece(const void* row, uint8_t* codes, uint8_t* sc, int c0, int cols, int lane) {
+    uint4 v[kPiece / 256];
+#pragma unroll
+    for (int i = 0; i < kPiece / 256; ++i) {
+        const int c = c0 + 256 * i + 8 * lane;
+        v[i] = c < cols ? ld_stream_v4(static_cast<const uint4*>(row) + (c >> 3)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPiece / 256; ++i)
+        if (c0 + 256 * i < cols) quantise256(v[i], reinterpret_cast<uint32_t*>(codes), sc, c0 + 256 * i, cols, lane);
 }
 
 // One block of the grid per (row block, piece of 1024 columns); the row blocks
@@ -79,12 +86,10 @@ quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (a.K + 127) >> 7;
     uint8_t* sc = scales + (int64_t)block * groups * 512;
-    const int c1 = min(a.K, (int)(blockIdx.y + 1) * 1024);
     for (int i = warp; i < n; i += kWarps) {
         const int64_t r = x.first + i0 + i;
-        for (int c = blockIdx.y * 1024; c < c1; c += 256)
-            quantise256(static_cast<const uint4*>(a.rows) + r * (a.K / 8),
-                        reinterpret_cast<uint32_t*>(codes + r * (a.K / 2)), sc + scale_byte(i, 0), c, a.K, lane);
+        quantise_piece(static_cast<const uint16_t*>(a.rows) + r * a.K, codes + r * (a.K / 2), sc + scale_byte(i, 0),
+                       blockIdx.y * kPiece, a.K, lane);
     }
 }
 
@@ -99,28 +104,26 @@ quant4_weights_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (a.K + 127) >> 7;
     uint8_t* sc = scales + (int64_t)blockIdx.x * groups * 512;
-    const int c1 = min(a.K, (int)(blockIdx.y + 1) * 1024);
     for (int i = warp; i < 128; i += kWarps) {
         const int n = b * per + i % per;                 // result column
         if (n >= a.N) continue;
         const int64_t r = e * a.W + n + (i >= per ? a.N : 0);
-        for (int c = blockIdx.y * 1024; c < c1; c += 256)
-            quantise256(static_cast<const uint4*>(a.weights) + r * (a.K / 8),
-                        reinterpret_cast<uint32_t*>(codes + r * (a.K / 2)), sc + scale_byte(i, 0), c, a.K, lane);
+        quantise_piece(static_cast<const uint16_t*>(a.weights) + r * a.K, codes + r * (a.K / 2), sc + scale_byte(i, 0),
+                       blockIdx.y * kPiece, a.K, lane);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s) {
-    const dim3 grid((unsigned)(a.R / 128 + min(a.E, a.R)), (unsigned)((a.K + 1023) / 1024));
+    const dim3 grid((unsigned)(a.R / 128 + min(a.E, a.R)), (unsigned)((a.K + kPiece - 1) / kPiece));
     quant4_rows_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
     return cudaGetLastError();
 }
 
 cudaError_t launch_quant4_weights(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s) {
     const int per = a.glu ? 64 : 128;
-    const dim3 grid((unsigned)((int64_t)a.E * ((a.N + per - 1) / per)), (unsigned)((a.K + 1023) / 1024));
+    const dim3 grid((unsigned)((int64_t)a.E * ((a.N + per - 1) / per)), (unsigned)((a.K + kPiece - 1) / kPiece));
     quant4_weights_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
     return cudaGetLastError();
 }
