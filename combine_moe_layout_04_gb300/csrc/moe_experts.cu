@@ -47,9 +47,12 @@ namespace {
 __device__ unsigned int g_expert_faults;
 
 constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
-constexpr int kThreads = 320;          // warp 0 copies, warp 1 multiplies, two groups of four warps store
+constexpr int kGroups = 4;             // of four warps that store
+constexpr int kThreads = 64 + 128 * kGroups;  // warp 0 copies, warp 1 multiplies
 constexpr int kHalf = 128;             // rows of the sums in one CTA
-constexpr int kColumns = 256;          // of one half of tensor memory; a wide tile takes both halves
+constexpr int kColumns = 256;          // most columns of one product instruction
+template <int OP>
+constexpr int kTop = OP == kForward4 ? 448 : 512;  // columns of tensor memory for sums
 constexpr int kRowBytes = 128;         // of a stage, along memory
 template <int OP>
 constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : kRowBytes / 2;  // its contraction
@@ -58,21 +61,19 @@ constexpr int kBytesA = kHalf * kRowBytes;
 template <int OP>
 constexpr int kRingBytes = (OP == kForward4 ? 170 : 180) * 1024;
 constexpr int kStages = 12;            // most stages in flight
-constexpr int kTurn = 32;              // columns turned at a time
+constexpr int kTurn = 16;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
 constexpr int kTurnBytes = 4 * kTurn * kTurnPitch;
 template <int OP>                      // 1024: alignment; in 4 bits also the experts' first scale blocks
-constexpr int kSmem = kRingBytes<OP> + 2 * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
+constexpr int kSmem = kRingBytes<OP> + kGroups * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
 
 // 4-bit stages end with the scales of 256 codes: 1 KB (two scale blocks along a row) of the weights' 128 rows and of
-// every 128 receive rows the tile touches; the products take them from tensor memory behind the sums, where a tile has
-// at most 192 columns for their sake.
-constexpr int kScaleBlock = 512, kScaleBytes = 3 * 2 * kScaleBlock;
-constexpr int kColumns4 = 192;
-constexpr uint32_t kScalesA = kColumns + kColumns4, kScalesB = kScalesA + 8;
+// every 128 receive rows the tile touches (three at most); the products take them from tensor memory above the sums.
+constexpr int kScaleBlock = 512, kScaleBytes = 4 * 2 * kScaleBlock;
+constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], done[2], free[2], last, tail;
+    uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail;
     uint32_t tmem;
     int scratch[32];
     int base[MOE_MAX_EXPERTS + 1];
@@ -135,7 +136,7 @@ struct Tile {
     int first;    // its first receive row
     int f0;       // first of the tile's features (result columns)
     int m0, rows; // its result rows, inside the expert: receive rows, or weight rows
-    int n, more;  // rows, rounded up to the tensor core's columns: up to 256, and a wide tile's others
+    int n;        // rows, rounded up to the tensor core's columns
     int length;   // of the contraction
 };
 
@@ -179,9 +180,7 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, cons
     t.m0 = (j % down) * per;
     t.f0 = (j / down) * p.wide;
     t.rows = min(per, total - t.m0);
-    const int n = (t.rows + 15) & ~15;
-    t.n = min(n, kColumns);
-    t.more = n - t.n;
+    t.n = (t.rows + 15) & ~15;
     return t;
 }
 
@@ -213,15 +212,16 @@ __device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]
     v[0] = swap ? b.x : a.x; v[1] = swap ? b.y : a.y; v[2] = swap ? b.z : a.z; v[3] = swap ? b.w : a.w;
     v[4] = swap ? a.x : b.x; v[5] = swap ? a.y : b.y; v[6] = swap ? a.z : b.z; v[7] = swap ? a.w : b.w;
 }
-// The 128 threads of a store group (barriers 1 and 2).
+// The 128 threads of a store group (barriers 1 and up).
 __device__ __forceinline__ void store_sync(int group) { asm volatile("bar.sync %0, 128;" :: "r"(1 + group) : "memory"); }
 
-// Rows m0 .. m0 + rows of a finished tile to their results: the store groups take blocks of 32 columns of the sums in
-// turn, each through its own block of shared memory, and fetch the next one while they write.  sums: tensor memory of
-// this warp's lanes; cta: which half of the features; tid: of 128.
+// A finished tile to its results: the store groups take blocks of 16 columns of the sums in turn, each through its own
+// block of shared memory, and fetch the next one while they write.  sums: tensor memory of this warp's lanes; cta: which
+// half of the features; tid: of 128.  up: from the first column to the last, else the other way; after `shared` blocks
+// (the columns the next tile's sums take over) this warp arrives on the barrier `over`.
 template <int OP, bool GLU>
-__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, int m0, int rows,
-                                           uint32_t sums, float* turn, int cta, int group, int tid) {
+__device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
+                                           int cta, int group, int tid, bool up, int shared, uint32_t over) {
     constexpr int kMine = GLU ? kHalf / 2 : kHalf;      // features of this CTA
     constexpr int kEights = kMine / 8, kAtOnce = 128 / kEights;
     const int f = t.f0 + cta * kMine + (tid % kEights) * 8;
@@ -229,25 +229,36 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     const bool swap = (tid & 4) != 0;
     const bool through = OP == kBackRows && a.pre_in != nullptr;
     const int64_t pitch = through ? 2 * (int64_t)p.features : p.features;
-    const int64_t r0 = OP == kBackWeights ? (int64_t)t.e * a.W + m0 : (int64_t)t.first + m0;
+    const int64_t r0 = OP == kBackWeights ? (int64_t)t.e * a.W + t.m0 : (int64_t)t.first + t.m0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
-    uint32_t v[32];
-    if (group * kTurn < rows) tc::ld32(sums + group * kTurn, v);
-    for (int c = group * kTurn; c < rows; c += 2 * kTurn) {
+    const int count = t.n / kTurn;
+    auto column = [&](int i) { return (up ? i : count - 1 - i) * kTurn; };
+    bool told = false;
+    auto tell = [&] {
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((tid & 31) == 0) tc::arrive_cluster(over);
+        told = true;
+    };
+    uint32_t v[kTurn];
+    if (group < count) tc::ld16(sums + column(group), v);
+    for (int b = group; b < count; b += kGroups) {
+        const int c = column(b);
+        if (!told && b >= shared) tell();
         tc::wait_ld();
         if (OP == kBackWeights && t.length == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0;
+            for (int i = 0; i < kTurn; ++i) v[i] = 0;
         }
         store_sync(group);  // the block before has been read
 #pragma unroll
-        for (int i = 0; i < 32; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
+        for (int i = 0; i < kTurn; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
         store_sync(group);
-        if (c + 2 * kTurn < rows) tc::ld32(sums + c + 2 * kTurn, v);
+        if (b + kGroups < count) tc::ld16(sums + column(b + kGroups), v);
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
-            if (!live || c + row >= rows) continue;
+            if (!live || c + row >= t.rows) continue;
             const float* from = turn + row * kTurnPitch + (tid % kEights) * 8;
             float x[8];
             turned8(from, swap, x);
@@ -281,6 +292,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
             }
         }
     }
+    if (!told) tell();
 }
 
 // ---- the kernel ----------------------------------------------------------------
@@ -300,7 +312,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
     const uint32_t stages = smem_u32(dynamic) + skip;
     float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes<OP>);
-    int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + 2 * kTurnBytes);  // [E + 1], in 4 bits
+    int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + kGroups * kTurnBytes);  // [E + 1], in 4 bits
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = (int)tc::cta_of_pair();
     const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
@@ -312,7 +324,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.done[i]), 1);
-            mbar_init(smem_u32(&sh.free[i]), 2 * 8);
+            mbar_init(smem_u32(&sh.free[i]), 2 * 4 * kGroups);
+            mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups);
         }
         mbar_init(smem_u32(&sh.last), 1);
         mbar_init(smem_u32(&sh.tail), 1);
@@ -321,7 +334,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     if (warp == 0 && lane < (across_b ? 1 : kMaps)) tc::prefetch_map(&maps.rows[lane]);
     if (warp == 0 && lane == kMaps) tc::prefetch_map(&map_a);
     if (k4 && warp == 0 && lane >= 8 && lane < 10) tc::prefetch_map(lane == 8 ? &maps.weight_scales : &maps.row_scales);
-    if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 2 * kColumns);
+    if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 512);
     scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch,
                     [&](int rows) { return (rows + cut.columns - 1) / cut.columns; }, sh.rows);
     if (k4) scan_row_blocks(a.count, a.offset, a.E, a.R, blocks, sh.scratch, blocks_of_128);
@@ -341,7 +354,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         int flying = 0;                // stages issued, up to all of them
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const int half = t.n / 2, half1 = t.more / 2;                    // columns of B in this CTA
+            const int n0 = min(t.n, kColumns);                                // columns of the first product, others
+            const int half = n0 / 2, half1 = (t.n - n0) / 2;                  // columns of B in this CTA
             const int fa = t.f0 + cta * (GLU ? kHalf / 2 : kHalf);            // its first feature
             // A in one box of 128 rows (forward without a gate) or two of 64
             const int boxes_a = GLU ? 2 : kOneBox<OP, GLU> ? fa < p.features
@@ -357,7 +371,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             const int rrow = k4 ? (blocks[t.e] + (t.m0 >> 7)) * groups : 0;
             if (k4) bytes += (1 + scaled) * 2 * kScaleBlock;
             const int b0 = (OP == kBackWeights ? 0 : t.first) + t.m0 + cta * half;
-            const int c0 = t.first + t.m0 + t.n + cta * half1;
+            const int c0 = t.first + t.m0 + n0 + cta * half1;
             for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
                 if (!warp_wait(empty + 8 * ring.stage, ring.phase ^ 1u)) {
                     ok = false;
@@ -394,6 +408,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                             tc::load2_pair(ss + 2 * kScaleBlock, &maps.row_scales, 0, rrow + g, bar);
                             if (scaled > 1)
                                 tc::load2_pair(ss + 4 * kScaleBlock, &maps.row_scales, 0, rrow + groups + g, bar);
+                            if (scaled > 2)
+                                tc::load2_pair(ss + 6 * kScaleBlock, &maps.row_scales, 0, rrow + 2 * groups + g, bar);
                         } else {
                             const uint32_t sc = sb + b.bytes();
                             if (c.rows0 > 0) tc::load2_pair(sc, c.map0, k0, c0, bar);
@@ -431,19 +447,25 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             }
     } else if (warp == 1 && cta == 0) {
         Ring ring;
-        int n = 0;                     // halves of tensor memory taken so far
-        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
+        int n = 0, before = 0;         // tiles so far, columns of the one before
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const bool wide = !across_b && !k4 && t.more > 0;
-            const int bytes_b = wide ? kHalf * kRowBytes : 0;                 // a wide tile's first half is full
-            const uint32_t sums = tmem + (n & 1) * kColumns, sums1 = tmem + ((n & 1) ^ 1) * kColumns;
+            const bool wide = !across_b && !k4 && t.n > kColumns;
+            const int bytes_b = wide ? kHalf * kRowBytes : 0;                 // a wide tile's first product is full
+            // tiles take the low and the high end of tensor memory in turn
+            const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
             // the instruction of the tile and, for a wide one, of its other columns; in 4 bits for either half of a scale word
-            const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0) : tc::instruction_pair(t.n, across_a, across_b);
-            const uint32_t instr1 = k4 ? tc::instruction4_pair(t.n, 1) : tc::instruction_pair(t.more, across_a, across_b);
+            const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0)
+                                      : tc::instruction_pair(min(t.n, kColumns), across_a, across_b);
+            const uint32_t instr1 = k4 ? tc::instruction4_pair(t.n, 1)
+                                       : tc::instruction_pair(max(t.n - kColumns, 16), across_a, across_b);
+            // this end is free when the tile before the last is stored, and what the last one holds of it when its store
+            // half has been there
             ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
-            if (ok && wide)
-                ok = warp_wait(smem_u32(&sh.free[(n + 1) & 1]), (uint32_t)(((n + 1) >> 1) & 1) ^ 1u);
+            if (ok && before + t.n > kTop<OP>)
+                ok = warp_wait(smem_u32(&sh.over[(n + 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
             if (!ok) break;
+            before = t.n;
             tc::fence_after_sync();
             for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
                 if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
@@ -461,10 +483,13 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         tc::copy_scales_pair(tmem + kScalesA + 4 * g, tc::at(tc::kScales, ss + g * kScaleBlock));
-                        tc::copy_scales_pair(tmem + kScalesB + 8 * g, tc::at(tc::kScales, ss + (2 + g) * kScaleBlock));
+                        tc::copy_scales_pair(tmem + kScalesB + 12 * g, tc::at(tc::kScales, ss + (2 + g) * kScaleBlock));
                         if ((t.m0 & 127) + t.n > 128)
-                            tc::copy_scales_pair(tmem + kScalesB + 8 * g + 4,
+                            tc::copy_scales_pair(tmem + kScalesB + 12 * g + 4,
                                                  tc::at(tc::kScales, ss + (4 + g) * kScaleBlock));
+                        if ((t.m0 & 127) + t.n > 256)
+                            tc::copy_scales_pair(tmem + kScalesB + 12 * g + 8,
+                                                 tc::at(tc::kScales, ss + (6 + g) * kScaleBlock));
                     }
                     // a tile that starts in the middle of a scale block starts two columns of 32 rows later
                     const uint32_t sb4 = tmem + kScalesB + ((t.m0 & 127) >> 5);
@@ -472,7 +497,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     for (int k = 0; k < 4; ++k)
                         if (k < count)
                             tc::mma4_pair(sums, da + k * 2, db + k * 2, k & 1 ? instr1 : instr,
-                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 8 * (k >> 1), k0 > 0 || k > 0);
+                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 12 * (k >> 1), k0 > 0 || k > 0);
                     tc::commit_pair(empty + 8 * ring.stage);
                 } else if (!k4 && tc::elect_one()) {
 #pragma unroll
@@ -484,7 +509,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + bytes_b);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < count) tc::mma_pair(sums1, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
+                            if (k < count) tc::mma_pair(sums + kColumns, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
                     }
                     tc::commit_pair(empty + 8 * ring.stage);
                 }
@@ -492,12 +517,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 ring.next(cut);
             }
             if (!ok) break;
-            if (tc::elect_one()) {
-                tc::commit_pair(smem_u32(&sh.done[n & 1]));
-                if (wide) tc::commit_pair(smem_u32(&sh.done[(n + 1) & 1]));
-            }
+            if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.done[n & 1]));
             __syncwarp();
-            n += wide ? 2 : 1;
         }
         // whatever was issued is done before tensor memory is freed
         if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last));
@@ -507,27 +528,32 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
-        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
-            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            for (int m = 0; m < t.rows; m += kColumns, ++n) {
-                // the four warps of a group go on or give up together: they meet at a barrier of their own below
-                const bool got = wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1));
-                int all;
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                             "bar.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                             : "=r"(all) : "r"((int)got), "r"(1 + group) : "memory");
-                if (!all) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after_sync();
-                store_tile<OP, GLU>(a, p, t, t.m0 + m, min(kColumns, t.rows - m),
-                                    tmem + (n & 1) * kColumns + ((uint32_t)(quarter * 32) << 16), mine, cta,
-                                    group, quarter * 32 + lane);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
+        Tile t{};
+        if (pair < p.tiles) t = tile_at<OP, GLU>(a, p, sh, pair);
+        for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
+            // columns that the next tile's sums share with this one's, and with them its first blocks to store
+            const Tile next = tile_at<OP, GLU>(a, p, sh, min(i + pairs, p.tiles - 1));
+            const int shared = i + pairs < p.tiles ? max(t.n + next.n - kTop<OP>, 0) / kTurn : 0;
+            // One warp of a group watches the sums' barrier, the others sleep at the group's own: sixteen watching
+            // warps would take issue slots from the two that feed the tensor core.  A group gives up together.
+            const bool got = ((warp - 2) & 3) != 0 ||
+                             wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1));
+            int all;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all) : "r"((int)got), "r"(1 + group) : "memory");
+            if (!all) {
+                ok = false;
+                break;
             }
+            tc::fence_after_sync();
+            store_tile<OP, GLU>(a, p, t, tmem + (n & 1 ? kTop<OP> - t.n : 0) + ((uint32_t)(quarter * 32) << 16), mine, cta,
+                                group, quarter * 32 + lane, (n & 1) != 0, shared,
+                                tc::in_first(smem_u32(&sh.over[n & 1])));
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
+            t = next;
         }
     }
     if (!ok && lane == 0) atomicOr(&g_expert_faults, MOE_FAULT_WAIT_TIMEOUT);
@@ -536,7 +562,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tc::dealloc_pair(tmem, 2 * kColumns);
+    if (warp == 1) tc::dealloc_pair(tmem, 512);
 }
 
 // The cut of a launch, from the mean rows of an expert (a is all the host knows of them).  A tile that takes all rows of
@@ -552,7 +578,7 @@ Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
     Cut cut{kColumns, 0, 0};
     if (OP == kForward4)
-        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : kColumns4;
+        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 192 ? 192 : 256;
     else if (OP != kBackWeights)
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 256 ? 256 : most <= 320 ? 320 : most <= 448 ? 384 : 256;
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? kScaleBytes : 0);
