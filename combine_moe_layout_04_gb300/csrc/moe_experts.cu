@@ -48,9 +48,12 @@ __device__ unsigned int g_expert_faults;
 
 constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
 constexpr int kGroups = 4;             // of four warps that store
-constexpr int kThreads = 64 + 128 * kGroups;  // warp 0 copies, warp 1 multiplies
+constexpr int kTailWarp = 2 + 4 * kGroups;
+template <int OP>                      // warp 0 copies, warp 1 multiplies; in the weights' gradient one more clears
+constexpr int kThreads = 32 * (kTailWarp + (OP == kBackWeights ? 1 : 0));
 constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // most columns of one product instruction
+constexpr int kFirst = 128;            // a wider tile is two products: this many columns, and the others
 template <int OP>
 constexpr int kTop = OP == kForward4 ? 448 : 512;  // columns of tensor memory for sums
 constexpr int kRowBytes = 128;         // of a stage, along memory
@@ -73,7 +76,7 @@ constexpr int kScaleBlock = 512, kScaleBytes = 4 * 2 * kScaleBlock;
 constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail;
+    uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
     uint32_t tmem;
     int scratch[32];
     int base[MOE_MAX_EXPERTS + 1];
@@ -303,7 +306,7 @@ constexpr bool kOneBox = (OP == kForward || OP == kForward4) && !GLU;
 
 // The weights (the rows, in the weights' gradient) come through map_a, the other operand through maps.
 template <int OP, bool GLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
     constexpr bool k4 = OP == kForward4, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
@@ -321,6 +324,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int i = 0; i < cut.stages; ++i) {
             mbar_init(full + 8 * i, 2);   // both CTAs' copies arrive on the first CTA's
             mbar_init(empty + 8 * i, 1);
+            mbar_init(smem_u32(&sh.tail[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.done[i]), 1);
@@ -328,7 +332,6 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups);
         }
         mbar_init(smem_u32(&sh.last), 1);
-        mbar_init(smem_u32(&sh.tail), 1);
         fence_mbar_init();
     }
     if (warp == 0 && lane < (across_b ? 1 : kMaps)) tc::prefetch_map(&maps.rows[lane]);
@@ -349,12 +352,11 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     bool ok = true;
     if (warp == 0) {
         const uint32_t full0 = tc::in_first(full);
-        uint32_t tails = 0;
         Ring ring;
         int flying = 0;                // stages issued, up to all of them
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const int n0 = min(t.n, kColumns);                                // columns of the first product, others
+            const int n0 = t.n > kColumns ? kFirst : t.n;                     // columns of the first product, others
             const int half = n0 / 2, half1 = (t.n - n0) / 2;                  // columns of B in this CTA
             const int fa = t.f0 + cta * (GLU ? kHalf / 2 : kHalf);            // its first feature
             // A in one box of 128 rows (forward without a gate) or two of 64
@@ -379,10 +381,10 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 }
                 const uint32_t sa = stages + ring.at, sb = sa + kBytesA;
                 const int left = t.length - k0;
-                // rows past the expert's last that would be summed: this CTA waits for the stage itself and clears them
+                // rows past the expert's last that would be summed: the tail warp gets the stage first
                 const bool clear = OP == kBackWeights && left < kStep<OP> && (left & 15) != 0;
                 if (tc::elect_one()) {
-                    const uint32_t bar = clear ? smem_u32(&sh.tail) : full0 + 8 * ring.stage;
+                    const uint32_t bar = clear ? smem_u32(&sh.tail[ring.stage]) : full0 + 8 * ring.stage;
                     tc::arrive_expect_cluster(bar, bytes);
                     if (OP == kBackWeights) {
                         if (boxes_a > 0) tc::load2_pair(sa, &map_a, fa, t.first + k0, bar);
@@ -418,20 +420,6 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     }
                 }
                 __syncwarp();
-                if (clear) {
-                    if (!warp_wait(smem_u32(&sh.tail), tails++ & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const int from = left * 8, to = ((left + 15) & ~15) * 8;  // 16-byte pieces of a box
-                    for (int k = 0; k < cut.bytes / kBoxBytes; ++k)
-                        for (int j = from + lane; j < to; j += 32)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
-                                         :: "r"(sa + k * kBoxBytes + j * 16), "r"(0u) : "memory");
-                    asm volatile("fence.proxy.async;" ::: "memory");  // also for the first CTA's products
-                    __syncwarp();
-                    if (lane == 0) tc::arrive_cluster(full0 + 8 * ring.stage);
-                }
                 ring.next(cut);
                 flying = min(flying + 1, cut.stages);
             }
@@ -451,14 +439,13 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const bool wide = !across_b && !k4 && t.n > kColumns;
-            const int bytes_b = wide ? kHalf * kRowBytes : 0;                 // a wide tile's first product is full
-            // tiles take the low and the high end of tensor memory in turn
+                        // tiles take the low and the high end of tensor memory in turn
             const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
             // the instruction of the tile and, for a wide one, of its other columns; in 4 bits for either half of a scale word
             const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0)
-                                      : tc::instruction_pair(min(t.n, kColumns), across_a, across_b);
+                                      : tc::instruction_pair(wide ? kFirst : t.n, across_a, across_b);
             const uint32_t instr1 = k4 ? tc::instruction4_pair(t.n, 1)
-                                       : tc::instruction_pair(max(t.n - kColumns, 16), across_a, across_b);
+                                       : tc::instruction_pair(max(t.n - kFirst, 16), across_a, across_b);
             // this end is free when the tile before the last is stored, and what the last one holds of it when its store
             // half has been there
             ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
@@ -506,10 +493,10 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                             tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
                                          k0 > 0 || k > 0);
                     if (wide) {
-                        const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + bytes_b);
+                        const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < count) tc::mma_pair(sums + kColumns, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
+                            if (k < count) tc::mma_pair(sums + kFirst, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
                     }
                     tc::commit_pair(empty + 8 * ring.stage);
                 }
@@ -524,7 +511,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last));
         __syncwarp();
         ok = warp_wait(smem_u32(&sh.last), 0) && ok;
-    } else if (warp >= 2) {
+    } else if (warp >= 2 && warp < kTailWarp) {
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
@@ -556,6 +543,36 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             t = next;
         }
     }
+    if (OP == kBackWeights && warp == kTailWarp) {
+        // Clears the rows past an expert's last in its last stage, in this CTA, and hands the stage on.  The copying warp
+        // does not wait for it: doing so there cost a memory latency a tile (1024 rows of 32 experts spread by routing,
+        // 2048 x 7168: 660 us against 604 us).
+        const uint32_t full0 = tc::in_first(full);
+        uint32_t phases = 0;           // of the tail barriers, a bit each
+        int stage = 0;
+        for (int64_t i = pair; i < p.tiles; i += pairs) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            const int steps = (t.length + kStep<OP> - 1) / kStep<OP>;
+            if ((t.length & 15) != 0) {
+                const int at = (stage + steps - 1) % cut.stages;
+                if (!warp_wait(smem_u32(&sh.tail[at]), (phases >> at) & 1)) {
+                    ok = false;
+                    break;
+                }
+                phases ^= 1u << at;
+                const int left = t.length - (steps - 1) * kStep<OP>;
+                const int from = left * 8, to = ((left + 15) & ~15) * 8;      // 16-byte pieces of a box
+                for (int k = 0; k < cut.bytes / kBoxBytes; ++k)
+                    for (int j = from + lane; j < to; j += 32)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                                     :: "r"(stages + at * cut.bytes + k * kBoxBytes + j * 16), "r"(0u) : "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");              // also for the first CTA's products
+                __syncwarp();
+                if (lane == 0) tc::arrive_cluster(full0 + 8 * at);
+            }
+            stage = (stage + steps) % cut.stages;
+        }
+    }
     if (!ok && lane == 0) atomicOr(&g_expert_faults, MOE_FAULT_WAIT_TIMEOUT);
     __syncwarp();
     tc::fence_before_sync();
@@ -565,22 +582,25 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     if (warp == 1) tc::dealloc_pair(tmem, 512);
 }
 
-// The cut of a launch, from the mean rows of an expert (a is all the host knows of them).  A tile that takes all rows of
-// its expert reads the weights once, and the narrower it is the more stages are in flight: 2 rows an expert (64 experts,
-// 7168 -> 2 x 2048) take 528 us with 64 columns, 548 with 256, 588 with 512; 128 rows take 677 us cut at 64 columns and
-// 582 us cut at 256.  Up to 256 columns one tile's sums are written while the next is computed.  A wide tile (both
-// halves of tensor memory) gives that up and still wins where it saves a second tile: 272 rows take 718 us cut at 320
-// columns and 854 us cut at 256, 360 rows (32 experts) 421 us at 384 and 474 us at 256; but 1040 rows, which four wide
-// tiles or five narrow ones hold, take 658 us cut at 320 and 582 us cut at 256 (2048 <- 7168, 32 experts).  Routing
-// spreads an expert's rows by about the square root of their mean; 3.5 of that hold almost all experts.
+// The cut of a launch, from the mean rows of an expert (all the host knows of them); routing spreads an expert's rows by
+// about the square root of their mean, and 3.5 of that hold almost all experts.
+//  * A tile that takes all rows of its expert reads the weights once, and the narrower it is the more stages are in
+//    flight: 2 rows an expert (64 experts, 7168 -> 2 x 2048) take 528 us with 64 columns, 548 with 256, 588 with 512; but
+//    128 rows take 677 us cut at 64 columns and 582 us cut at 256.
+//  * Tiles of more than 256 columns win where they save one: 272 rows take 682 us cut at 320 and 858 us cut at 256, 360
+//    rows (32 experts) 421 us at 384 and 478 at 256, 600 rows (7168 -> 2048) 333 us at 320 and 387 at 256.
+//  * Many tiles an expert waste little of either, and 256 columns issue fewer instructions: 3000 rows (8 experts) take
+//    388 us at 256 and 406 at 320; 1040 rows 594 and 600.
+//  * In 4 bits (tensor memory also holds scales: 256 columns at most) 100 rows take 169 us at 128 columns and 185 at 256;
+//    256 rows 212 us at 256 and 245 at 128; 1024 rows (32 experts) 331 us at 256 and 402 at 192.
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
     Cut cut{kColumns, 0, 0};
-    if (OP == kForward4)
-        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 192 ? 192 : 256;
-    else if (OP != kBackWeights)
-        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : most <= 256 ? 256 : most <= 320 ? 320 : most <= 448 ? 384 : 256;
+    if (OP != kBackWeights) {
+        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
+        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 420 ? 384 : 320;
+    }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? kScaleBytes : 0);
     cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
     return cut;
@@ -616,7 +636,7 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads, kSmem<OP>, s>>>(a, cut, ma, mb);
+    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads<OP>, kSmem<OP>, s>>>(a, cut, ma, mb);
     return cudaGetLastError();
 }
 
