@@ -31,6 +31,8 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
     __shared__ float part[kWarps][kSlots];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int j0 = 0; j0 < k; j0 += kSlots) {
         int64_t row[kSlots];
         float w[kSlots], acc[kSlots];
@@ -86,10 +88,9 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
 
 cudaError_t launch_combine_backward(const int32_t* pos, int T, int k, int h, const void* dout, const void* y,
                                     const float* weights, void* dy, float* dweights, cudaStream_t s) {
-    combine_backward_kernel<<<T, kThreads, 0, s>>>(pos, k, h / 8, T * k, static_cast<const uint4*>(dout),
-                                                   static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
-                                                   dweights);
-    return cudaGetLastError();
+    return launch_pdl(combine_backward_kernel, dim3(T), dim3(kThreads), 0, s, pos, k, h / 8, T * k,
+                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
+                      dweights);
 }
 
 }  // namespace moe

@@ -338,6 +338,9 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     if (warp == 0 && lane == kMaps) tc::prefetch_map(&map_a);
     if (k4 && warp == 0 && lane >= 8 && lane < 10) tc::prefetch_map(lane == 8 ? &maps.weight_scales : &maps.row_scales);
     if (warp == 1) tc::alloc_pair(smem_u32(&sh.tmem), 512);
+    // the kernel before may still be running until here
+    pdl_wait();
+    pdl_launch_dependents();
     scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch,
                     [&](int rows) { return (rows + cut.columns - 1) / cut.columns; }, sh.rows);
     if (k4) scan_row_blocks(a.count, a.offset, a.E, a.R, blocks, sh.scratch, blocks_of_128);
@@ -636,8 +639,8 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    kern<<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kThreads<OP>, kSmem<OP>, s>>>(a, cut, ma, mb);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kThreads<OP>), kSmem<OP>, s, a, cut, ma,
+                      mb);
 }
 
 }  // namespace

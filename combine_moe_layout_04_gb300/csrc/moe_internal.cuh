@@ -375,7 +375,9 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
 }
 
 // Programmatic dependent launch: let the next kernel in the stream start its
-// prologue, and wait for the previous kernel's results.
+// prologue, and wait for the previous kernel's results.  A kernel waits first and
+// lets the next one start then: what runs two kernels on before its own wait
+// still finds this kernel's predecessors complete.
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

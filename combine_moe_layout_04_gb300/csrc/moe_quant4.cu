@@ -76,6 +76,8 @@ __device__ __forceinline__ void quantise_piece(const void* row, uint8_t* codes, 
 __global__ void __launch_bounds__(kThreads)
 quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     __shared__ int base[MOE_MAX_EXPERTS + 1], scratch[32];
+    pdl_wait();
+    pdl_launch_dependents();
     scan_row_blocks(a.count, a.offset, a.E, a.R, base, scratch, blocks_of_128);
     const int block = blockIdx.x;
     if (block >= base[a.E]) return;
@@ -97,6 +99,8 @@ quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
 // activation the scale block holds 64 gate rows and then their 64 up rows.
 __global__ void __launch_bounds__(kThreads)
 quant4_weights_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
+    pdl_wait();
+    pdl_launch_dependents();
     const int per = a.glu ? 64 : 128;
     const int blocks = (a.N + per - 1) / per;
     const int64_t e = blockIdx.x / blocks;
@@ -117,15 +121,13 @@ quant4_weights_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
 
 cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s) {
     const dim3 grid((unsigned)(a.R / 128 + min(a.E, a.R)), (unsigned)((a.K + kPiece - 1) / kPiece));
-    quant4_rows_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
-    return cudaGetLastError();
+    return launch_pdl(quant4_rows_kernel, grid, dim3(kThreads), 0, s, a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
 cudaError_t launch_quant4_weights(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s) {
     const int per = a.glu ? 64 : 128;
     const dim3 grid((unsigned)((int64_t)a.E * ((a.N + per - 1) / per)), (unsigned)((a.K + kPiece - 1) / kPiece));
-    quant4_weights_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
-    return cudaGetLastError();
+    return launch_pdl(quant4_weights_kernel, grid, dim3(kThreads), 0, s, a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
 }  // namespace moe

@@ -99,6 +99,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
     if (t >= a.T) return;
     const int E = a.E;
     float l[V];
@@ -148,6 +150,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
     if (t >= a.T) return;
     const int E = a.E;
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
@@ -198,24 +202,22 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
 }
 
 template <typename T, int V>
-void launch(const RouteArgs& a, bool back, cudaStream_t s) {
+cudaError_t launch(const RouteArgs& a, bool back, cudaStream_t s) {
     constexpr int per = kRouteThreads / 32;
     const dim3 grid((unsigned)((a.T + (int64_t)per - 1) / per));
-    if (back) route_backward_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
-    else route_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
+    return launch_pdl(back ? route_backward_kernel<T, V> : route_kernel<T, V>, grid, dim3(kRouteThreads), 0, s, a);
 }
 
 // The registers a lane needs grow with E (at most 1024): powers of two keep
 // the unused ones below the used ones.
 template <typename T>
 cudaError_t pick(const RouteArgs& a, bool back, cudaStream_t s) {
-    if (a.E <= 32) launch<T, 1>(a, back, s);
-    else if (a.E <= 64) launch<T, 2>(a, back, s);
-    else if (a.E <= 128) launch<T, 4>(a, back, s);
-    else if (a.E <= 256) launch<T, 8>(a, back, s);
-    else if (a.E <= 512) launch<T, 16>(a, back, s);
-    else launch<T, 32>(a, back, s);
-    return cudaGetLastError();
+    if (a.E <= 32) return launch<T, 1>(a, back, s);
+    if (a.E <= 64) return launch<T, 2>(a, back, s);
+    if (a.E <= 128) return launch<T, 4>(a, back, s);
+    if (a.E <= 256) return launch<T, 8>(a, back, s);
+    if (a.E <= 512) return launch<T, 16>(a, back, s);
+    return launch<T, 32>(a, back, s);
 }
 
 }  // namespace
