@@ -31,6 +31,10 @@
 // neighbours that a copy reaches into only make sums that nobody stores; where
 // rows are summed (weights' gradient) they are cleared in shared memory first.
 //
+// Few tiles and a long contraction: two or four pairs of a cluster share a tile,
+// each over its part of the contraction, and its CTAs' store halves add the parts up
+// through distributed shared memory, in part order.
+//
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
 
@@ -77,6 +81,7 @@ constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
+    uint64_t ready[kGroups], seen[kGroups];  // of a store group's block, by the parts of a tile
     uint32_t tmem;
     int scratch[32];
     int base[MOE_MAX_EXPERTS + 1];
@@ -85,9 +90,10 @@ struct Shared {
 
 // How a launch cuts rows and shared memory: a tile has at most `columns` columns,
 // and shared memory holds `stages` stages of `bytes` (16 KB of one operand and
-// half the columns of the other).
+// half the columns of the other); `parts` pairs share a tile.
 struct Cut {
     int columns, stages, bytes;
+    int parts;                         // pairs that share a tile
 };
 
 // Where in the ring of stages a thread is.
@@ -217,14 +223,40 @@ __device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]
 }
 // The 128 threads of a store group (barriers 1 and up).
 __device__ __forceinline__ void store_sync(int group) { asm volatile("bar.sync %0, 128;" :: "r"(1 + group) : "memory"); }
+// The same, and whether all of them say yes.
+__device__ __forceinline__ bool store_all(int group, bool yes) {
+    int all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                 "bar.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"((int)yes), "r"(1 + group) : "memory");
+    return all != 0;
+}
+// How the store groups of a tile's parts meet, a group with the same one of every other part.
+struct Link {
+    uint32_t ready, seen;              // barriers of this store group
+    uint32_t phase;                    // of both
+    int part, parts, cta;
+    bool ok, empty;                    // empty: this part has no stage of the tile
+};
+// 8 floats of a turned row, added up over the parts of the tile in their order.
+__device__ __forceinline__ void summed8(const float* p, const Link& link, float (&v)[8]) {
+    const uint32_t at = smem_u32(p);
+    for (int i = 0; i < link.parts; ++i) {
+        const uint32_t there = tc::in_rank(at, 2 * i + link.cta);
+        const float4 a = tc::load_cluster(there), b = tc::load_cluster(there + 16);
+        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i == 0 ? w[k] : v[k] + w[k];
+    }
+}
 
 // A finished tile to its results: the store groups take blocks of 16 columns of the sums in turn, each through its own
 // block of shared memory, and fetch the next one while they write.  sums: tensor memory of this warp's lanes; cta: which
-// half of the features; tid: of 128.  up: from the first column to the last, else the other way; after `shared` blocks
+// half of the features; tid: of 128; link: how the parts of a tile meet (SPLIT).  up: from the first column to the last, else the other way; after `shared` blocks
 // (the columns the next tile's sums take over) this warp arrives on the barrier `over`.
-template <int OP, bool GLU>
+template <int OP, bool GLU, bool SPLIT>
 __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
-                                           int cta, int group, int tid, bool up, int shared, uint32_t over) {
+                                           int cta, int group, int tid, bool up, int shared, uint32_t over, Link& link) {
     constexpr int kMine = GLU ? kHalf / 2 : kHalf;      // features of this CTA
     constexpr int kEights = kMine / 8, kAtOnce = 128 / kEights;
     const int f = t.f0 + cta * kMine + (tid % kEights) * 8;
@@ -249,26 +281,40 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         const int c = column(b);
         if (!told && b >= shared) tell();
         tc::wait_ld();
-        if (OP == kBackWeights && t.length == 0) {
+        if (SPLIT ? link.empty : OP == kBackWeights && t.length == 0) {
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) v[i] = 0;
+        }
+        if (SPLIT) {
+            // the block before has been read by all parts
+            if (tid == 0 && !within_second([&] { return tc::try_wait_cluster(link.seen, link.phase ^ 1u); })) link.ok = false;
         }
         store_sync(group);  // the block before has been read
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
         store_sync(group);
+        if (SPLIT) {
+            if (tid < link.parts)
+                tc::arrive_release_cluster(tc::in_rank(link.ready, 2 * tid + link.cta));
+            if (tid == 0 && !within_second([&] { return tc::try_wait_cluster(link.ready, link.phase); })) link.ok = false;
+            link.ok = store_all(group, link.ok);
+            if (!link.ok) break;
+            link.phase ^= 1u;
+        }
         if (b + kGroups < count) tc::ld16(sums + column(b + kGroups), v);
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
-            if (!live || c + row >= t.rows) continue;
+            if (!live || c + row >= t.rows || (SPLIT && row % link.parts != link.part)) continue;
             const float* from = turn + row * kTurnPitch + (tid % kEights) * 8;
             float x[8];
-            turned8(from, swap, x);
+            if (SPLIT) summed8(from, link, x);
+            else turned8(from, swap, x);
             const int64_t at = (c + row) * pitch;
             if (GLU) {
                 float u[8];
-                turned8(from + kHalf / 2, swap, u);
+                if (SPLIT) summed8(from + kHalf / 2, link, u);
+                else turned8(from + kHalf / 2, swap, u);
                 if (a.pre != nullptr) {
                     __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(a.pre) + (r0 + c + row) * a.W + f;
                     store8(pre, x);
@@ -294,6 +340,10 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
                 store8(out + at, x);
             }
         }
+        if (SPLIT) {
+            store_sync(group);
+            if (tid < link.parts) tc::arrive_cluster(tc::in_rank(link.seen, 2 * tid + link.cta));
+        }
     }
     if (!told) tell();
 }
@@ -305,8 +355,8 @@ template <int OP, bool GLU>
 constexpr bool kOneBox = (OP == kForward || OP == kForward4) && !GLU;
 
 // The weights (the rows, in the weights' gradient) come through map_a, the other operand through maps.
-template <int OP, bool GLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<OP>, 1)
+template <int OP, bool GLU, bool SPLIT>
+__global__ void __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
     constexpr bool k4 = OP == kForward4, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
@@ -317,7 +367,9 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes<OP>);
     int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + kGroups * kTurnBytes);  // [E + 1], in 4 bits
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cta = (int)tc::cta_of_pair();
+    const int rank = (int)tc::rank_in_cluster(), cta = rank & 1, lead = rank & ~1;
+    const uint16_t both = (uint16_t)(3u << lead);
+    const int parts = SPLIT ? cut.parts : 1, part = SPLIT ? rank >> 1 : 0;
     const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
 
     if (threadIdx.x == 0) {
@@ -331,6 +383,11 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             mbar_init(smem_u32(&sh.free[i]), 2 * 4 * kGroups);
             mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups);
         }
+        if (SPLIT)
+            for (int i = 0; i < kGroups; ++i) {
+                mbar_init(smem_u32(&sh.ready[i]), parts);
+                mbar_init(smem_u32(&sh.seen[i]), parts);
+            }
         mbar_init(smem_u32(&sh.last), 1);
         fence_mbar_init();
     }
@@ -350,11 +407,19 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const Plan p = make_plan<OP, GLU>(a, sh.base);
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // the pairs (or the parts of a tile together) and the stages of this part
+    const int64_t pair = (blockIdx.x >> 1) / parts, pairs = (gridDim.x >> 1) / parts;
+    auto begin_of = [&](const Tile& t) {
+        return SPLIT ? (int)((int64_t)((t.length + kStep<OP> - 1) / kStep<OP>) * part / parts) * kStep<OP> : 0;
+    };
+    auto end_of = [&](const Tile& t) {
+        if (!SPLIT) return t.length;
+        return min(t.length, (int)((int64_t)((t.length + kStep<OP> - 1) / kStep<OP>) * (part + 1) / parts) * kStep<OP>);
+    };
 
     bool ok = true;
     if (warp == 0) {
-        const uint32_t full0 = tc::in_first(full);
+        const uint32_t full0 = tc::in_rank(full, lead);
         Ring ring;
         int flying = 0;                // stages issued, up to all of them
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
@@ -377,7 +442,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             if (k4) bytes += (1 + scaled) * 2 * kScaleBlock;
             const int b0 = (OP == kBackWeights ? 0 : t.first) + t.m0 + cta * half;
             const int c0 = t.first + t.m0 + n0 + cta * half1;
-            for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
+            const int end = end_of(t);
+            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>) {
                 if (!warp_wait(empty + 8 * ring.stage, ring.phase ^ 1u)) {
                     ok = false;
                     break;
@@ -457,7 +523,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             if (!ok) break;
             before = t.n;
             tc::fence_after_sync();
-            for (int k0 = 0; k0 < t.length; k0 += kStep<OP>) {
+            const int begin = begin_of(t), end = end_of(t);
+            for (int k0 = begin; k0 < end; k0 += kStep<OP>) {
                 if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
                     ok = false;
                     break;
@@ -487,37 +554,38 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     for (int k = 0; k < 4; ++k)
                         if (k < count)
                             tc::mma4_pair(sums, da + k * 2, db + k * 2, k & 1 ? instr1 : instr,
-                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 12 * (k >> 1), k0 > 0 || k > 0);
-                    tc::commit_pair(empty + 8 * ring.stage);
+                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 12 * (k >> 1), k0 > begin || k > 0);
+                    tc::commit_pair(empty + 8 * ring.stage, both);
                 } else if (!k4 && tc::elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (k < count)
                             tc::mma_pair(sums, da + k * (across_a ? 128 : 2), db + k * (across_b ? 128 : 2), instr,
-                                         k0 > 0 || k > 0);
+                                         k0 > begin || k > 0);
                     if (wide) {
                         const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < count) tc::mma_pair(sums + kFirst, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > 0 || k > 0);
+                            if (k < count) tc::mma_pair(sums + kFirst, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > begin || k > 0);
                     }
-                    tc::commit_pair(empty + 8 * ring.stage);
+                    tc::commit_pair(empty + 8 * ring.stage, both);
                 }
                 __syncwarp();
                 ring.next(cut);
             }
             if (!ok) break;
-            if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.done[n & 1]));
+            if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.done[n & 1]), both);
             __syncwarp();
         }
         // whatever was issued is done before tensor memory is freed
-        if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last));
+        if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last), both);
         __syncwarp();
         ok = warp_wait(smem_u32(&sh.last), 0) && ok;
     } else if (warp >= 2 && warp < kTailWarp) {
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
+        Link link{smem_u32(&sh.ready[group]), smem_u32(&sh.seen[group]), 0, part, parts, cta, true, false};
         Tile t{};
         if (pair < p.tiles) t = tile_at<OP, GLU>(a, p, sh, pair);
         for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
@@ -528,21 +596,22 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             // warps would take issue slots from the two that feed the tensor core.  A group gives up together.
             const bool got = ((warp - 2) & 3) != 0 ||
                              wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1));
-            int all;
-            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                         "bar.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                         : "=r"(all) : "r"((int)got), "r"(1 + group) : "memory");
-            if (!all) {
+            if (!store_all(group, got)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            store_tile<OP, GLU>(a, p, t, tmem + (n & 1 ? kTop<OP> - t.n : 0) + ((uint32_t)(quarter * 32) << 16), mine, cta,
+            if (SPLIT) link.empty = begin_of(t) >= end_of(t);
+            store_tile<OP, GLU, SPLIT>(a, p, t, tmem + (n & 1 ? kTop<OP> - t.n : 0) + ((uint32_t)(quarter * 32) << 16), mine, cta,
                                 group, quarter * 32 + lane, (n & 1) != 0, shared,
-                                tc::in_first(smem_u32(&sh.over[n & 1])));
+                                tc::in_rank(smem_u32(&sh.over[n & 1]), lead), link);
+            if (SPLIT && !link.ok) {
+                ok = false;
+                break;
+            }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::arrive_cluster(tc::in_first(smem_u32(&sh.free[n & 1])));
+            if (lane == 0) tc::arrive_cluster(tc::in_rank(smem_u32(&sh.free[n & 1]), lead));
             t = next;
         }
     }
@@ -550,7 +619,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         // Clears the rows past an expert's last in its last stage, in this CTA, and hands the stage on.  The copying warp
         // does not wait for it: doing so there cost a memory latency a tile (1024 rows of 32 experts spread by routing,
         // 2048 x 7168: 660 us against 604 us).
-        const uint32_t full0 = tc::in_first(full);
+        const uint32_t full0 = tc::in_rank(full, lead);
         uint32_t phases = 0;           // of the tail barriers, a bit each
         int stage = 0;
         for (int64_t i = pair; i < p.tiles; i += pairs) {
@@ -599,14 +668,78 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
-    Cut cut{kColumns, 0, 0};
+    Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
-        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 420 ? 384 : 320;
+        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 365 ? 384 : 320;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? kScaleBytes : 0);
     cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
     return cut;
+}
+
+// Clusters of this many pairs of CTAs that the current device runs at once (a cluster's CTAs share a processing cluster
+// of the GPU: GB300 holds 76, 36 and 15 of 1, 2 and 4 pairs, not 76, 38 and 19).
+template <typename K>
+int clusters(K* kern, int threads, int smem, int pairs) {
+    static std::mutex mu;
+    static std::unordered_map<int, int> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[4 * dev + pairs / 2];
+    if (n == 0) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2 * pairs;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * pairs);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = 1;
+    }
+    return n;
+}
+
+// Pairs that share a tile: the fewest rounds of tiles times stages of a round.  Sharing costs a round about as long as 14
+// stages (two meetings of the parts per 16 columns): one row of one expert, 7168 -> 2 x 1024 (8 tiles of 112 stages), takes
+// 17.4 us in four parts and 31.6 us in one; the same in 4 bits (28 stages) 15.2 us either way.
+template <typename K>
+int parts_of(K* split, int threads, int smem, int64_t tiles, int steps, int64_t pairs) {
+    int best = 1;
+    int64_t least = (tiles + pairs - 1) / pairs * steps;
+    for (int parts = 2; parts <= 4 && steps > 28; parts *= 2) {
+        const int64_t teams = clusters(split, threads, smem, parts);
+        const int64_t cost = (tiles + teams - 1) / teams * ((steps + parts - 1) / parts + 14);
+        if (cost < least) {
+            least = cost;
+            best = parts;
+        }
+    }
+    return best;
+}
+
+// Launches a pair kernel in clusters of cut.parts pairs, under programmatic dependent launch.
+template <int OP, typename K>
+cudaError_t start(K* kern, const ExpertArgs& a, const Cut& cut, int64_t tiles, int64_t teams, const CUtensorMap& ma,
+                  const Maps& mb, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * cut.parts * (tiles < teams ? tiles : teams)));
+    cfg.blockDim = dim3(kThreads<OP>);
+    cfg.dynamicSmemBytes = kSmem<OP>;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * cut.parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, cut, ma, mb);
 }
 
 template <int OP, bool GLU>
@@ -629,18 +762,26 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
                                     0, 8 << i);
     }
     if (!ok) return cudaErrorInvalidValue;
-    auto* kern = pair_kernel<OP, GLU>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem<OP>);
-    if (e != cudaSuccess) return e;
-    const Cut cut = make_cut<OP>(a);
+    Cut cut = make_cut<OP>(a);
     // no more pairs than there can be tiles
     const int64_t features = OP == kForward || OP == kForward4 ? a.N : a.K, wide = GLU ? kHalf : 2 * kHalf;
     const int64_t across = (features + wide - 1) / wide;
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.W + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    return launch_pdl(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kThreads<OP>), kSmem<OP>, s, a, cut, ma,
-                      mb);
+    auto* whole = pair_kernel<OP, GLU, false>;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(whole), kSmem<OP>);
+    if (e != cudaSuccess) return e;
+    if constexpr (OP != kBackWeights) {
+        auto* split = pair_kernel<OP, GLU, true>;
+        e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
+        if (e != cudaSuccess) return e;
+        const int steps = ((OP == kBackRows ? a.W : a.K) + kStep<OP> - 1) / kStep<OP>;
+        cut.parts = parts_of(split, kThreads<OP>, kSmem<OP>, tiles, steps, pairs);
+        if (cut.parts > 1)
+            return start<OP>(split, a, cut, tiles, clusters(split, kThreads<OP>, kSmem<OP>, cut.parts), ma, mb, s);
+    }
+    return start<OP>(whole, a, cut, tiles, pairs, ma, mb, s);
 }
 
 }  // namespace

@@ -74,10 +74,11 @@ __device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
 __device__ __forceinline__ void dealloc_pair(uint32_t at, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(at), "r"(cols) : "memory");
 }
-// Arrives on the barrier at this address in both CTAs when every tensor-core operation this thread issued before is done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+// Arrives on the barrier at this address in both CTAs (a bit of `ctas` each) when every tensor-core operation this thread
+// issued before is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t ctas) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(bar), "h"((uint16_t)3) : "memory");
+                 :: "r"(bar), "h"(ctas) : "memory");
 }
 // Instruction descriptor of a bf16 product with fp32 sums: 256 rows, n columns (a multiple of 16).
 __host__ __device__ constexpr uint32_t instruction_pair(int n, bool a_across, bool b_across) {
@@ -116,16 +117,31 @@ __device__ __forceinline__ void load3_pair(uint32_t dst, const CUtensorMap* map,
     asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t cta_of_pair() {
+__device__ __forceinline__ uint32_t rank_in_cluster() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// The address in the first CTA of what lies at `local` in this one.
-__device__ __forceinline__ uint32_t in_first(uint32_t local) {
+// The address in the cluster's CTA `rank` of what lies at `local` in this one.
+__device__ __forceinline__ uint32_t in_rank(uint32_t local, uint32_t rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
+}
+__device__ __forceinline__ float4 load_cluster(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// Arrival that other CTAs of the cluster take as a sign that this CTA's earlier writes are there, and the wait for it.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");

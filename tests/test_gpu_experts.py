@@ -83,6 +83,25 @@ def test_forward_many_rows(moe, act):
     _check_forward(lay, *_forward(moe, prob, lay, 2048, 776, act), act)
 
 
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 1], [5, 64, 0, 65], [17] * 8, [1] * 20])
+@pytest.mark.parametrize("K", [768, 2056, 7168])
+def test_few_tiles_and_long_sums(moe, counts, K):
+    """Contractions that are cut into parts because there are few tiles, every way round."""
+    prob, lay = layout_of_counts(moe, counts)
+    for act, N in ((True, 72), (False, 520)):
+        _check_forward(lay, *_forward(moe, prob, lay, K, N, act), act)
+    weights, dout, rows, pre, drows, dw = _backward(moe, prob, lay, 136, K, False, True)
+    _check_rows(lay, weights, dout, pre, drows)
+    _check_weights(lay, rows, dout, dw)
+    again = _backward(moe, prob, lay, 136, K, False, True)
+    assert (drows.view(torch_uint16()) == again[4].view(torch_uint16())).all()
+
+
+def torch_uint16():
+    import torch
+    return torch.int16
+
+
 def test_forward_top_k_and_placement(moe):
     """Top-8 of 64 experts on 8 ranks out of order: offsets do not ascend with the expert."""
     rng = np.random.default_rng(3)

@@ -139,6 +139,19 @@ def test_product(moe, counts, K, N, act):
         close(out, ref, slack)
 
 
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 130], [17] * 8])
+@pytest.mark.parametrize("K,N,act", [(8224, 72, True), (10272, 264, False), (4128, 136, True)])
+def test_product_of_few_tiles(moe, counts, K, N, act):
+    """Contractions that are cut into parts because there are few tiles."""
+    prob, lay = layout_of_counts(moe, counts)
+    rows = randn((sum(counts), K), 5)
+    weights = randn((len(counts), 2 * N if act else N, K), 6, K ** -0.5)
+    out, pre, values, wv = _product(moe, prob, lay, K, N, act, rows, weights)
+    ref, mag = products(lay, values, wv)
+    slack = sum_slack(mag, K)
+    close(out, gated(ref) if act else ref, gated_slack(ref, slack) if act else slack)
+
+
 def test_product_wide_scales(moe):
     """Scales far from one, a different one for every block: 2^-40 .. 2^40 on rows and weights."""
     import torch
