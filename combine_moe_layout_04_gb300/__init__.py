@@ -553,10 +553,16 @@ def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy,
     p, where = problem, "moe_combine_backward"
     slots = p.num_tokens * p.topk
     _check(load_library().moe_combine_backward(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take(where, dout, "bfloat16", p.num_tokens, p.hidden),
+        ctypes.byref(p.c()), ctypes.byref(_LayoutC(pos=layout.pos.data_ptr())),
+        _take(where, dout, "bfloat16", p.num_tokens, p.hidden),
         _take(where, y, "bfloat16", slots, p.hidden), _take(where, weights, "float32", p.num_tokens, p.topk),
         _take(where, dy, "bfloat16", slots, p.hidden), _take(where, dweights, "float32", p.num_tokens, p.topk),
         _stream(stream)), where)
+
+
+def _groups(layout) -> _LayoutC:
+    """The two layout arrays that the experts' calls read (the struct's first two fields)."""
+    return _LayoutC(layout.expert_count.data_ptr(), layout.expert_offset.data_ptr())
 
 
 def _take_weights(where: str, p: Problem, x: Experts):
@@ -570,7 +576,7 @@ def moe_expert_forward(problem: Problem, layout: Layout, experts: Experts, rows,
     p, x, where = problem, experts, "moe_expert_forward"
     slots = p.num_tokens * p.topk
     _check(load_library().moe_expert_forward(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take_weights(where, p, x),
+        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, pre, "bfloat16", slots, x.weight_rows),
         _take(where, out, "bfloat16", slots, x.out_cols), _stream(stream)), where)
 
@@ -581,7 +587,7 @@ def moe_expert_backward_rows(problem: Problem, layout: Layout, experts: Experts,
     p, x, where = problem, experts, "moe_expert_backward_rows"
     slots, wide = p.num_tokens * p.topk, x.in_cols * (1 if pre is None else 2)
     _check(load_library().moe_expert_backward_rows(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), _take_weights(where, p, x),
+        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
         _take(where, dout, "bfloat16", slots, x.weight_rows), _take(where, pre, "bfloat16", slots, wide),
         _take(where, drows, "bfloat16", slots, wide), _stream(stream)), where)
 
@@ -591,7 +597,7 @@ def moe_expert_backward_weights(problem: Problem, layout: Layout, experts: Exper
     p, x, where = problem, experts, "moe_expert_backward_weights"
     slots = p.num_tokens * p.topk
     _check(load_library().moe_expert_backward_weights(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), ctypes.byref(x.c()),
+        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, dout, "bfloat16", slots, x.weight_rows),
         _take(where, dweights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols), _stream(stream)), where)
 
@@ -623,7 +629,7 @@ def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, strea
     p, where = problem, "moe_quant4_rows"
     slots, cols = p.num_tokens * p.topk, 2 * int(codes.shape[1])
     _check(load_library().moe_quant4_rows(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), cols, _take(where, rows, "bfloat16", slots, cols),
+        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), cols, _take(where, rows, "bfloat16", slots, cols),
         _take(where, codes, "uint8", slots, cols // 2),
         _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, cols)), _stream(stream)), where)
 
@@ -646,7 +652,7 @@ def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, code
     if x.scales is not None:
         _take_bytes(where, x.scales, moe_quant4_weight_scale_bytes(p, x))
     _check(load_library().moe_expert_forward4(
-        ctypes.byref(p.c()), ctypes.byref(layout.c()), ctypes.byref(x.c()),
+        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
         _take(where, codes, "uint8", slots, x.in_cols // 2),
         _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, x.in_cols)),
         _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),

@@ -66,7 +66,7 @@ __device__ __forceinline__ void scan_row_blocks(const int32_t* count, const int3
         const int e = tid * per + i;
         if (e < E) {
             base[e] = at;
-            at += blocks(expert_rows(count, offset, e, R).count);
+            at += blocks(keep != nullptr ? keep[e].count : expert_rows(count, offset, e, R).count);
             if (e == E - 1) base[E] = at;
         }
     }
