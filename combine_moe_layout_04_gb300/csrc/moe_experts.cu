@@ -287,7 +287,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         }
         if (SPLIT) {
             // the block before has been read by all parts
-            if (tid == 0 && !within_second([&] { return tc::try_wait_cluster(link.seen, link.phase ^ 1u); })) link.ok = false;
+            if (tid == 0 && !within(kSecond, [&] { return tc::try_wait_cluster(link.seen, link.phase ^ 1u); })) link.ok = false;
         }
         store_sync(group);  // the block before has been read
 #pragma unroll
@@ -296,7 +296,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         if (SPLIT) {
             if (tid < link.parts)
                 tc::arrive_release_cluster(tc::in_rank(link.ready, 2 * tid + link.cta));
-            if (tid == 0 && !within_second([&] { return tc::try_wait_cluster(link.ready, link.phase); })) link.ok = false;
+            if (tid == 0 && !within(kSecond, [&] { return tc::try_wait_cluster(link.ready, link.phase); })) link.ok = false;
             link.ok = store_all(group, link.ok);
             if (!link.ok) break;
             link.phase ^= 1u;

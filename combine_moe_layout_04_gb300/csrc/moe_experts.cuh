@@ -6,22 +6,24 @@
 
 namespace moe {
 
-// Tries until it succeeds, giving up after a second.  The clock is read only once
-// in 1024 tries: reading it costs more than a stage of a product lasts.
+// Tries until it succeeds, giving up after limit_ns (or somewhat later: the clock
+// is read only once in 1024 tries, because reading it costs more than a stage of a
+// product lasts).
 template <typename F>
-__device__ __forceinline__ bool within_second(F attempt) {
+__device__ __forceinline__ bool within(uint64_t limit_ns, F attempt) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
         if (attempt()) return true;
         if ((it & 1023u) == 0u) {
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            else if (now - t0 > 1000000000ull) return false;
+            else if (now - t0 > limit_ns) return false;
         }
     }
 }
+constexpr uint64_t kSecond = 1000000000ull;
 __device__ __forceinline__ bool wait_second(uint32_t bar, uint32_t parity) {
-    return within_second([&] { return mbar_try_wait(bar, parity); });
+    return within(kSecond, [&] { return mbar_try_wait(bar, parity); });
 }
 
 // Rows of one expert, kept inside [0, R) whatever the layout holds.

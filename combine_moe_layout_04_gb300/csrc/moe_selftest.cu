@@ -1,13 +1,14 @@
 // moe_selftest.cu -- drives the library's bounded device waits into their
 // give-up paths on purpose, without faulting, trapping or hanging the GPU.
 //
-// The production kernels wait in two places: the bulk-copy pipelines of
-// dispatch and combine wait on shared-memory barriers (mbar_wait_bounded), and
-// the cooperative layout kernel waits at a grid barrier (grid_barrier).  Both
-// give up after a wall-time limit.  This file runs those same functions:
-//   bit 0  an mbarrier that expects 16 bytes no copy will ever deliver: the
-//          wait must give up;
-//   bit 1  an mbarrier whose phase completes: the wait must succeed;
+// The production kernels wait in three places: the bulk-copy pipelines of
+// dispatch and combine wait on shared-memory barriers (mbar_wait_bounded), the
+// experts' products do too (within), and the cooperative layout kernel waits at
+// a grid barrier (grid_barrier).  All give up after a wall-time limit.  This
+// file runs those same functions:
+//   bit 0  an mbarrier that expects 16 bytes no copy will ever deliver: both
+//          kinds of wait must give up;
+//   bit 1  an mbarrier whose phase completes: both must succeed;
 //   bit 2  a two-block cooperative grid where one block never arrives: the
 //          other block's barrier wait must give up;
 //   bit 3  the same grid with both blocks arriving: both waits must succeed.
@@ -15,7 +16,7 @@
 
 #include <cuda_runtime.h>
 
-#include "moe_internal.cuh"
+#include "moe_experts.cuh"
 
 namespace moe {
 namespace {
@@ -36,10 +37,13 @@ __global__ void selftest_mbar_kernel() {
     fence_mbar_init();
     // Expect bytes that never arrive: the phase cannot complete.
     mbar_arrive_expect_tx(b0, 16);
-    if (!mbar_wait_bounded(b0, 0u, kSelftestLimitNs)) atomicOr(&g_selftest_bits, 0x1u);
+    if (!mbar_wait_bounded(b0, 0u, kSelftestLimitNs) &&
+        !within(kSelftestLimitNs, [&] { return mbar_try_wait(b0, 0u); }))
+        atomicOr(&g_selftest_bits, 0x1u);
     // Arrive with nothing expected: the phase completes at once.
     mbar_arrive_expect_tx(b1, 0);
-    if (mbar_wait_bounded(b1, 0u, kSelftestLimitNs)) atomicOr(&g_selftest_bits, 0x2u);
+    if (mbar_wait_bounded(b1, 0u, kSelftestLimitNs) && within(kSelftestLimitNs, [&] { return mbar_try_wait(b1, 0u); }))
+        atomicOr(&g_selftest_bits, 0x2u);
 }
 
 __global__ void selftest_grid_kernel(int skip_block) {

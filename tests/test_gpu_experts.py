@@ -250,6 +250,56 @@ def test_repeatable_and_on_another_stream(moe):
     assert torch.equal(a[4], b[4]) and torch.equal(a[5], b[5])
 
 
+def test_two_streams_at_once(moe):
+    """Two problems on two streams, their kernels side by side on the GPU: the bits of each alone."""
+    import torch
+    jobs = []
+    for i, counts in enumerate((COUNTS["skewed"], COUNTS["few each"])):
+        prob, lay = layout_of_counts(moe, counts)
+        R, E, K, N = prob.num_tokens, prob.num_experts, 1024, 520
+        rows, w = randn((R, K), i), randn((E, 2 * N, K), 10 + i, K ** -0.5)
+        out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+        x = moe.Experts(K, N, w, act=moe.MOE_ACT_SWIGLU)
+        moe.moe_expert_forward(prob, lay, x, rows, out)
+        jobs.append((prob, lay, x, rows, out, out.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for j in jobs:
+        j[4].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for prob, lay, x, rows, out, _, stream in jobs:
+            moe.moe_expert_forward(prob, lay, x, rows, out, stream=stream)
+    torch.cuda.synchronize()
+    for j in jobs:
+        assert torch.equal(j[4], j[5])
+
+
+def test_least_alignment(moe):
+    """Arrays that start on 16 bytes and no more."""
+    import torch
+
+    def off(t):
+        raw = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        assert raw.data_ptr() % 256 == 0
+        v = raw[8:].view(t.shape)
+        v.copy_(t)
+        return v
+    prob, lay = layout_of_counts(moe, COUNTS["tile edges"])
+    R, K, N = prob.num_tokens, 72, 136
+    rows, w, dout, pre = randn((R, K), 1), randn((8, N, K), 2, K ** -0.5), randn((R, N), 3), randn((R, 2 * K), 4)
+    for fix in (lambda t: t, off):
+        out, dw, drows = (fix(torch.zeros(s, dtype=torch.bfloat16, device="cuda")) for s in ((R, N), (8, N, K), (R, 2 * K)))
+        x = moe.Experts(K, N, fix(w))
+        moe.moe_expert_forward(prob, lay, x, fix(rows), out)
+        moe.moe_expert_backward_rows(prob, lay, x, fix(dout), drows, pre=fix(pre))
+        moe.moe_expert_backward_weights(prob, lay, x, fix(rows), fix(dout), dw)
+        torch.cuda.synchronize()
+        if fix is off:
+            assert all(torch.equal(a, b) for a, b in zip(first, (out, dw, drows)))
+        else:
+            first = (out, dw, drows)
+
+
 def test_captured_in_a_graph(moe):
     import torch
     prob, lay = layout_of_counts(moe, COUNTS["tile edges"])
