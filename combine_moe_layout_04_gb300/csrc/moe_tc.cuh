@@ -55,6 +55,11 @@ constexpr uint64_t kScales = descriptor(0, 128, 0);
 
 // ---- tensor copies ---------------------------------------------------------
 
+// A box from shared memory to its place, in this thread's bulk group; what lies past the end is left out.
+__device__ __forceinline__ void store3(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 :: "l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
 }
@@ -172,20 +177,21 @@ inline Encode encoder() {
     return fn;
 }
 
-// [depth][rows][cols] of bf16 (or of bytes), dense ([rows][cols] when depth is 0), in boxes of box_rows x 128 bytes with
-// 128-byte swizzle; what a box reaches past the end reads as zeros.
+// [depth][rows][cols] of bf16 (or of bytes), dense ([rows][cols] when depth is 0), in boxes of box_rows x box_bytes (64 or
+// 128) with a swizzle of box_bytes; what a box reaches past the end reads as zeros.
 inline bool make_map(CUtensorMap* map, const void* data, bool bytes, int64_t cols, int64_t rows, int64_t depth,
-                     int box_rows) {
+                     int box_rows, int box_bytes = 128) {
     const Encode encode = encoder();
     if (encode == nullptr) return false;
     const cuuint64_t size = bytes ? 1 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
     const cuuint64_t pitch[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
                   const_cast<void*>(data), dims, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
