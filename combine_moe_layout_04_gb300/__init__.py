@@ -616,6 +616,17 @@ def moe_quant4_weight_scale_bytes(problem: Problem, experts: Experts) -> int:
     return n.value
 
 
+# The sizes again, without a call into the library (a test holds them together).
+
+def _row_scale_bytes(p: Problem, cols: int) -> int:
+    return (p.num_tokens * p.topk // 128 + p.num_experts) * -(-cols // 128) * 512
+
+
+def _weight_scale_bytes(p: Problem, x: Experts) -> int:
+    per = 64 if x.act == MOE_ACT_SWIGLU else 128
+    return p.num_experts * -(-x.out_cols // per) * -(-x.in_cols // 128) * 512
+
+
 def _take_bytes(where: str, t, size: int):
     """Address of a dense uint8 tensor of at least `size` bytes."""
     at = _take(where, t, "uint8")
@@ -631,7 +642,7 @@ def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, strea
     _check(load_library().moe_quant4_rows(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), cols, _take(where, rows, "bfloat16", slots, cols),
         _take(where, codes, "uint8", slots, cols // 2),
-        _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, cols)), _stream(stream)), where)
+        _take_bytes(where, scales, _row_scale_bytes(p, cols)), _stream(stream)), where)
 
 
 def moe_quant4_weights(problem: Problem, experts: Experts, codes, scales, stream=None):
@@ -640,7 +651,7 @@ def moe_quant4_weights(problem: Problem, experts: Experts, codes, scales, stream
     _check(load_library().moe_quant4_weights(
         ctypes.byref(p.c()), _take_weights(where, p, x),
         _take(where, codes, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2),
-        _take_bytes(where, scales, moe_quant4_weight_scale_bytes(p, x)), _stream(stream)), where)
+        _take_bytes(where, scales, _weight_scale_bytes(p, x)), _stream(stream)), where)
 
 
 def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, codes, scales, out, pre=None, stream=None):
@@ -650,11 +661,11 @@ def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, code
     slots = p.num_tokens * p.topk
     _take(where, x.weights, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2)
     if x.scales is not None:
-        _take_bytes(where, x.scales, moe_quant4_weight_scale_bytes(p, x))
+        _take_bytes(where, x.scales, _weight_scale_bytes(p, x))
     _check(load_library().moe_expert_forward4(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
         _take(where, codes, "uint8", slots, x.in_cols // 2),
-        _take_bytes(where, scales, moe_quant4_row_scale_bytes(p, x.in_cols)),
+        _take_bytes(where, scales, _row_scale_bytes(p, x.in_cols)),
         _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),
         _stream(stream)), where)
 

@@ -139,6 +139,11 @@ def test_quant4_sizes_and_refusals(moe):
     assert moe.moe_quant4_row_scale_bytes(p, 160) == (512 // 128 + 16) * 2 * 512
     assert moe.moe_quant4_weight_scale_bytes(p, moe.Experts(160, 136)) == 16 * 2 * 2 * 512
     assert moe.moe_quant4_weight_scale_bytes(p, moe.Experts(160, 136, act=moe.MOE_ACT_SWIGLU)) == 16 * 3 * 2 * 512
+    for act in (moe.MOE_ACT_NONE, moe.MOE_ACT_SWIGLU):
+        for cols, n in ((32, 8), (160, 136), (256, 64), (1056, 1000)):
+            x = moe.Experts(cols, n, act=act)
+            assert moe._row_scale_bytes(p, cols) == moe.moe_quant4_row_scale_bytes(p, cols)
+            assert moe._weight_scale_bytes(p, x) == moe.moe_quant4_weight_scale_bytes(p, x)
     for cols in (0, 16, -32, 100, (1 << 20) + 32):
         with pytest.raises(moe.MoeError) as ei:
             moe.moe_quant4_row_scale_bytes(p, cols)
