@@ -55,3 +55,44 @@ def test_layer_in_4_bits(example):
     (E2M1 with a power-of-two scale is 0.11 to 0.14 off in norm), two products one after the other."""
     off = example.main(["--tokens", "257", "--hidden", "512", "--inter", "256"])
     assert 0.05 < off < 0.45
+
+
+CHILD = r"""
+import importlib.util, sys
+sys.path.insert(0, {root!r})
+import torch
+spec = importlib.util.spec_from_file_location("example", {root!r} + "/examples/moe_layer.py")
+example = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(example)
+torch.manual_seed(3)
+layer = example.MoeLayer(40, 2048, 256, 8, 2)
+x = torch.randn((40, 2048), device="cuda").to(torch.bfloat16)
+logits = torch.randn((40, 8), device="cuda")
+dout = torch.randn((40, 2048), device="cuda").to(torch.bfloat16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = [layer.forward(x, logits), *layer.backward(logits, dout)]
+    layer.quantise()
+    four = layer.serve(x, logits).clone()
+for o in outs:
+    o.zero_()
+g.replay()
+torch.cuda.synchronize()
+replayed = [o.clone() for o in outs[1:]] + [four.clone()]
+layer.forward(x, logits)
+eager = list(layer.backward(logits, dout))
+for o, r in zip(eager, replayed):
+    assert torch.equal(o, r)
+assert torch.equal(layer.serve(x, logits), replayed[-1])
+print("cold capture ok")
+"""
+
+
+def test_a_process_s_first_calls_inside_a_graph_capture(example):
+    """The launch-shape lookups of a first call are legal in a capture, and the replay gives the eager results."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", CHILD.format(root=ROOT)], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
+    assert "cold capture ok" in r.stdout
