@@ -12,13 +12,14 @@
 //   gradient of rows    sums[column][row]    = W^T dout^T     W across it
 //   gradient of weights sums[w][column]      = dout^T rows    both across it (rows are summed)
 //
-// Ten warps a CTA: one feeds a ring of shared-memory stages with tensor copies (128
-// bytes along memory, 128-byte swizzle), one of the pair issues the products, two
-// groups of four turn finished sums into results while the next tile is computed
-// (two tiles' sums of 256 columns fit in tensor memory).  A result row runs along the
-// lanes of tensor memory, so the store half turns 32 columns at a time through
-// shared memory, in fp32: activations see unrounded sums, and a result row is
-// written 256 bytes at a time.
+// Eighteen warps a CTA: one feeds a ring of shared-memory stages with tensor copies
+// (128 bytes along memory, 128-byte swizzle), one of the pair issues the products,
+// four groups of four turn finished sums into results while the next tile is
+// computed: tiles take the two ends of tensor memory in turn, and where two do not
+// fit beside each other the shared columns are stored first.  A result row runs
+// along the lanes of tensor memory, so the store half turns 16 columns at a time
+// through shared memory, in fp32: activations see unrounded sums, and a result row
+// is written 256 bytes at a time.
 //
 // With a gated activation the 128 weight rows of a CTA are 64 gate rows and the 64
 // up rows of the same features.
@@ -34,6 +35,14 @@
 // Few tiles and a long contraction: two or four pairs of a cluster share a tile,
 // each over its part of the contraction, and its CTAs' store halves add the parts up
 // through distributed shared memory, in part order.
+//
+// What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows: the copies from L2 into shared
+// memory, which end at 52-54 bytes a clock and SM whatever the tile (16 KB of weights and up to 20 KB of rows a stage
+// against 512 clocks of products for 256 columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run
+// at 1800 TFLOP/s in a burst (the library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a
+// stage is 36 KB for the same 512 clocks: 5.8 PFLOP/s.  Taking the scales to tensor memory one stage early, by the same
+// warp (406 us) or by one of its own (368 us), measured slower than between the products (333 us; 32768 rows of 32
+// experts, 7168 -> 2 x 2048).
 //
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
