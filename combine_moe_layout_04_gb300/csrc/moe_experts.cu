@@ -208,7 +208,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)); the reciprocal is good to one unit in the last place, small results included.
+__device__ __forceinline__ float sigmoid(float g) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+    return r;
+}
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     st_v4(reinterpret_cast<uint4*>(p), make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]),
@@ -262,8 +267,8 @@ __device__ __forceinline__ void summed8(const float* p, const Link& link, float 
 // A finished tile of the weights' gradient: a lane holds a weight row, so that nothing has to be turned.  A store group
 // puts 32 columns of its 128 rows into shared memory (64 bytes a row, swizzled so that 8 lanes cover all banks) and a
 // tensor copy takes them from there; the result has no ragged side, and the copy leaves out what lies past its ends.
-// Through the turned block and vector stores, as below, a 256 x 256 tile takes 2.6 us of the store half instead of 1.6 us; straight
-// from registers, 32 bytes a lane at the pitch of a row, 3.7 us (16 rows of 64 experts, 1024 x 1024: 36.6, 25.1 and 51 us).
+// 16 rows of 64 experts, 1024 x 1024, take 25.1 us; through the turned block and vector stores, as below, they took 36.6
+// us, and straight from registers, 32 bytes a lane at the pitch of a row, 51 us.
 __device__ __forceinline__ void store_weights(const Plan& p, const Tile& t, const CUtensorMap* map, uint32_t sums,
                                               uint32_t block, int cta, int group, int tid) {
     const int w0 = t.f0 + cta * kHalf;
@@ -298,8 +303,9 @@ __device__ __forceinline__ void store_weights(const Plan& p, const Tile& t, cons
 
 // A finished tile to its results: the store groups take blocks of 16 columns of the sums in turn, each through its own
 // block of shared memory, and fetch the next one while they write.  sums: tensor memory of this warp's lanes; cta: which
-// half of the features; tid: of 128; link: how the parts of a tile meet (SPLIT).  up: from the first column to the last, else the other way; after `shared` blocks
-// (the columns the next tile's sums take over) this warp arrives on the barrier `over`.
+// half of the features; tid: of 128; link: how the parts of a tile meet (SPLIT).  up: from the first column to the last,
+// else the other way; after `shared` blocks (the columns the next tile's sums take over) this warp arrives on the barrier
+// `over`.
 template <int OP, bool GLU, bool SPLIT>
 __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
                                            int cta, int group, int tid, bool up, int shared, uint32_t over, Link& link) {
@@ -554,7 +560,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const bool wide = !across_b && !k4 && t.n > kColumns;
-                        // tiles take the low and the high end of tensor memory in turn
+            // tiles take the low and the high end of tensor memory in turn
             const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
             // the instruction of the tile and, for a wide one, of its other columns; in 4 bits for either half of a scale word
             const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0)
@@ -612,7 +618,9 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (k < count) tc::mma_pair(sums + kFirst, da + k * (across_a ? 128 : 2), dc + k * 2, instr1, k0 > begin || k > 0);
+                            if (k < count)
+                                tc::mma_pair(sums + kFirst, da + k * (across_a ? 128 : 2), dc + k * 2, instr1,
+                                             k0 > begin || k > 0);
                     }
                     tc::commit_pair(empty + 8 * ring.stage, both);
                 }

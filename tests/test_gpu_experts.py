@@ -69,6 +69,33 @@ def test_forward(moe, counts, K, N, act):
     _check_forward(lay, *_forward(moe, prob, lay, K, N, act), act)
 
 
+def test_gate_far_out(moe):
+    """Gates from -100 to 100 (one weight, so that a row is its own gate): silu keeps its relative accuracy where
+    exp(-g) nears and passes the largest float, and its gradient too."""
+    import torch
+    g = torch.linspace(-100, 100, 4096, device="cuda").to(torch.bfloat16)
+    counts = [4096]
+    prob, lay = layout_of_counts(moe, counts)
+    rows = torch.zeros((4096, 8), dtype=torch.bfloat16, device="cuda")
+    rows[:, 0], rows[:, 1] = g, 3.0
+    w = torch.zeros((1, 16, 8), dtype=torch.bfloat16, device="cuda")
+    w[0, :8, 0], w[0, 8:, 1] = 1.0, 1.0
+    out = torch.empty((4096, 8), dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_forward(prob, lay, moe.Experts(8, 8, w, act=moe.MOE_ACT_SWIGLU), rows, out)
+    x = g.double()
+    # exp(-g) past the largest float is infinity: 0 there (the true value is below 2^-121)
+    close(out[:, 0], 3 * x * torch.sigmoid(x), 2.0 ** -20 * 3 * (x * torch.sigmoid(x)).abs() + 2.0 ** -119 * (x < -88))
+    pre = torch.stack((g, torch.full_like(g, 3.0)), 1).repeat_interleave(8, 1).contiguous()
+    dout = torch.ones((4096, 8), dtype=torch.bfloat16, device="cuda")
+    eye = torch.eye(8, dtype=torch.bfloat16, device="cuda")[None].contiguous()
+    drows = torch.empty((4096, 16), dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_backward_rows(prob, lay, moe.Experts(8, 8, eye), dout, drows, pre=pre)
+    s = torch.sigmoid(x)
+    low = 2.0 ** -119 * (x < -88)
+    close(drows[:, 0], 3 * s * (1 + x * (1 - s)), 2.0 ** -20 * 3 * s * (1 + x.abs()) + low)
+    close(drows[:, 8], x * s, 2.0 ** -20 * (x * s).abs() + low)
+
+
 def test_forward_without_pre(moe):
     prob, lay = layout_of_counts(moe, COUNTS["tile edges"])
     a = _forward(moe, prob, lay, 136, 200, True)
