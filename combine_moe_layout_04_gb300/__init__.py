@@ -277,7 +277,24 @@ class Problem:
             return self.hidden + 4 * (self.hidden // MOE_FP8_GROUP)
         return 2 * self.hidden
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_sizes", None)
+
+    def __getstate__(self):
+        return {name: value for name, value in self.__dict__.items() if name != "_sizes"}
+
     def c(self) -> _ProblemC:
+        # a struct of sizes alone is made once and again when a field changes
+        pc = self.__dict__.get("_sizes")
+        if pc is not None:
+            return pc
+        if self.expert_to_rank is None and self.src_rank_offsets is None and self.tuning is None:
+            pc = self.__dict__["_sizes"] = self._struct()
+            return pc
+        return self._struct()
+
+    def _struct(self) -> _ProblemC:
         # the struct keeps its tuning alive for as long as it is referenced
         pc = _ProblemC(self.num_tokens, self.hidden, self.topk, self.num_experts, self.num_ranks,
                        self.ranks_per_host, self.num_src_ranks, self.dtype,
@@ -529,7 +546,7 @@ def moe_combine_group(problem: Problem, layout: Layout, ids, expert_group, group
 def moe_route(problem: Problem, routing: Routing, logits, ids, gates, bias=None, stream=None):
     """ids and gates of every token's top-k experts from logits [T, E] (fp32 or bf16)."""
     p, where = problem, "moe_route"
-    _check(load_library().moe_route(
+    _check((_lib or load_library()).moe_route(
         ctypes.byref(p.c()), ctypes.byref(routing.c(logits)),
         _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
         _take(where, bias, "float32", p.num_experts), _take(where, ids, "int32", p.num_tokens, p.topk),
@@ -542,7 +559,7 @@ def moe_route_backward(problem: Problem, routing: Routing, logits, ids, dgates, 
     at = _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts)
     if getattr(logits, "dtype", None) != getattr(dlogits, "dtype", None):
         raise MoeError(MOE_ERR_INVALID, f"{where}: dlogits has the logits' type")
-    _check(load_library().moe_route_backward(
+    _check((_lib or load_library()).moe_route_backward(
         ctypes.byref(p.c()), ctypes.byref(routing.c(logits)), at, _take(where, ids, "int32", p.num_tokens, p.topk),
         _take(where, dgates, "float32", p.num_tokens, p.topk),
         _take(where, dlogits, "float32|bfloat16", p.num_tokens, p.num_experts), _stream(stream)), where)
@@ -552,7 +569,7 @@ def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy,
     """Gradients of moe_combine: dy [T*k, h] and dweights [T, k] from dout [T, h]."""
     p, where = problem, "moe_combine_backward"
     slots = p.num_tokens * p.topk
-    _check(load_library().moe_combine_backward(
+    _check((_lib or load_library()).moe_combine_backward(
         ctypes.byref(p.c()), ctypes.byref(_LayoutC(pos=layout.pos.data_ptr())),
         _take(where, dout, "bfloat16", p.num_tokens, p.hidden),
         _take(where, y, "bfloat16", slots, p.hidden), _take(where, weights, "float32", p.num_tokens, p.topk),
@@ -575,7 +592,7 @@ def moe_expert_forward(problem: Problem, layout: Layout, experts: Experts, rows,
     with MOE_ACT_SWIGLU (pre [T*k, W] then receives what the gate is made of)."""
     p, x, where = problem, experts, "moe_expert_forward"
     slots = p.num_tokens * p.topk
-    _check(load_library().moe_expert_forward(
+    _check((_lib or load_library()).moe_expert_forward(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, pre, "bfloat16", slots, x.weight_rows),
         _take(where, out, "bfloat16", slots, x.out_cols), _stream(stream)), where)
@@ -586,7 +603,7 @@ def moe_expert_backward_rows(problem: Problem, layout: Layout, experts: Experts,
     pre [T*k, 2 * in_cols] (the rows were its gated halves) drows is pre's gradient."""
     p, x, where = problem, experts, "moe_expert_backward_rows"
     slots, wide = p.num_tokens * p.topk, x.in_cols * (1 if pre is None else 2)
-    _check(load_library().moe_expert_backward_rows(
+    _check((_lib or load_library()).moe_expert_backward_rows(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
         _take(where, dout, "bfloat16", slots, x.weight_rows), _take(where, pre, "bfloat16", slots, wide),
         _take(where, drows, "bfloat16", slots, wide), _stream(stream)), where)
@@ -596,7 +613,7 @@ def moe_expert_backward_weights(problem: Problem, layout: Layout, experts: Exper
     """dweights [E, W, in_cols] = per expert, the sum of dout[r]^T rows[r] over its rows."""
     p, x, where = problem, experts, "moe_expert_backward_weights"
     slots = p.num_tokens * p.topk
-    _check(load_library().moe_expert_backward_weights(
+    _check((_lib or load_library()).moe_expert_backward_weights(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, dout, "bfloat16", slots, x.weight_rows),
         _take(where, dweights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols), _stream(stream)), where)
@@ -639,7 +656,7 @@ def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, strea
     """Receive rows bf16 [T*k, cols] to 4-bit codes [T*k, cols / 2] and scale blocks."""
     p, where = problem, "moe_quant4_rows"
     slots, cols = p.num_tokens * p.topk, 2 * int(codes.shape[1])
-    _check(load_library().moe_quant4_rows(
+    _check((_lib or load_library()).moe_quant4_rows(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), cols, _take(where, rows, "bfloat16", slots, cols),
         _take(where, codes, "uint8", slots, cols // 2),
         _take_bytes(where, scales, _row_scale_bytes(p, cols)), _stream(stream)), where)
@@ -648,7 +665,7 @@ def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, strea
 def moe_quant4_weights(problem: Problem, experts: Experts, codes, scales, stream=None):
     """The experts' bf16 weights to 4-bit codes [E, W, in_cols / 2] and scale blocks."""
     p, x, where = problem, experts, "moe_quant4_weights"
-    _check(load_library().moe_quant4_weights(
+    _check((_lib or load_library()).moe_quant4_weights(
         ctypes.byref(p.c()), _take_weights(where, p, x),
         _take(where, codes, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2),
         _take_bytes(where, scales, _weight_scale_bytes(p, x)), _stream(stream)), where)
@@ -662,7 +679,7 @@ def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, code
     _take(where, x.weights, "uint8", p.num_experts, x.weight_rows, x.in_cols // 2)
     if x.scales is not None:
         _take_bytes(where, x.scales, _weight_scale_bytes(p, x))
-    _check(load_library().moe_expert_forward4(
+    _check((_lib or load_library()).moe_expert_forward4(
         ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
         _take(where, codes, "uint8", slots, x.in_cols // 2),
         _take_bytes(where, scales, _row_scale_bytes(p, x.in_cols)),

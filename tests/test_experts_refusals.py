@@ -198,3 +198,26 @@ def test_no_tokens_is_no_work(moe):
     moe.moe_route_backward(p, moe.Routing(), None, None, None, None, stream=0)
     moe.moe_combine_backward(p, _lay(moe), None, None, None, None, None, stream=0)
     moe.moe_expert_forward(p, _lay(moe), moe.Experts(64, 64, None), None, None, stream=0)
+
+
+def test_problem_struct_follows_its_fields(moe):
+    """The C struct is made once for plain sizes; a changed field, a placement or a tuning makes another, and
+    copies and pickles carry the fields alone."""
+    import copy
+    import pickle
+    p = _p(moe)
+    assert p.c() is p.c() and p.c().num_tokens == 256
+    p.num_tokens = 64
+    assert p.c().num_tokens == 64
+    p.tuning = moe.Tuning(layout_kind=moe.MOE_LAYOUT_FUSED)
+    assert p.c() is not p.c() and p.c().tuning.contents.layout_kind == moe.MOE_LAYOUT_FUSED
+    p.tuning = None
+    assert not p.c().tuning
+    p.expert_to_rank = At(0x5000)
+    assert p.c().expert_to_rank == 0x5000
+    p.expert_to_rank = None
+    p.c()
+    for other in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert other == p and other.c().num_tokens == 64
+        other.hidden = 2048
+        assert p.c().hidden == 1024 and other.c().hidden == 2048
