@@ -10,10 +10,12 @@
 // integer warp reductions.  Lane j keeps choice j, so the gates are one value a
 // lane.
 //
-// Instructions bound it, not the 4 E bytes a token: 16384 x 128, top-8 takes 10.5
-// us forward (floor 1.3 us) and 4.8 us backward, one token of 256 experts 2.5 us.
-// Eight lanes a token, four tokens a warp, measured 9.9 and 3.5 us there but 5.2 us
-// for one token; one form for all sizes is kept.
+// Instructions bound it, not the 4 E bytes a token.  Up to 256 experts every lane
+// sorts its (at most 8) keys once and a round takes the winner's head off; sorting
+// more costs more than the rounds save, so beyond that the winner looks through its
+// keys again.  16384 x 128, top-8: 7.8 us forward (searching lanes: 10.1 us; floor
+// 1.3 us) and 4.8 us backward; one token of 256 experts 2.2 us.  Eight lanes a token,
+// four tokens a warp, measured no faster.
 //
 // Softmax sums, sigmoids and gradients are fp32 throughout; bf16 logits widen
 // exactly, and a bf16 gradient is rounded once, when it is stored.
@@ -105,38 +107,62 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     const int E = a.E;
     float l[V];
     load_row<T, V>(static_cast<const T*>(a.logits) + t * a.E, E, lane, l);
-    unsigned key[V];
+    unsigned key[V], id[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = 32 * i + lane;
-        key[i] = e < E ? key_of(a.bias != nullptr ? l[i] + a.bias[e] : l[i]) : kTaken;
+        id[i] = 32 * i + lane;
+        key[i] = (int)id[i] < E ? key_of(a.bias != nullptr ? l[i] + a.bias[id[i]] : l[i]) : kTaken;
     }
-    float mine = -INFINITY;  // logit of choice `lane`
+    constexpr bool kSorted = V <= 8;
+    if (kSorted) {
+        // neighbours change places only when the later one is larger: equal keys stay in the order of their ids
+#pragma unroll
+        for (int n = V - 1; n > 0; --n)
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (key[i + 1] > key[i]) {
+                    const unsigned k = key[i], e = id[i];
+                    key[i] = key[i + 1];
+                    id[i] = id[i + 1];
+                    key[i + 1] = k;
+                    id[i + 1] = e;
+                }
+    }
     int chosen = 0;
+    unsigned best = key[0], at = id[0];            // of this lane
     for (int j = 0; j < a.k; ++j) {
-        unsigned best = key[0];
-        int at = 0;
+        if (!kSorted && (j == 0 || at == kFull)) {
+            best = key[0];
+            at = id[0];
 #pragma unroll
-        for (int i = 1; i < V; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        const unsigned top = __reduce_max_sync(kFull, best);
-        const unsigned id = __reduce_min_sync(kFull, best == top ? 32u * at + lane : 0xffffffffu);
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (id == (unsigned)(32 * i + lane)) {
-                key[i] = kTaken;
-                v = l[i];
-            }
-        v = __shfl_sync(kFull, v, id & 31);
-        if (lane == j) {
-            mine = v;
-            chosen = (int)id;
+            for (int i = 1; i < V; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = id[i];
+                }
         }
+        const unsigned top = __reduce_max_sync(kFull, best);
+        const unsigned won = __reduce_min_sync(kFull, best == top ? at : kFull);
+        if (at == won) {
+            if (kSorted) {
+#pragma unroll
+                for (int i = 0; i + 1 < V; ++i) {
+                    key[i] = key[i + 1];
+                    id[i] = id[i + 1];
+                }
+                key[V - 1] = kTaken;
+                best = key[0];
+                at = id[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (id[i] == won) key[i] = kTaken;
+                at = kFull;                        // looked up again before the next round
+            }
+        }
+        if (lane == j) chosen = (int)won;
     }
+    const float mine = lane < a.k ? widen(static_cast<const T*>(a.logits)[t * a.E + chosen]) : -INFINITY;
     const bool on = lane < a.k;
     float s;
     const float w = weight_of<V>(a, l, mine, on, &s);
