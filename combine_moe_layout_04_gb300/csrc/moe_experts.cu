@@ -36,13 +36,16 @@
 // each over its part of the contraction, and its CTAs' store halves add the parts up
 // through distributed shared memory, in part order.
 //
-// What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows: the copies from L2 into shared
-// memory, which end at 52-54 bytes a clock and SM whatever the tile (16 KB of weights and up to 20 KB of rows a stage
-// against 512 clocks of products for 256 columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run
-// at 1800 TFLOP/s in a burst (the library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a
-// stage is 36 KB for the same 512 clocks: 5.8 PFLOP/s.  Taking the scales to tensor memory one stage early, by the same
-// warp (406 us) or by one of its own (368 us), measured slower than between the products (333 us; 32768 rows of 32
-// experts, 7168 -> 2 x 2048).
+// What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows: the stages, which arrive at 52 to
+// 54 bytes a clock and SM whatever the tile (16 KB of weights and 16 KB of rows against 512 clocks of products for 256
+// columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run at 1800 TFLOP/s in a burst (the
+// library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a stage is 36 KB for the same 512
+// clocks: 5.8 PFLOP/s.  It is not L2: two pairs that share their rows by multicast, a quarter fewer bytes out of L2,
+// fill their stages no faster (and clusters of four CTAs leave 8 SMs idle: 681 -> 705 us at 272 rows of 64 experts).
+// Nor do earlier requests help: prefetching weights into L2 8 to 20 stages ahead took 685 -> 707 us and more, marking
+// them as first to leave it 675 -> 696 us, fetching 128 bytes at a time instead of 256 675 -> 702 us.  Taking 4-bit
+// scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
+// between the products (333 us; 32768 rows of 32 experts, 7168 -> 2 x 2048).
 //
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
