@@ -4,11 +4,16 @@
 //   dy[pos[t, j]] = bf16(w[t, j] dout[t]),  dw[t, j] = <dout[t], y[pos[t, j]]>
 //
 // HBM-bound: per token it reads one row and k rows and writes k rows, 4 flops
-// an element: 16384 tokens, top-8, h = 7168 (4.0 GB) take 607 us, 6.58 TB/s, 0.97
-// of what a plain copy moves; 131 tokens 8 us.  A block owns a token, so that dout
-// is read once and the dot products end in the block, in an order that only the
-// sizes fix: every thread takes the columns tid, tid + 256, ... of 8, then lanes,
-// then warps.  Eight slots' loads are issued together, 36 KB a block in flight.
+// an element: 16384 tokens, top-8, h = 7168 (4.0 GB) take 588 us, 6.78 TB/s, what a
+// plain copy moves.  A block owns a token, so that dout is read once and the dot
+// products end in the block, in an order that only the sizes fix: a thread takes
+// every THREADS-th group of 8 columns, then come the lanes, then the warps.  Eight
+// slots' loads are issued together.
+//
+// The block's size, both sides measured (us): with many tokens threads without columns only
+// take room from other blocks (4096 tokens: h = 512, top-10, 14.6 with 64 threads and 47.2 with 256; h = 2048, top-8,
+// 45.6 with 128 and 55.1 with 256; 16384 tokens, h = 7168: 588 with 128, 608 with 256, 685 with 512).  With few
+// tokens a block should have its row in flight at once (131 tokens, h = 7168: 9.5 with 128, 6.8 with 256, 5.8 with 512).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -18,18 +23,18 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = 8;  // slots taken at a time (their loads are issued together)
 
 __device__ __forceinline__ float2 wide2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-__global__ void __launch_bounds__(kThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
 combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R, const uint4* __restrict__ dout,
                         const uint4* __restrict__ y, const float* __restrict__ weights, uint4* __restrict__ dy,
                         float* __restrict__ dweights) {
+    constexpr int kWarps = THREADS / 32;
     __shared__ float part[kWarps][kSlots];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -46,7 +51,7 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
             w[j] = live ? weights[t * k + j0 + j] : 0.0f;
             acc[j] = 0.0f;
         }
-        for (int c = tid; c < nvec; c += kThreads) {
+        for (int c = tid; c < nvec; c += THREADS) {
             const uint4 d = dout[t * nvec + c];
             uint4 v[kSlots];
 #pragma unroll
@@ -58,14 +63,16 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
                 if (row[j] < 0) continue;
                 const uint32_t yw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
                 uint32_t o[4];
+                float sum = 0.0f;  // of the group by itself: fewer roundings in a row than one chain over the thread's columns
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 g = wide2(dw[i]), x = wide2(yw[i]);
-                    acc[j] = fmaf(g.x, x.x, acc[j]);
-                    acc[j] = fmaf(g.y, x.y, acc[j]);
+                    sum = fmaf(g.x, x.x, sum);
+                    sum = fmaf(g.y, x.y, sum);
                     const __nv_bfloat162 p = __floats2bfloat162_rn(w[j] * g.x, w[j] * g.y);
                     o[i] = *reinterpret_cast<const uint32_t*>(&p);
                 }
+                acc[j] += sum;
                 st_v4(dy + row[j] + c, make_uint4(o[0], o[1], o[2], o[3]));
             }
         }
@@ -86,13 +93,26 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
     }
 }
 
+template <int THREADS>
+cudaError_t launch(const int32_t* pos, int T, int k, int h, const void* dout, const void* y, const float* weights, void* dy,
+                   float* dweights, cudaStream_t s) {
+    return launch_pdl(combine_backward_kernel<THREADS>, dim3(T), dim3(THREADS), 0, s, pos, k, h / 8, T * k,
+                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
+                      dweights);
+}
+
 }  // namespace
 
 cudaError_t launch_combine_backward(const int32_t* pos, int T, int k, int h, const void* dout, const void* y,
                                     const float* weights, void* dy, float* dweights, cudaStream_t s) {
-    return launch_pdl(combine_backward_kernel, dim3(T), dim3(kThreads), 0, s, pos, k, h / 8, T * k,
-                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
-                      dweights);
+    // a thread for every 8 columns, up to 128 threads where the tokens fill the GPU anyway
+    const int sms = device_sm_count();
+    const int most = T <= sms ? 512 : T <= 4 * sms ? 256 : 128, want = h / 8 < most ? h / 8 : most;
+    if (want <= 32) return launch<32>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    if (want <= 64) return launch<64>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    if (want <= 128) return launch<128>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    if (want <= 256) return launch<256>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    return launch<512>(pos, T, k, h, dout, y, weights, dy, dweights, s);
 }
 
 }  // namespace moe

@@ -51,6 +51,24 @@ def test_matches_definition(moe, T, k, E, h):
     assert bool(((dw.double() - ref).abs() <= mag * (h / 256 + 8 + 16) * 2.0 ** -24).all())
 
 
+@pytest.mark.parametrize("T,k,h", [(700, 3, 8), (700, 2, 256), (700, 2, 264), (640, 2, 512), (650, 9, 520), (615, 3, 1032),
+                                   (620, 2, 7168), (160, 3, 1032), (160, 2, 4096), (151, 2, 2056), (100, 1, 520)])
+def test_every_block_size(moe, T, k, h):
+    """Many, some and few tokens at row widths on both sides of each block size."""
+    import torch
+    prob, lay = _problem(moe, T, k, 12, h)
+    dout, y = randn((T, h), 1), randn((T * k, h), 2)
+    w = torch.rand((T, k), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    dy, dw = _run(moe, prob, lay, dout, y, w)
+    pos = lay.pos.long()
+    want = torch.empty_like(dy)
+    want[pos.reshape(-1)] = (w[..., None] * dout.float()[:, None, :]).to(torch.bfloat16).flatten(0, 1)
+    assert torch.equal(dy, want)
+    a, b = dout.double()[:, None, :], y.double()[pos]
+    # groups of 8 products, at most h / 256 groups a thread, 5 additions over lanes and at most 16 over warps
+    assert bool(((dw.double() - (a * b).sum(-1)).abs() <= (a * b).abs().sum(-1) * (8 + h / 256 + 1 + 21) * 2.0 ** -24).all())
+
+
 def test_gates_of_zero_and_values_that_are_not_finite(moe):
     import torch
     prob, lay = _problem(moe, 10, 3, 6, 64)
