@@ -8,12 +8,15 @@
 // saturated.
 //
 // HBM-bound: 64 bytes in, 17 out, per 32 columns: 32768 rows of 7168 columns in
-// 112 us (5.3 TB/s of 6.8), 128 rows in 6.7 us.  A block takes 128 rows of 1024
-// columns: smaller ones (32 rows: 122 us), or blocks that stay and take one piece of
-// work after another (32 rows: 128 us), spend more on finding their expert than
-// their better balance gives.  Four lanes share a block, 8
-// columns each (one 16-byte load), so a warp takes 256 columns of a row: 128
-// bytes of codes and two 4-byte words of scales.
+// 95 us (6.3 TB/s of 6.8), 128 rows in 6.7 us.  A block takes 128 rows of 1024
+// columns: smaller ones (32 rows: a tenth longer), blocks of 2048 columns (100 us)
+// or blocks that stay and take one piece after another (100 us) measured slower.
+// Two lanes share a scale, 16 columns each (one 32-byte load), so a warp takes 512
+// columns of a row: 256 bytes of codes and four 4-byte words of scales.  With four
+// lanes a scale and 16-byte loads the warps' shuffles and index arithmetic,
+// paid twice as often, bound it (106 us; 112 with magnitudes compared one by one).
+// The next row's loads ahead of the current one's arithmetic gave nothing (95 us) and
+// cost the blocks of a decode their single wave (128 rows: 8.7 us).
 
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
@@ -28,24 +31,28 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
 
-constexpr int kPiece = 1024;  // columns of a row a warp takes: four loads of 256 in flight
+constexpr int kPiece = 1024;  // columns of a row a warp takes: two loads of 512 in flight
 
-// 256 columns of a row, c0 + 8 lane on this lane (cols: a multiple of 32), already loaded (v; 0 past the end).  Codes go
-// to the row's codes, scales to the 4-byte words of the row's place in the scale blocks: word g of the row is at sc + 512 g.
-__device__ __forceinline__ void quantise256(uint4 v, uint32_t* codes, uint8_t* sc, int c0, int cols, int lane) {
-    const int c = c0 + 8 * lane;
-    const bool live = c < cols;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    // magnitudes as integers order as the floats do; bf16 is the upper half
-    uint32_t top = 0;
+// 16 columns at p to w.  wide: p lies on 32 bytes.
+__device__ __forceinline__ void load16(uint32_t* w, const uint16_t* p, bool wide) {
+    if (wide) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    top = max(top, __shfl_xor_sync(kFull, top, 1));
-    top = max(top, __shfl_xor_sync(kFull, top, 2));
-    const uint32_t exponent = top >> 7;
-    const bool bad = exponent == 255u;
-    const uint32_t b = bad ? 255u : (exponent > 2u ? exponent - 2u : 0u);
-    const float inv = __uint_as_float((254u - min(b, 253u)) << 23);  // 2^(127 - b)
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = ld_stream_v4(reinterpret_cast<const uint4*>(p) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    }
+}
+
+// The codes of 8 columns, times inv.
+__device__ __forceinline__ uint32_t codes8(const uint32_t* w, float inv) {
     uint32_t out = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -53,27 +60,48 @@ __device__ __forceinline__ void quantise256(uint4 v, uint32_t* codes, uint8_t* s
         const uint32_t two = __nv_cvt_float2_to_fp4x2(x, __NV_E2M1, cudaRoundNearest);
         out |= two << (8 * i);
     }
-    if (live) codes[c >> 3] = bad ? 0u : out;
-    // the four scales of 128 columns meet in their first lane (0 and 16); past the last column the scale byte is 0
+    return out;
+}
+
+// 512 columns of a row, c0 + 16 lane on this lane (cols: a multiple of 32), already loaded (w; 0 past the end).  Codes go
+// to the row's codes, scales to the 4-byte words of the row's place in the scale blocks: word g of the row is at sc + 512 g.
+__device__ __forceinline__ void quantise512(const uint32_t* w, uint8_t* codes, uint8_t* sc, int c0, int cols, int lane) {
+    const int c = c0 + 16 * lane;
+    const bool live = c < cols;
+    // magnitudes as integers order as the floats do; bf16 is 16 bits, so two are compared at once
+    uint32_t two = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) two = __vmaxs2(two, w[i] & 0x7fff7fffu);
+    two = __vmaxs2(two, __shfl_xor_sync(kFull, two, 1));
+    const uint32_t exponent = max(two >> 16, two & 0xffffu) >> 7;
+    const bool bad = exponent == 255u;
+    const uint32_t b = bad ? 255u : (exponent > 2u ? exponent - 2u : 0u);
+    const float inv = __uint_as_float((254u - min(b, 253u)) << 23);  // 2^(127 - b)
+    const uint2 out = make_uint2(codes8(w, inv), codes8(w + 4, inv));
+    if (live) *reinterpret_cast<uint2*>(codes + (c >> 1)) = bad ? make_uint2(0u, 0u) : out;
+    // the four scales of 128 columns meet in their first lane (0, 8, 16, 24); past the last column the scale byte is 0
     uint32_t word = live ? b : 0u;
-    word |= __shfl_down_sync(kFull, word, 4) << 8;
-    word |= __shfl_down_sync(kFull, word, 8) << 16;
-    const int col = c0 + 8 * (lane & 16);
-    if ((lane & 15) == 0 && col < cols) *reinterpret_cast<uint32_t*>(sc + (int64_t)(col >> 7) * 512) = word;
+    word |= __shfl_down_sync(kFull, word, 2) << 8;
+    word |= __shfl_down_sync(kFull, word, 4) << 16;
+    if ((lane & 7) == 0 && live) *reinterpret_cast<uint32_t*>(sc + (int64_t)(c >> 7) * 512) = word;
 }
 
 // Columns c0 .. c0 + 1024 of a row (bf16) to its codes and scales.
-__device__ __forceinline__ void quantise_piece(const void* row, uint8_t* codes, uint8_t* sc, int c0, int cols, int lane) {
-    uint4 v[kPiece / 256];
+__device__ __forceinline__ void quantise_piece(const uint16_t* row, bool wide, uint8_t* codes, uint8_t* sc, int c0, int cols,
+                                               int lane) {
+    uint32_t w[kPiece / 512][8] = {};
 #pragma unroll
-    for (int i = 0; i < kPiece / 256; ++i) {
-        const int c = c0 + 256 * i + 8 * lane;
-        v[i] = c < cols ? ld_stream_v4(static_cast<const uint4*>(row) + (c >> 3)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kPiece / 512; ++i) {
+        const int c = c0 + 512 * i + 16 * lane;
+        if (c < cols) load16(w[i], row + c, wide);
     }
 #pragma unroll
-    for (int i = 0; i < kPiece / 256; ++i)
-        if (c0 + 256 * i < cols) quantise256(v[i], reinterpret_cast<uint32_t*>(codes), sc, c0 + 256 * i, cols, lane);
+    for (int i = 0; i < kPiece / 512; ++i)
+        if (c0 + 512 * i < cols) quantise512(w[i], codes, sc, c0 + 512 * i, cols, lane);
 }
+
+// Rows are a multiple of 64 bytes, so all lie on 32 bytes where the first does.
+__device__ __forceinline__ bool on_32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 // One block of the grid per (row block, piece of 1024 columns); the row blocks
 // of the experts follow one another, and the grid covers the most there can be.
@@ -92,9 +120,10 @@ quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (a.K + 127) >> 7;
     uint8_t* sc = scales + (int64_t)block * groups * 512;
+    const bool wide = on_32(a.rows);
     for (int i = warp; i < n; i += kWarps) {
         const int64_t r = x.first + i0 + i;
-        quantise_piece(static_cast<const uint16_t*>(a.rows) + r * a.K, codes + r * (a.K / 2), sc + scale_byte(i, 0),
+        quantise_piece(static_cast<const uint16_t*>(a.rows) + r * a.K, wide, codes + r * (a.K / 2), sc + scale_byte(i, 0),
                        blockIdx.y * kPiece, a.K, lane);
     }
 }
@@ -112,11 +141,12 @@ quant4_weights_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (a.K + 127) >> 7;
     uint8_t* sc = scales + (int64_t)blockIdx.x * groups * 512;
+    const bool wide = on_32(a.weights);
     for (int i = warp; i < 128; i += kWarps) {
         const int n = b * per + i % per;                 // result column
         if (n >= a.N) continue;
         const int64_t r = e * a.W + n + (i >= per ? a.N : 0);
-        quantise_piece(static_cast<const uint16_t*>(a.weights) + r * a.K, codes + r * (a.K / 2), sc + scale_byte(i, 0),
+        quantise_piece(static_cast<const uint16_t*>(a.weights) + r * a.K, wide, codes + r * (a.K / 2), sc + scale_byte(i, 0),
                        blockIdx.y * kPiece, a.K, lane);
     }
 }

@@ -67,6 +67,21 @@ def test_row_codes_and_scales_exact(moe, counts, K):
     assert torch.equal(unpack4(codes), want)
 
 
+@pytest.mark.parametrize("K", [32, 544, 1056, 2208])
+def test_rows_on_16_bytes_only(moe, K):
+    """Rows that start 16 bytes past a 32-byte boundary: the same codes and scales."""
+    import torch
+    counts = [3, 0, 130, 7]
+    prob, lay = layout_of_counts(moe, counts)
+    n = sum(counts)
+    rows = torch.empty(n * K + 8, dtype=torch.bfloat16, device="cuda")[8:].view(n, K)
+    rows.copy_(_wild(n, K, K))
+    assert rows.data_ptr() % 32 == 16
+    codes, scales = _quant_rows(moe, prob, lay, rows)
+    want, byte = quantise4(rows)
+    assert torch.equal(row_scales(lay, scales, K)[:, : K // 32], byte) and torch.equal(unpack4(codes), want)
+
+
 def test_not_finite_blocks(moe):
     import torch
     prob, lay = layout_of_counts(moe, [3, 2])
