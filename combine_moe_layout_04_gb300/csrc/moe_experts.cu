@@ -39,13 +39,13 @@
 // What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows: the stages, which arrive at 52 to
 // 54 bytes a clock and SM whatever the tile (16 KB of weights and 16 KB of rows against 512 clocks of products for 256
 // columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run at 1800 TFLOP/s in a burst (the
-// library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a stage is 36 KB for the same 512
-// clocks: 5.8 PFLOP/s.  It is not L2: two pairs that share their rows by multicast, a quarter fewer bytes out of L2,
+// library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a stage is 35 KB for the same 512
+// clocks: 6 PFLOP/s.  It is not L2: two pairs that share their rows by multicast, a quarter fewer bytes out of L2,
 // fill their stages no faster (and clusters of four CTAs leave 8 SMs idle: 681 -> 705 us at 272 rows of 64 experts).
 // Nor do earlier requests help: prefetching weights into L2 8 to 20 stages ahead took 685 -> 707 us and more, marking
 // them as first to leave it 675 -> 696 us, fetching 128 bytes at a time instead of 256 675 -> 702 us.  Taking 4-bit
 // scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
-// between the products (333 us; 32768 rows of 32 experts, 7168 -> 2 x 2048).
+// between the products (333 us then; 32768 rows of 32 experts, 7168 -> 2 x 2048).
 //
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
@@ -78,7 +78,7 @@ constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : kRowBytes / 2;  // its c
 constexpr int kBoxBytes = 64 * kRowBytes;
 constexpr int kBytesA = kHalf * kRowBytes;
 template <int OP>
-constexpr int kRingBytes = (OP == kForward4 ? 170 : 180) * 1024;
+constexpr int kRingBytes = (OP == kForward4 ? 176 : 180) * 1024;
 constexpr int kStages = 12;            // most stages in flight
 constexpr int kTurn = 16;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
@@ -87,8 +87,10 @@ template <int OP>                      // 1024: alignment; in 4 bits also the ex
 constexpr int kSmem = kRingBytes<OP> + kGroups * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
 
 // 4-bit stages end with the scales of 256 codes: 1 KB (two scale blocks along a row) of the weights' 128 rows and of
-// every 128 receive rows the tile touches (three at most); the products take them from tensor memory above the sums.
-constexpr int kScaleBlock = 512, kScaleBytes = 4 * 2 * kScaleBlock;
+// every 128 receive rows the tile touches (tiles start at multiples of 64 rows: one of up to 256 touches two, of up to
+// 384 three); the products take them from tensor memory above the sums.
+constexpr int kScaleBlock = 512;
+constexpr int scale_bytes(int columns) { return (columns > 256 ? 4 : 3) * 2 * kScaleBlock; }
 constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 struct Shared {
@@ -528,7 +530,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         tc::load2_pair(sb, b.map0, x, b0, bar);
                         if (b.rows1 > 0) tc::load2_pair(sb + b.rows0 * kRowBytes, b.map1, x, b0 + b.rows0, bar);
                         if (k4) {
-                            const uint32_t ss = sa + cut.bytes - kScaleBytes;
+                            const uint32_t ss = sa + kBytesA + cut.columns / 2 * kRowBytes;
                             const int g = k0 >> 7;
                             tc::load2_pair(ss, &maps.weight_scales, 0, wrow + g, bar);
                             tc::load2_pair(ss + 2 * kScaleBlock, &maps.row_scales, 0, rrow + g, bar);
@@ -536,11 +538,10 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                                 tc::load2_pair(ss + 4 * kScaleBlock, &maps.row_scales, 0, rrow + groups + g, bar);
                             if (scaled > 2)
                                 tc::load2_pair(ss + 6 * kScaleBlock, &maps.row_scales, 0, rrow + 2 * groups + g, bar);
-                        } else {
-                            const uint32_t sc = sb + b.bytes();
-                            if (c.rows0 > 0) tc::load2_pair(sc, c.map0, k0, c0, bar);
-                            if (c.rows1 > 0) tc::load2_pair(sc + c.rows0 * kRowBytes, c.map1, k0, c0 + c.rows0, bar);
                         }
+                        const uint32_t sc = sb + b.bytes();
+                        if (c.rows0 > 0) tc::load2_pair(sc, c.map0, x, c0, bar);
+                        if (c.rows1 > 0) tc::load2_pair(sc + c.rows0 * kRowBytes, c.map1, x, c0 + c.rows0, bar);
                     }
                 }
                 __syncwarp();
@@ -562,14 +563,13 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         int n = 0, before = 0;         // tiles so far, columns of the one before
         for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
-            const bool wide = !across_b && !k4 && t.n > kColumns;
+            const bool wide = !across_b && t.n > kColumns;
             // tiles take the low and the high end of tensor memory in turn
             const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
-            // the instruction of the tile and, for a wide one, of its other columns; in 4 bits for either half of a scale word
-            const uint32_t instr = k4 ? tc::instruction4_pair(t.n, 0)
-                                      : tc::instruction_pair(wide ? kFirst : t.n, across_a, across_b);
-            const uint32_t instr1 = k4 ? tc::instruction4_pair(t.n, 1)
-                                       : tc::instruction_pair(max(t.n - kFirst, 16), across_a, across_b);
+            // the instruction of the tile and, for a wide one, of its other columns
+            const int n0 = wide ? kFirst : t.n, n1 = max(t.n - kFirst, 16);
+            const uint32_t instr = tc::instruction_pair(n0, across_a, across_b);
+            const uint32_t instr1 = tc::instruction_pair(n1, across_a, across_b);
             // this end is free when the tile before the last is stored, and what the last one holds of it when its store
             // half has been there
             ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
@@ -591,7 +591,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 constexpr int kOne = k4 ? 64 : 16;                            // contraction of an instruction
                 const int count = (min(kStep<OP>, t.length - k0) + kOne - 1) / kOne;
                 if (k4 && tc::elect_one()) {
-                    const uint32_t ss = sa + cut.bytes - kScaleBytes;
+                    const uint32_t ss = sa + kBytesA + cut.columns / 2 * kRowBytes;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         tc::copy_scales_pair(tmem + kScalesA + 4 * g, tc::at(tc::kScales, ss + g * kScaleBlock));
@@ -606,10 +606,19 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     // a tile that starts in the middle of a scale block starts two columns of 32 rows later
                     const uint32_t sb4 = tmem + kScalesB + ((t.m0 & 127) >> 5);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k)   // two to a scale word
                         if (k < count)
-                            tc::mma4_pair(sums, da + k * 2, db + k * 2, k & 1 ? instr1 : instr,
+                            tc::mma4_pair(sums, da + k * 2, db + k * 2, tc::instruction4_pair(n0, k & 1),
                                           tmem + kScalesA + 4 * (k >> 1), sb4 + 12 * (k >> 1), k0 > begin || k > 0);
+                    if (wide) {
+                        const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < count)
+                                tc::mma4_pair(sums + kFirst, da + k * 2, dc + k * 2, tc::instruction4_pair(n1, k & 1),
+                                              tmem + kScalesA + 4 * (k >> 1), sb4 + kFirst / 32 + 12 * (k >> 1),
+                                              k0 > begin || k > 0);
+                    }
                     tc::commit_pair(empty + 8 * ring.stage, both);
                 } else if (!k4 && tc::elect_one()) {
 #pragma unroll
@@ -725,8 +734,12 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 //    rows (32 experts) 421 us at 384 and 478 at 256, 600 rows (7168 -> 2048) 333 us at 320 and 387 at 256.
 //  * Many tiles an expert waste little of either, and 256 columns issue fewer instructions: 3000 rows (8 experts) take
 //    388 us at 256 and 406 at 320; 1040 rows 594 and 600.
-//  * In 4 bits (tensor memory also holds scales: 256 columns at most) 100 rows take 169 us at 128 columns and 185 at 256;
-//    256 rows 212 us at 256 and 245 at 128; 1024 rows (32 experts) 331 us at 256 and 402 at 192.
+//  * In 4 bits a stage's copies take longer than its products, so wide tiles pay where they save one and their store half,
+//    which the next tile's sums wait for, costs less (32 experts, 7168 -> 2 x 2048): 256 rows take 117 us cut at 384 and
+//    129 at 256, 340 rows 133 and 153, but 400 rows 172 and 159, 700 rows 239 and 234; 850 rows (three tiles for four)
+//    291 and 306, 1100 rows 346 and 357, but 1300 rows (16 experts) 230 and 222.  170 rows take 97 us at 256, 129 at 128.
+//    The stages in flight count: 384 columns take 330 us with four and 353 with three (1024 rows), 256 columns 129 with five
+//    and 142 with four (256 rows).
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
@@ -734,8 +747,9 @@ Cut make_cut(const ExpertArgs& a) {
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
         if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 365 ? 384 : 320;
+        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean < 1200))) cut.columns = 384;
     }
-    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? kScaleBytes : 0);
+    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
     cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
     return cut;
 }

@@ -183,6 +183,29 @@ def test_product_wide_scales(moe):
     close(out, ref, sum_slack(mag, K))
 
 
+@pytest.mark.parametrize("counts,K,N", [([300, 0, 384, 290, 321, 129], 512, 136), ([257, 385, 310], 96, 264),
+                                        ([1000, 1153, 0, 1152, 900], 288, 72)])
+@pytest.mark.parametrize("act", [False, True])
+def test_product_wide_tiles(moe, counts, K, N, act):
+    """Tiles of two products, a different scale for every block: 2^-20 .. 2^20 on rows, up to 2^4 on weights."""
+    import torch
+    prob, lay = layout_of_counts(moe, counts)
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def spread(shape, most):
+        x = randn(shape, shape[-2], K ** -0.5)
+        s = torch.randint(-most, most + 1, shape[:-1] + (K // 32,), generator=g, device="cuda").float()
+        return (x.float() * torch.pow(2.0, s).repeat_interleave(32, dim=-1)).to(torch.bfloat16)
+    out, pre, values, wv = _product(moe, prob, lay, K, N, act, spread((sum(counts), K), 20),
+                                    spread((len(counts), 2 * N if act else N, K), 4))
+    ref, mag = products(lay, values, wv)
+    slack = sum_slack(mag, K)
+    if act:
+        close(pre, ref, slack)
+    else:
+        close(out, ref, slack)
+
+
 def test_rows_that_are_not_finite_stay_alone(moe):
     """A row with an infinity gives NaN in its own results and changes no other row; so do weights."""
     import torch
