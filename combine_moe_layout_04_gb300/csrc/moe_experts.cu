@@ -40,8 +40,11 @@
 // 54 bytes a clock and SM whatever the tile (16 KB of weights and 16 KB of rows against 512 clocks of products for 256
 // columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run at 1800 TFLOP/s in a burst (the
 // library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a stage is 35 KB for the same 512
-// clocks: 6 PFLOP/s.  It is not L2: two pairs that share their rows by multicast, a quarter fewer bytes out of L2,
-// fill their stages no faster (and clusters of four CTAs leave 8 SMs idle: 681 -> 705 us at 272 rows of 64 experts).
+// clocks: 6 PFLOP/s, a stage in some 740 clocks, and in 620 with a quarter of its products.  It is not L2: two pairs
+// that share their rows by multicast, a quarter fewer bytes out of L2, fill their stages no faster (and clusters of four
+// CTAs leave 8 SMs idle: 681 -> 705 us at 272 rows of 64 experts).  Nor is it one warp's issuing: a second copying warp
+// changed nothing in 4 bits.  Keeping the weights beside the tensor core between the two products of a wide tile did not
+// either (in 16 bits 583 -> 573 us at 1040 rows cut at 320, where 256 columns take 554).
 // Nor do earlier requests help: prefetching weights into L2 8 to 20 stages ahead took 685 -> 707 us and more, marking
 // them as first to leave it 675 -> 696 us, fetching 128 bytes at a time instead of 256 675 -> 702 us.  Taking 4-bit
 // scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
@@ -605,20 +608,21 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     }
                     // a tile that starts in the middle of a scale block starts two columns of 32 rows later
                     const uint32_t sb4 = tmem + kScalesB + ((t.m0 & 127) >> 5);
+                    auto products = [&](uint32_t d, uint64_t db, int n, uint32_t sb, int count) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)   // two to a scale word
-                        if (k < count)
-                            tc::mma4_pair(sums, da + k * 2, db + k * 2, tc::instruction4_pair(n0, k & 1),
-                                          tmem + kScalesA + 4 * (k >> 1), sb4 + 12 * (k >> 1), k0 > begin || k > 0);
-                    if (wide) {
-                        const uint64_t dc = tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 4; ++k)   // two to a scale word
                             if (k < count)
-                                tc::mma4_pair(sums + kFirst, da + k * 2, dc + k * 2, tc::instruction4_pair(n1, k & 1),
-                                              tmem + kScalesA + 4 * (k >> 1), sb4 + kFirst / 32 + 12 * (k >> 1),
-                                              k0 > begin || k > 0);
-                    }
+                                tc::mma4_pair(d, da + k * 2, db + k * 2, tc::instruction4_pair(n, k & 1),
+                                              tmem + kScalesA + 4 * (k >> 1), sb + 12 * (k >> 1), k0 > begin || k > 0);
+                    };
+                    auto both_products = [&](int count) {
+                        products(sums, db, n0, sb4, count);
+                        if (wide)
+                            products(sums + kFirst, tc::at(tc::kAlongK, sa + kBytesA + kFirst / 2 * kRowBytes), n1,
+                                     sb4 + kFirst / 32, count);
+                    };
+                    if (count == 4) both_products(4);  // without tests between the instructions (384 columns: 329 -> 325 us)
+                    else both_products(count);
                     tc::commit_pair(empty + 8 * ring.stage, both);
                 } else if (!k4 && tc::elect_one()) {
 #pragma unroll
