@@ -738,10 +738,12 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 //    rows (32 experts) 421 us at 384 and 478 at 256, 600 rows (7168 -> 2048) 333 us at 320 and 387 at 256.
 //  * Many tiles an expert waste little of either, and 256 columns issue fewer instructions: 3000 rows (8 experts) take
 //    388 us at 256 and 406 at 320; 1040 rows 594 and 600.
-//  * In 4 bits a stage's copies take longer than its products, so wide tiles pay where they save one and their store half,
-//    which the next tile's sums wait for, costs less (32 experts, 7168 -> 2 x 2048): 256 rows take 117 us cut at 384 and
-//    129 at 256, 340 rows 133 and 153, but 400 rows 172 and 159, 700 rows 239 and 234; 850 rows (three tiles for four)
-//    291 and 306, 1100 rows 346 and 357, but 1300 rows (16 experts) 230 and 222.  170 rows take 97 us at 256, 129 at 128.
+//  * In 4 bits tensor memory also holds scales, so the next tile's sums wait for most of a wide one's store half; wide tiles
+//    pay where they save one of two or of four (7168 -> 2 x 2048): 256 rows (32 experts) take 116 us cut at 384 and 129 at
+//    256, 340 rows 133 and 152, but 400 rows 172 and 159, 700 rows 239 and 234; 850 rows (16 experts) 150 and 159.  Three
+//    for four and a half, at 1024 rows, pay where the contraction is long and rounds of tiles are many: 32 experts 326 us
+//    cut at 384 and 337 at 256, 16 experts 176 and 175; 32 experts with 4096 columns 224 and 224, with 2048 158 and 151.
+//    1300 rows (16 experts) take 230 and 222; 170 rows 129 cut at 128 and 97 at 256.
 //    The stages in flight count: 384 columns take 330 us with four and 353 with three (1024 rows), 256 columns 129 with five
 //    and 142 with four (256 rows).
 template <int OP>
@@ -751,7 +753,8 @@ Cut make_cut(const ExpertArgs& a) {
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
         if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 365 ? 384 : 320;
-        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean < 1200))) cut.columns = 384;
+        const bool many = a.K >= 24 * kStep<kForward4> && (int64_t)a.E * a.N >= (a.glu ? 400 : 800) * kHalf;
+        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean < (many ? 1200 : 900)))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
     cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
