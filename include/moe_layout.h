@@ -450,7 +450,8 @@ int moe_combine_group(const moe_problem* problem, const moe_layout_t* layout, co
  *     MOE_SCORE_SIGMOID: 1 / (1 + exp(-logit)), divided by the sum of the
  *       chosen ones when renormalise is not 0.
  *   scale: every gate is multiplied by it (finite; 1 for none).
- *   logits_dtype: MOE_LOGITS_F32 or MOE_LOGITS_BF16, of logits and dlogits. */
+ *   logits_dtype: MOE_LOGITS_F32 or MOE_LOGITS_BF16, of logits and dlogits.
+ * No output overlaps an input or another output. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 #define MOE_LOGITS_F32    0
@@ -504,7 +505,8 @@ int moe_route_backward(const moe_problem* problem, const moe_routing* routing, c
  *     gate rows, then the up rows;
  *   scales: the 4-bit weights' scale blocks, else NULL.
  * in_cols and out_cols: multiples of 8 in [8, 2^20]; in_cols a multiple of 32
- * for the 4-bit calls.  E * W < 2^31.  Every array 16-byte aligned.
+ * for the 4-bit calls.  E * W < 2^31.  Every array 16-byte aligned; no output
+ * overlaps an input or another output, in these calls and those below.
  * Products are summed in fp32 and rounded once to bf16. */
 #define MOE_ACT_NONE   0
 #define MOE_ACT_SWIGLU 1
