@@ -7,8 +7,10 @@
 // an element: 16384 tokens, top-8, h = 7168 (4.0 GB) take 588 us, 6.78 TB/s, what a
 // plain copy moves.  A block owns a token, so that dout is read once and the dot
 // products end in the block, in an order that only the sizes fix: a thread takes
-// every THREADS-th group of 8 columns, then come the lanes, then the warps.  Eight
-// slots' loads are issued together.
+// every THREADS-th group of 8 columns, then come the lanes, then the warps.  Two,
+// four or eight slots' loads are issued together, by the least that takes k: registers for slots that are not
+// there would leave room for fewer blocks (16384 tokens, h = 7168: top-1 105 us with two slots and 165 with eight, top-2
+// 172 and 214, top-4 311 with four and 323 with eight; top-2, h = 2048: 51 and 77).
 //
 // The block's size, both sides measured (us): with many tokens threads without columns only
 // take room from other blocks (4096 tokens: h = 512, top-10, 14.6 with 64 threads and 47.2 with 256; h = 2048, top-8,
@@ -23,28 +25,27 @@
 namespace moe {
 namespace {
 
-constexpr int kSlots = 8;  // slots taken at a time (their loads are issued together)
-
 __device__ __forceinline__ float2 wide2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-template <int THREADS>
+// SLOTS are taken at a time.
+template <int THREADS, int SLOTS>
 __global__ void __launch_bounds__(THREADS)
 combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R, const uint4* __restrict__ dout,
                         const uint4* __restrict__ y, const float* __restrict__ weights, uint4* __restrict__ dy,
                         float* __restrict__ dweights) {
     constexpr int kWarps = THREADS / 32;
-    __shared__ float part[kWarps][kSlots];
+    __shared__ float part[kWarps][SLOTS];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    for (int j0 = 0; j0 < k; j0 += kSlots) {
-        int64_t row[kSlots];
-        float w[kSlots], acc[kSlots];
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        int64_t row[SLOTS];
+        float w[SLOTS], acc[SLOTS];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
             const bool live = j0 + j < k;
             const int r = live ? pos[t * k + j0 + j] : -1;
             row[j] = r >= 0 && r < R ? (int64_t)r * nvec : -1;
@@ -53,13 +54,13 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
         }
         for (int c = tid; c < nvec; c += THREADS) {
             const uint4 d = dout[t * nvec + c];
-            uint4 v[kSlots];
+            uint4 v[SLOTS];
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
+            for (int j = 0; j < SLOTS; ++j)
                 if (row[j] >= 0) v[j] = ld_stream_v4(y + row[j] + c);
             const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
+            for (int j = 0; j < SLOTS; ++j) {
                 if (row[j] < 0) continue;
                 const uint32_t yw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
                 uint32_t o[4];
@@ -77,13 +78,13 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
             }
         }
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], s);
             if (lane == 0) part[warp][j] = acc[j];
         }
         __syncthreads();
-        if (tid < kSlots && j0 + tid < k) {
+        if (tid < SLOTS && j0 + tid < k) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) sum += part[i][tid];
@@ -93,12 +94,19 @@ combine_backward_kernel(const int32_t* __restrict__ pos, int k, int nvec, int R,
     }
 }
 
+template <int THREADS, int SLOTS>
+cudaError_t launch(const int32_t* pos, int T, int k, int h, const void* dout, const void* y, const float* weights, void* dy,
+                   float* dweights, cudaStream_t s) {
+    return launch_pdl(combine_backward_kernel<THREADS, SLOTS>, dim3(T), dim3(THREADS), 0, s, pos, k, h / 8, T * k,
+                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
+                      dweights);
+}
 template <int THREADS>
 cudaError_t launch(const int32_t* pos, int T, int k, int h, const void* dout, const void* y, const float* weights, void* dy,
                    float* dweights, cudaStream_t s) {
-    return launch_pdl(combine_backward_kernel<THREADS>, dim3(T), dim3(THREADS), 0, s, pos, k, h / 8, T * k,
-                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y), weights, static_cast<uint4*>(dy),
-                      dweights);
+    if (k <= 2) return launch<THREADS, 2>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    if (k <= 4) return launch<THREADS, 4>(pos, T, k, h, dout, y, weights, dy, dweights, s);
+    return launch<THREADS, 8>(pos, T, k, h, dout, y, weights, dy, dweights, s);
 }
 
 }  // namespace

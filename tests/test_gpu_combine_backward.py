@@ -52,7 +52,8 @@ def test_matches_definition(moe, T, k, E, h):
 
 
 @pytest.mark.parametrize("T,k,h", [(700, 3, 8), (700, 2, 256), (700, 2, 264), (640, 2, 512), (650, 9, 520), (615, 3, 1032),
-                                   (620, 2, 7168), (160, 3, 1032), (160, 2, 4096), (151, 2, 2056), (100, 1, 520)])
+                                   (620, 2, 7168), (160, 3, 1032), (160, 2, 4096), (151, 2, 2056), (100, 1, 520),
+                                   (700, 1, 520), (700, 4, 264), (640, 5, 256), (151, 4, 7168), (160, 5, 2056), (20, 5, 1032)])
 def test_every_block_size(moe, T, k, h):
     """Many, some and few tokens at row widths on both sides of each block size."""
     import torch
