@@ -451,7 +451,7 @@ int moe_combine_group(const moe_problem* problem, const moe_layout_t* layout, co
  *       chosen ones when renormalise is not 0.
  *   scale: every gate is multiplied by it (finite; 1 for none).
  *   logits_dtype: MOE_LOGITS_F32 or MOE_LOGITS_BF16, of logits and dlogits.
- * No output overlaps an input or another output. */
+ * No output overlaps an input or another output, unless a call says so. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 #define MOE_LOGITS_F32    0
@@ -486,7 +486,7 @@ int moe_route(const moe_problem* problem, const moe_routing* routing, const void
  *   sigmoid, renormalised:    w_i (1 - s_i) (a_i - sum_j w_j a_j).
  *   logits, ids: as moe_route took and gave them (an id out of [0, E)
  *   contributes nothing); dgates: fp32 [T, k]; dlogits: [T, E] of the logits'
- *   type, every value written. */
+ *   type, every value written; it may be logits itself. */
 int moe_route_backward(const moe_problem* problem, const moe_routing* routing, const void* logits,
                        const int32_t* ids, const float* dgates, void* dlogits, moe_stream_t stream);
 

@@ -181,6 +181,22 @@ def test_route_backward_ignores_bad_ids(moe):
 
 
 @pytest.mark.parametrize("score,renorm", FORMS)
+def test_route_gradient_over_its_logits(moe, score, renorm):
+    """dlogits may be logits itself: the same bits as in a buffer of its own."""
+    import torch
+    T, E, k = 301, 160, 6
+    logits = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    dg = torch.randn((T, k), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    for x in (logits, logits.to(torch.bfloat16)):
+        ids, _, dl = _run(moe, x, k, score, renorm, 1.5, None, dg)
+        prob = moe.Problem(T, 1024, k, E, 1, 1)
+        r = moe.Routing(moe.MOE_SCORE_SOFTMAX if score == "softmax" else moe.MOE_SCORE_SIGMOID, renorm, 1.5)
+        moe.moe_route_backward(prob, r, x, torch.from_numpy(ids).cuda(), dg, x)
+        torch.cuda.synchronize()
+        assert np.array_equal(x.float().cpu().numpy(), dl)
+
+
+@pytest.mark.parametrize("score,renorm", FORMS)
 def test_route_gradient_against_differences(moe, score, renorm):
     """dlogits is the slope of sum(gates * dgates) along a direction (central differences of the forward
     call's own gates; step 2^-6: the second-order term is below 2^-12 of the third derivative, at most 1)."""
