@@ -10,12 +10,13 @@
 // integer warp reductions.  Lane j keeps choice j, so the gates are one value a
 // lane.
 //
-// Instructions bound it, not the 4 E bytes a token.  Up to 256 experts every lane
-// sorts its (at most 8) keys once and a round takes the winner's head off; sorting
-// more costs more than the rounds save, so beyond that the winner looks through its
-// keys again.  16384 x 128, top-8: 7.8 us forward (searching lanes: 10.1 us; floor
-// 1.3 us) and 4.8 us backward; one token of 256 experts 2.2 us.  Eight lanes a token,
-// four tokens a warp, measured no faster.
+// Instructions bound it, not the 4 E bytes a token.  Every lane sorts its keys in
+// runs once, a round compares the runs' heads and takes the winner's off.  Up to 256
+// experts a lane has one run (16384 x 256, top-8: 11.5 us, 11.1 with runs of 4, but one token 2.2 us and
+// 2.4), beyond that runs of 4: sorting longer ones costs more than its rounds save, shorter ones leave
+// more heads to a round (16384 x 512, top-8: 17.3 us with runs of 4, 19.9 with 8, 21.2 with 2, and 26.3 when the
+// winner looks through its unsorted keys again).  16384 x 128, top-8: 7.8 us forward (floor 1.3 us) and
+// 4.8 us backward.  Eight lanes a token, four tokens a warp, measured no faster.
 //
 // Softmax sums, sigmoids and gradients are fp32 throughout; bf16 logits widen
 // exactly, and a bf16 gradient is rounded once, when it is stored.
@@ -113,13 +114,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
         id[i] = 32 * i + lane;
         key[i] = (int)id[i] < E ? key_of(a.bias != nullptr ? l[i] + a.bias[id[i]] : l[i]) : kTaken;
     }
-    constexpr bool kSorted = V <= 8;
-    if (kSorted) {
-        // neighbours change places only when the later one is larger: equal keys stay in the order of their ids
+    // runs, each sorted: neighbours change places only when the later one is larger, so equal keys stay in
+    // the order of their ids, and so do equal heads of the runs
+    constexpr int kRun = V <= 8 ? V : 4;
 #pragma unroll
-        for (int n = V - 1; n > 0; --n)
+    for (int r = 0; r < V; r += kRun)
 #pragma unroll
-            for (int i = 0; i < n; ++i)
+        for (int n = kRun - 1; n > 0; --n)
+#pragma unroll
+            for (int i = r; i < r + n; ++i)
                 if (key[i + 1] > key[i]) {
                     const unsigned k = key[i], e = id[i];
                     key[i] = key[i + 1];
@@ -127,38 +130,28 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
                     key[i + 1] = k;
                     id[i + 1] = e;
                 }
-    }
     int chosen = 0;
-    unsigned best = key[0], at = id[0];            // of this lane
     for (int j = 0; j < a.k; ++j) {
-        if (!kSorted && (j == 0 || at == kFull)) {
-            best = key[0];
-            at = id[0];
+        unsigned best = key[0], at = id[0];        // of this lane
 #pragma unroll
-            for (int i = 1; i < V; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = id[i];
-                }
-        }
+        for (int r = kRun; r < V; r += kRun)
+            if (key[r] > best) {
+                best = key[r];
+                at = id[r];
+            }
         const unsigned top = __reduce_max_sync(kFull, best);
         const unsigned won = __reduce_min_sync(kFull, best == top ? at : kFull);
         if (at == won) {
-            if (kSorted) {
 #pragma unroll
-                for (int i = 0; i + 1 < V; ++i) {
-                    key[i] = key[i + 1];
-                    id[i] = id[i + 1];
+            for (int r = 0; r < V; r += kRun)
+                if (V == kRun || id[r] == won) {
+#pragma unroll
+                    for (int i = r; i + 1 < r + kRun; ++i) {
+                        key[i] = key[i + 1];
+                        id[i] = id[i + 1];
+                    }
+                    key[r + kRun - 1] = kTaken;
                 }
-                key[V - 1] = kTaken;
-                best = key[0];
-                at = id[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (id[i] == won) key[i] = kTaken;
-                at = kFull;                        // looked up again before the next round
-            }
         }
         if (lane == j) chosen = (int)won;
     }

@@ -138,6 +138,24 @@ def test_route_ties_masks_and_empty_rows(moe, score, renorm):
     _check(moe, torch.from_numpy(rows).cuda(), k, score, renorm)
 
 
+@pytest.mark.parametrize("E,k", [(129, 32), (256, 32), (257, 8), (384, 32), (511, 16), (512, 32), (700, 32), (1024, 32)])
+def test_route_ties_of_many_experts(moe, E, k):
+    """Keys of few values, so that a lane's keys and those of other lanes tie all the time; choices from one lane's keys."""
+    import torch
+    rng = np.random.default_rng(E)
+    rows = rng.integers(0, 4, (40, E)).astype(np.float32)
+    rows[0] = 0.5
+    rows[1] = -np.inf
+    rows[2, :] = -np.inf
+    rows[2, E - k:] = 1.0
+    rows[3], rows[3, 5::32] = -2.0, np.arange(len(rows[3, 5::32]))        # lane 5 holds the largest, rising
+    rows[4], rows[4, 31::32] = -2.0, -np.arange(len(rows[4, 31::32])) + 9.0
+    rows[5], rows[5, ::32] = -2.0, 3.0
+    for score, renorm in (("softmax", True), ("sigmoid", False)):
+        _check(moe, torch.from_numpy(rows).cuda(), k, score, renorm)
+        _check(moe, torch.from_numpy(rows).cuda().to(torch.bfloat16), k, score, renorm)
+
+
 def test_route_nan_is_chosen_last(moe):
     import torch
     E, k = 40, 6
