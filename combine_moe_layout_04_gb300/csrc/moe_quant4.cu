@@ -8,9 +8,12 @@
 // saturated.
 //
 // HBM-bound: 64 bytes in, 17 out, per 32 columns: 32768 rows of 7168 columns in
-// 95 us (6.3 TB/s of 6.8), 128 rows in 6.7 us.  A block takes 128 rows of 1024
-// columns: smaller ones (32 rows: a tenth longer), blocks of 2048 columns (100 us)
+// 95 us (6.3 TB/s of 6.8), 128 rows in 6.7 us (4.7 in a run of such calls).  A block takes 128 rows of 1024
+// columns: smaller ones (32 rows: 96 us), blocks of 2048 columns (100 us)
 // or blocks that stay and take one piece after another (100 us) measured slower.
+// Where those would be few, though, and experts have some dozens of rows, four blocks share
+// one: 8192 rows of 8 experts take 26 us and not 38, 1840 rows of 16 experts, 2336 columns, 6.6 and not 11.5; with
+// one row of 128 experts (one block per expert and piece either way) it would be 10.7 and not 4.7 us, in a run of such calls.
 // Two lanes share a scale, 16 columns each (one 32-byte load), so a warp takes 512
 // columns of a row: 256 bytes of codes and four 4-byte words of scales.  With four
 // lanes a scale and 16-byte loads the warps' shuffles and index arithmetic,
@@ -103,7 +106,7 @@ __device__ __forceinline__ void quantise_piece(const uint16_t* row, bool wide, u
 // Rows are a multiple of 64 bytes, so all lie on 32 bytes where the first does.
 __device__ __forceinline__ bool on_32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
-// One block of the grid per (row block, piece of 1024 columns); the row blocks
+// One block of the grid per (row block, piece of 1024 columns, share of its rows); the row blocks
 // of the experts follow one another, and the grid covers the most there can be.
 __global__ void __launch_bounds__(kThreads)
 quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
@@ -121,7 +124,8 @@ quant4_rows_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
     const int groups = (a.K + 127) >> 7;
     uint8_t* sc = scales + (int64_t)block * groups * 512;
     const bool wide = on_32(a.rows);
-    for (int i = warp; i < n; i += kWarps) {
+    const int share = 128 / gridDim.z, from = blockIdx.z * share;
+    for (int i = from + warp; i < min(n, from + share); i += kWarps) {
         const int64_t r = x.first + i0 + i;
         quantise_piece(static_cast<const uint16_t*>(a.rows) + r * a.K, wide, codes + r * (a.K / 2), sc + scale_byte(i, 0),
                        blockIdx.y * kPiece, a.K, lane);
@@ -154,7 +158,9 @@ quant4_weights_kernel(ExpertArgs a, uint8_t* codes, uint8_t* scales) {
 }  // namespace
 
 cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s) {
-    const dim3 grid((unsigned)(a.R / 128 + min(a.E, a.R)), (unsigned)((a.K + kPiece - 1) / kPiece));
+    const int64_t blocks = a.R / 128 + min(a.E, a.R), pieces = (a.K + kPiece - 1) / kPiece;
+    const bool share = a.R >= 32 * (int64_t)a.E && blocks * pieces <= 8 * device_sm_count();
+    const dim3 grid((unsigned)blocks, (unsigned)pieces, share ? 4u : 1u);
     return launch_pdl(quant4_rows_kernel, grid, dim3(kThreads), 0, s, a, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
