@@ -67,6 +67,18 @@ def test_row_codes_and_scales_exact(moe, counts, K):
     assert torch.equal(unpack4(codes), want)
 
 
+@pytest.mark.parametrize("counts", [[0] * 20 + [1000, 3] + [0] * 18, [300, 0, 129, 31]])
+def test_blocks_of_rows_whole_and_shared(moe, counts):
+    """Few rows an expert on average, and one with many: a block takes 128 rows; many on average: four blocks share them."""
+    import torch
+    K = 1056
+    prob, lay = layout_of_counts(moe, counts)
+    rows = _wild(sum(counts), K, K)
+    codes, scales = _quant_rows(moe, prob, lay, rows)
+    want, byte = quantise4(rows)
+    assert torch.equal(row_scales(lay, scales, K)[:, : K // 32], byte) and torch.equal(unpack4(codes), want)
+
+
 @pytest.mark.parametrize("K", [32, 544, 1056, 2208])
 def test_rows_on_16_bytes_only(moe, K):
     """Rows that start 16 bytes past a 32-byte boundary: the same codes and scales."""
