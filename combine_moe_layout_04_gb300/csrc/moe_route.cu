@@ -73,9 +73,10 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&
 }
 
 // A gate's weight before scale, lane j's for choice j, from its logit v; all:
-// every logit of the row.  Returns w, and in *s the sigmoid.
+// every logit of the row.  Returns w, and in *rest 1 less the sigmoid: sigmoid(-v), because the
+// difference loses every digit that the gradient needs where the sigmoid nears 1 (1 % at a logit of 12, all at 17).
 template <int V>
-__device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all)[V], float v, bool on, float* s) {
+__device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all)[V], float v, bool on, float* rest) {
     if (a.score == MOE_SCORE_SOFTMAX) {
         float top = on ? v : -INFINITY, sum;
         if (a.renorm) {
@@ -92,10 +93,11 @@ __device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all
         }
         return on && sum != 0.0f ? soft(v, top) / sum : 0.0f;
     }
-    *s = on ? sigmoid(v) : 0.0f;
-    if (!a.renorm) return *s;
-    const float sum = warp_sum(*s);
-    return sum != 0.0f ? *s / sum : 0.0f;
+    const float s = on ? sigmoid(v) : 0.0f;
+    *rest = sigmoid(-v);
+    if (!a.renorm) return s;
+    const float sum = warp_sum(s);
+    return sum != 0.0f ? s / sum : 0.0f;
 }
 
 template <typename T, int V>
@@ -157,8 +159,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     }
     const float mine = lane < a.k ? widen(static_cast<const T*>(a.logits)[t * a.E + chosen]) : -INFINITY;
     const bool on = lane < a.k;
-    float s;
-    const float w = weight_of<V>(a, l, mine, on, &s);
+    float rest;
+    const float w = weight_of<V>(a, l, mine, on, &rest);
     if (on) {
         a.ids[t * a.k + lane] = chosen;
         a.gates[t * a.k + lane] = a.scale * w;
@@ -183,13 +185,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(RouteArgs
     if (!on) id = -1;
     const float v = on ? widen(row[id]) : -INFINITY;
     const float g = on ? a.scale * a.dgates[t * a.k + lane] : 0.0f;
-    float s = 0.0f;
-    const float w = weight_of<V>(a, l, v, on, &s);
+    float rest = 0.0f;
+    const float w = weight_of<V>(a, l, v, on, &rest);
     const float mean = warp_sum(w * g);
     if (!spread) {
-        float grad = g * s * (1.0f - s);
-        if (a.score == MOE_SCORE_SOFTMAX) grad = w * (g - mean);
-        else if (a.renorm) grad = w * (1.0f - s) * (g - mean);
+        float grad = w * (g - mean);
+        if (a.score == MOE_SCORE_SIGMOID) grad = w * rest * (a.renorm ? g - mean : g);
         __syncwarp();  // dlogits may lie over logits: every lane has read
 #pragma unroll
         for (int i = 0; i < V; ++i)

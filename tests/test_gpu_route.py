@@ -243,3 +243,50 @@ def test_route_gradient_against_differences(moe, score, renorm):
     # third-order remainder: |way|^3 / 6 times the third derivative, over at most E terms
     bound = (way.abs().double() ** 3).sum(1).cuda() * dg.abs().sum(1).double() * 4 + 1e-6
     assert torch.all(((slope - want).abs() <= bound) | ~same)
+
+
+# ---- sigmoid gates far out ----------------------------------------------------------
+#
+# The reference works with logarithms, so that nothing of it underflows or cancels: log s = -log(1 + exp(-v)),
+# 1 - s = exp(-log(1 + exp(v))).
+
+
+def _sigmoid_reference(x, ids, renorm, a):
+    v = np.take_along_axis(x.astype(np.float64), ids, 1)
+    log_s, rest = -np.logaddexp(0, -v), np.exp(-np.logaddexp(0, v))
+    w = np.exp(log_s - (np.logaddexp.reduce(log_s, axis=1, keepdims=True) if renorm else 0))
+    d, size = np.zeros_like(x, dtype=np.float64), np.zeros_like(x, dtype=np.float64)
+    mean, spread = ((w * a).sum(1, keepdims=True), np.abs(w * a).sum(1, keepdims=True)) if renorm else (0, 0)
+    np.put_along_axis(d, ids, w * rest * (a - mean), 1)
+    np.put_along_axis(size, ids, w * rest * (np.abs(a) + spread), 1)
+    return w, d, size
+
+
+def _check_sigmoid(moe, rows, k, renorm, what):
+    """Chosen by the largest logits; the bounds of _check, the gradient's with the slope in it."""
+    import torch
+    x = np.ascontiguousarray(rows, np.float32)
+    T, E = x.shape
+    dg = np.random.default_rng(T).standard_normal((T, k)).astype(np.float32)
+    ids, gates, dl = _run(moe, torch.from_numpy(x).cuda(), k, "sigmoid", renorm, 1.0, None, torch.from_numpy(dg).cuda())
+    assert np.array_equal(ids, np.argsort(-x, axis=1, kind="stable")[:, :k])
+    w, d, size = _sigmoid_reference(x, ids, renorm, dg.astype(np.float64))
+    rel = 2.0 ** -24 * (64 + 8 * min(128.0, float(np.abs(x).max())))
+    got, want, bound = (gates, w, rel * w + 1e-37) if what == "gates" else (dl, d, 4 * rel * size + 1e-37)
+    off = np.abs(got - want)
+    assert np.all(off <= bound), (float((off / np.maximum(bound, 1e-300)).max()), got[off > bound][:4], want[off > bound][:4])
+
+
+def _rows_up(E):
+    """Confident experts: logits of 8 to 30, alone or with low ones."""
+    rng = np.random.default_rng(8)
+    rows = rng.uniform(8, 30, (40, E))
+    rows[20:] = np.where(rng.random((20, E)) < 0.1, rows[20:], rng.uniform(-30, 0, (20, E)))
+    rows[0, :4] = 12.0, 15.0, 17.0, 29.0
+    return rows
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_gradient_of_confident_experts(moe, renorm):
+    """s (1 - s) where s is one but for its last bits: the slope keeps its relative accuracy."""
+    _check_sigmoid(moe, _rows_up(64), 6, renorm, "gradient")
