@@ -93,9 +93,14 @@ __device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all
         }
         return on && sum != 0.0f ? soft(v, top) / sum : 0.0f;
     }
-    const float s = on ? sigmoid(v) : 0.0f;
     *rest = sigmoid(-v);
-    if (!a.renorm) return s;
+    if (!a.renorm) return on ? sigmoid(v) : 0.0f;
+    // exp(min(v, 0)) / (1 + exp(-|v|)) is the sigmoid, and a common factor exp(-least) of the chosen ones leaves their
+    // shares as they are: with the largest min(v, 0) for `least` the sum never underflows, however low all of them are
+    // (magnitudes as integers order as the floats do; a NaN counts as 0 here and then makes the sum NaN)
+    const float low = fminf(v, 0.0f);
+    const float least = -__uint_as_float(__reduce_min_sync(kFull, on ? __float_as_uint(fabsf(low)) : 0x7f800000u));
+    const float s = on ? soft(low, least) / (1.0f + expf(-fabsf(v))) : 0.0f;
     const float sum = warp_sum(s);
     return sum != 0.0f ? s / sum : 0.0f;
 }

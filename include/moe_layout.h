@@ -471,7 +471,9 @@ typedef struct moe_routing {
  * key comes after every number, so the ids are always in range and distinct.
  * gates as moe_routing says, in fp32 from the logits without bias.  A chosen
  * logit of -infinity has weight 0, and a token whose chosen logits are all
- * -infinity has gates 0; a NaN or +infinity that a gate is made of gives NaN.
+ * -infinity has gates 0; renormalised sigmoids of finite logits share 1 however
+ * low all of them are.  A NaN that a gate is made of gives NaN, and so does
+ * +infinity under a softmax (the sigmoid of +infinity is 1).
  *   logits: [T, E] fp32 or bf16; bias: fp32 [E] or NULL;
  *   ids: int32 [T, k]; gates: fp32 [T, k]; k <= E. */
 int moe_route(const moe_problem* problem, const moe_routing* routing, const void* logits, const float* bias,

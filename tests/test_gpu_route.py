@@ -254,7 +254,8 @@ def test_route_gradient_against_differences(moe, score, renorm):
 def _sigmoid_reference(x, ids, renorm, a):
     v = np.take_along_axis(x.astype(np.float64), ids, 1)
     log_s, rest = -np.logaddexp(0, -v), np.exp(-np.logaddexp(0, v))
-    w = np.exp(log_s - (np.logaddexp.reduce(log_s, axis=1, keepdims=True) if renorm else 0))
+    w = np.exp(log_s - (log_s.max(axis=1, keepdims=True) if renorm else 0))
+    w = w / w.sum(axis=1, keepdims=True) if renorm else w
     d, size = np.zeros_like(x, dtype=np.float64), np.zeros_like(x, dtype=np.float64)
     mean, spread = ((w * a).sum(1, keepdims=True), np.abs(w * a).sum(1, keepdims=True)) if renorm else (0, 0)
     np.put_along_axis(d, ids, w * rest * (a - mean), 1)
@@ -290,3 +291,43 @@ def _rows_up(E):
 def test_sigmoid_gradient_of_confident_experts(moe, renorm):
     """s (1 - s) where s is one but for its last bits: the slope keeps its relative accuracy."""
     _check_sigmoid(moe, _rows_up(64), 6, renorm, "gradient")
+
+
+def _rows_down(E):
+    """Every logit so low that exp(-v) nears or passes the largest float: the chosen ones still share 1."""
+    rng = np.random.default_rng(9)
+    rows = rng.uniform(-120, -80, (40, E))
+    rows[0] = -95.0
+    rows[1] = -95.0 + 1e-3 * np.arange(E)
+    rows[2] = np.finfo(np.float32).min              # a whole row under a mask of the type's lowest value
+    rows[3] = -1e30
+    rows[4] = np.linspace(-90, -88, E)
+    rows[5] = np.linspace(-500, -100, E)
+    rows[6:12, ::3] = rng.uniform(-5, 30, rows[6:12, ::3].shape)
+    rows[12, :2] = 20.0, -87.0
+    return rows
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("what", ["gates", "gradient"])
+def test_sigmoid_gates_of_low_logits(moe, renorm, what):
+    _check_sigmoid(moe, _rows_down(70), 5, renorm, what)
+    _check_sigmoid(moe, _rows_up(64), 6, renorm, what)
+
+
+def test_sigmoid_of_infinities(moe):
+    """+infinity has a sigmoid of 1 (a share of it when renormalised), -infinity one of 0, and rows of -infinity have
+    gates 0; a NaN that is chosen makes the renormalised gates of its row NaN and no other."""
+    import torch
+    E, k, inf = 40, 3, np.inf
+    rows = np.full((5, E), -inf, np.float32)
+    rows[0, :2] = inf, 0.0
+    rows[1, :3] = inf, inf, -200.0
+    rows[3, 7] = -300.0
+    rows[4, :2], rows[4, 2:] = (-100.0, -101.0), np.nan
+    dg = torch.ones((5, k), device="cuda")
+    one = _run(moe, torch.from_numpy(rows).cuda(), k, "sigmoid", False, 1.0, None, dg)[1]
+    assert np.allclose(one[:4], [[1, 0.5, 0], [1, 1, 0], [0, 0, 0], [0, 0, 0]], rtol=1e-6, atol=0)
+    share = _run(moe, torch.from_numpy(rows).cuda(), k, "sigmoid", True, 1.0, None, dg)[1]
+    assert np.allclose(share[:4], [[2 / 3, 1 / 3, 0], [0.5, 0.5, 0], [0, 0, 0], [1, 0, 0]], rtol=1e-6, atol=0)
+    assert np.isnan(share[4]).all()
