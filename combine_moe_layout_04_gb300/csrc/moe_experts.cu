@@ -156,6 +156,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_second(bar, parity)) != 0;
 }
 
+// The same for barriers on which other CTAs arrive for memory that they hand over.
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, within(kSecond, [&] { return tc::try_wait_cluster(bar, parity); })) != 0;
+}
+
 // One tile of sums.
 struct Tile {
     int e;        // expert
@@ -332,7 +337,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     auto tell = [&] {
         tc::fence_before_sync();
         __syncwarp();
-        if ((tid & 31) == 0) tc::arrive_cluster(over);
+        if ((tid & 31) == 0) tc::arrive_cluster_tmem(over);
         told = true;
     };
     uint32_t v[kTurn];
@@ -355,7 +360,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         store_sync(group);
         if (SPLIT) {
             if (tid < link.parts)
-                tc::arrive_release_cluster(tc::in_rank(link.ready, 2 * tid + link.cta));
+                tc::arrive_cluster_smem(tc::in_rank(link.ready, 2 * tid + link.cta));
             if (tid == 0 && !within(kSecond, [&] { return tc::try_wait_cluster(link.ready, link.phase); })) link.ok = false;
             link.ok = store_all(group, link.ok);
             if (!link.ok) break;
@@ -574,15 +579,18 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             const uint32_t instr1 = tc::instruction_pair(n1, across_a, across_b);
             // this end is free when the tile before the last is stored, and what the last one holds of it when its store
             // half has been there
-            ok = warp_wait(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
+            ok = warp_wait_cluster(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
             if (ok && before + t.n > kTop<OP>)
-                ok = warp_wait(smem_u32(&sh.over[(n + 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
+                ok = warp_wait_cluster(smem_u32(&sh.over[(n + 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
             if (!ok) break;
             before = t.n;
             tc::fence_after_sync();
             const int begin = begin_of(t), end = end_of(t);
             for (int k0 = begin; k0 < end; k0 += kStep<OP>) {
-                if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
+                // a stage that the tail warps of both CTAs have cleared is theirs to hand over, any other the copies'
+                const bool cleared = OP == kBackWeights && t.length - k0 < kStep<OP> && (t.length & 15) != 0;
+                if (!(cleared ? warp_wait_cluster(full + 8 * ring.stage, ring.phase)
+                              : warp_wait(full + 8 * ring.stage, ring.phase))) {
                     ok = false;
                     break;
                 }
@@ -684,7 +692,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::arrive_cluster(tc::in_rank(smem_u32(&sh.free[n & 1]), lead));
+            if (lane == 0) tc::arrive_cluster_tmem(tc::in_rank(smem_u32(&sh.free[n & 1]), lead));
             t = next;
         }
         if (OP == kBackWeights && quarter * 32 + lane == 0) bulk_wait_all();
@@ -714,7 +722,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                                      :: "r"(stages + at * cut.bytes + k * kBoxBytes + j * 16), "r"(0u) : "memory");
                 asm volatile("fence.proxy.async;" ::: "memory");              // also for the first CTA's products
                 __syncwarp();
-                if (lane == 0) tc::arrive_cluster(full0 + 8 * at);
+                if (lane == 0) tc::arrive_cluster_smem(full0 + 8 * at);
             }
             stage = (stage + steps) % cut.stages;
         }
