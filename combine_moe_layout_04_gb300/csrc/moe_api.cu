@@ -143,6 +143,7 @@ int code_of_status(uint32_t bits) {
 int check_experts(const moe_experts* x, const Dims& d, int wide, moe::ExpertArgs* a) {
     if (x == nullptr || x->reserved != 0) return MOE_ERR_INVALID;
     if (x->act != MOE_ACT_NONE && x->act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID;
+    if (d.T * d.k > MOE_MAX_EXPERT_ROWS) return MOE_ERR_INVALID;
     if (x->in_cols < 8 || x->in_cols > MOE_MAX_HIDDEN || x->in_cols % wide != 0) return MOE_ERR_INVALID;
     if (x->out_cols < 8 || x->out_cols > MOE_MAX_HIDDEN || x->out_cols % 8 != 0) return MOE_ERR_INVALID;
     *a = moe::ExpertArgs{};
@@ -623,6 +624,7 @@ int moe_quant4_row_scale_bytes(const moe_problem* problem, int32_t cols, size_t*
     const int rc = check_problem(problem, &d);
     if (rc != MOE_OK) return rc;
     if (bytes == nullptr || cols < 32 || cols > MOE_MAX_HIDDEN || cols % 32 != 0) return MOE_ERR_INVALID;
+    if (d.T * d.k > MOE_MAX_EXPERT_ROWS) return MOE_ERR_INVALID;
     *bytes = scale_block_bytes((size_t)d.T * d.k / 128 + d.E, cols);
     return MOE_OK;
 }
@@ -647,6 +649,7 @@ int moe_quant4_rows(const moe_problem* problem, const moe_layout_t* layout, int3
     moe::ExpertArgs a{};
     int rc = check_problem(problem, &d);
     if (rc == MOE_OK && (cols < 32 || cols > MOE_MAX_HIDDEN || cols % 32 != 0)) rc = MOE_ERR_INVALID;
+    if (rc == MOE_OK && d.T * d.k > MOE_MAX_EXPERT_ROWS) rc = MOE_ERR_INVALID;
     if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
     if (rc != MOE_OK) return rc;
     if (d.T == 0) return MOE_OK;

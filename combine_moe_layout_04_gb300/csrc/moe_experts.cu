@@ -176,14 +176,16 @@ struct Plan {
     int features;  // in all
     int wide;      // of them in a tile
     int across;    // tiles of features
+    int columns;   // most rows of a tile
 };
 
 template <int OP, bool GLU>
-__device__ __forceinline__ Plan make_plan(const ExpertArgs& a, const int* base) {
+__device__ __forceinline__ Plan make_plan(const ExpertArgs& a, const Cut& cut, const int* base) {
     Plan p;
     p.features = OP == kBackWeights ? a.W : OP == kBackRows ? a.K : a.N;
     p.wide = GLU ? kHalf : 2 * kHalf;
     p.across = (p.features + p.wide - 1) / p.wide;
+    p.columns = cut.columns;
     p.tiles = (OP == kBackWeights ? (int64_t)a.E * ((a.K + kColumns - 1) / kColumns) : (int64_t)base[a.E]) * p.across;
     return p;
 }
@@ -207,7 +209,7 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& a, const Plan& p, cons
     total = OP == kBackWeights ? a.K : x.count;
     // equal tiles, in sixteens (in 4 bits by half blocks of scales, in the weights' gradient by the blocks it stores)
     constexpr int kUnit = OP == kForward4 ? 64 : OP == kBackWeights ? 32 : 16;
-    const int per = ((total + down - 1) / down + kUnit - 1) / kUnit * kUnit;
+    const int per = min(rows_of_tile(total, down, kUnit), p.columns);  // (more only where the count of tiles has hit its end)
     t.m0 = (j % down) * per;
     t.f0 = (j / down) * p.wide;
     t.rows = min(per, total - t.m0);
@@ -463,14 +465,14 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     // the kernel before may still be running until here
     pdl_wait();
     scan_row_blocks(a.count, a.offset, a.E, a.R, sh.base, sh.scratch,
-                    [&](int rows) { return (rows + cut.columns - 1) / cut.columns; }, sh.rows);
+                    [&](int rows) { return tiles_of(rows, cut.columns); }, sh.rows);
     if (k4) scan_row_blocks(a.count, a.offset, a.E, a.R, blocks, sh.scratch, blocks_of_128);
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    const Plan p = make_plan<OP, GLU>(a, sh.base);
+    const Plan p = make_plan<OP, GLU>(a, cut, sh.base);
     // the pairs (or the parts of a tile together) and the stages of this part
     const int64_t pair = (blockIdx.x >> 1) / parts, pairs = (gridDim.x >> 1) / parts;
     auto begin_of = [&](const Tile& t) {

@@ -507,9 +507,11 @@ int moe_route_backward(const moe_problem* problem, const moe_routing* routing, c
  *     gate rows, then the up rows;
  *   scales: the 4-bit weights' scale blocks, else NULL.
  * in_cols and out_cols: multiples of 8 in [8, 2^20]; in_cols a multiple of 32
- * for the 4-bit calls.  E * W < 2^31.  Every array 16-byte aligned; no output
+ * for the 4-bit calls.  E * W < 2^31; T*k <= MOE_MAX_EXPERT_ROWS, in these calls
+ * and the 4-bit ones below.  Every array 16-byte aligned; no output
  * overlaps an input or another output, in these calls and those below.
  * Products are summed in fp32 and rounded once to bf16. */
+#define MOE_MAX_EXPERT_ROWS 2147483136  /* 2^31 - 512 */
 #define MOE_ACT_NONE   0
 #define MOE_ACT_SWIGLU 1
 typedef struct moe_experts {

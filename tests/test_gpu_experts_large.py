@@ -119,3 +119,41 @@ def test_combine_gradient_past_32_bits(moe):
         a, b = dout[t].double(), y[pos].double()
         assert bool(((dw[t].double() - b @ a).abs() <= (b.abs() @ a.abs()) * (h / 256 + 24) * 2.0 ** -24).all())
     assert bool(torch.isfinite(dy[:: 997].float()).all())
+
+
+def test_rows_past_the_plain_sums_of_counts(moe):
+    """So many rows that the counts of tiles are added up with checks: rows at both ends of every expert."""
+    import torch
+    counts, K, N = [1, (1 << 26) - 70, 0, 131, 5], 32, 8
+    R, E = sum(counts), len(counts)
+    assert R >= 1 << 26
+    prob = moe.Problem(R, 1024, 1, E, 1, 1)
+    lay = moe.Layout.__new__(moe.Layout)            # the two arrays that the experts' calls read
+    lay.expert_count = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    lay.expert_offset = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    lay.expert_offset[1:] = lay.expert_count.cumsum(0)
+    lay.recv_src = torch.empty(0, device="cuda")
+    rows = torch.empty((R, K), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    w = moe.Experts(K, N, randn((E, N, K), 2, K ** -0.5))
+    out = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_forward(prob, lay, w, rows, out)
+    at, owner = _sample(R, lay)
+    for r in at:
+        a, b = rows[r].double(), w.weights[owner[r]].double()
+        close(out[r], b @ a, sum_slack(b.abs() @ a.abs(), K))
+    assert bool(torch.isfinite(out).all())
+    codes = torch.empty((R, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(moe.moe_quant4_row_scale_bytes(prob, K), dtype=torch.uint8, device="cuda")
+    moe.moe_quant4_rows(prob, lay, rows, codes, scales)
+    wc = torch.empty((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moe.moe_quant4_weight_scale_bytes(prob, w), dtype=torch.uint8, device="cuda")
+    moe.moe_quant4_weights(prob, w, wc, ws)
+    out.fill_(float("nan"))
+    moe.moe_expert_forward4(prob, lay, moe.Experts(K, N, wc, scales=ws), codes, scales, out)
+    want, byte = quantise4(rows[at])
+    assert torch.equal(unpack4(codes[at]), want)
+    value = values4(want, byte)
+    for i, r in enumerate(at):
+        b = values4(*quantise4(w.weights[owner[r]]))
+        close(out[r], b @ value[i], sum_slack(b.abs() @ value[i].abs(), K))
+    assert bool(torch.isfinite(out).all())
