@@ -57,6 +57,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "moe_clusters.cuh"
 #include "moe_experts.cuh"
 #include "moe_tc.cuh"
 
@@ -773,45 +774,21 @@ Cut make_cut(const ExpertArgs& a) {
     return cut;
 }
 
-// Clusters of this many pairs of CTAs that the current device runs at once (a cluster's CTAs share a processing cluster
-// of the GPU: GB300 holds 76, 36 and 15 of 1, 2 and 4 pairs, not 76, 38 and 19).
-template <typename K>
-int clusters(K* kern, int threads, int smem, int pairs) {
-    static std::mutex mu;
-    static std::unordered_map<int, int> known;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    std::lock_guard<std::mutex> lock(mu);
-    int& n = known[4 * dev + pairs / 2];
-    if (n == 0) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2 * pairs;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * pairs);
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = 1;
-    }
-    return n;
-}
-
 // Pairs that share a tile: the fewest rounds of tiles times stages of a round.  Sharing costs a round about as long as 14
 // stages (two meetings of the parts per 16 columns): one row of one expert, 7168 -> 2 x 1024 (8 tiles of 112 stages), takes
 // 17.4 us in four parts and 31.6 us in one; the same in 4 bits (28 stages) 15.2 us either way.
-template <typename K>
-int parts_of(K* split, int threads, int smem, int64_t tiles, int steps, int64_t pairs) {
+// *all: the teams of pairs that run at once; left alone where a tile is one pair's (so too where the device cannot say).
+int parts_of(const void* split, int threads, int smem, int64_t tiles, int steps, int64_t pairs, int64_t* all) {
     int best = 1;
     int64_t least = (tiles + pairs - 1) / pairs * steps;
     for (int parts = 2; parts <= 4 && steps > 28; parts *= 2) {
-        const int64_t teams = clusters(split, threads, smem, parts);
+        const int64_t teams = active_clusters(split, threads, smem, 2 * parts);
+        if (teams < 1) continue;
         const int64_t cost = (tiles + teams - 1) / teams * ((steps + parts - 1) / parts + 14);
         if (cost < least) {
             least = cost;
             best = parts;
+            *all = teams;
         }
     }
     return best;
@@ -873,9 +850,9 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
         e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
         if (e != cudaSuccess) return e;
         const int steps = ((OP == kBackRows ? a.W : a.K) + kStep<OP> - 1) / kStep<OP>;
-        cut.parts = parts_of(split, kThreads<OP>, kSmem<OP>, tiles, steps, pairs);
-        if (cut.parts > 1)
-            return start<OP>(split, a, cut, tiles, clusters(split, kThreads<OP>, kSmem<OP>, cut.parts), ma, mb, s);
+        int64_t teams = pairs;
+        cut.parts = parts_of(reinterpret_cast<const void*>(split), kThreads<OP>, kSmem<OP>, tiles, steps, pairs, &teams);
+        if (cut.parts > 1) return start<OP>(split, a, cut, tiles, teams, ma, mb, s);
     }
     return start<OP>(whole, a, cut, tiles, pairs, ma, mb, s);
 }
