@@ -22,8 +22,9 @@ built, every call raises ``MoeLibraryMissing``; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -278,32 +279,29 @@ class Problem:
             return self.hidden + 4 * (self.hidden // MOE_FP8_GROUP)
         return 2 * self.hidden
 
-    def __setattr__(self, name, value):
-        self.__dict__[name] = value
-        self.__dict__.pop("_sizes", None)
-
     def __getstate__(self):
-        return {name: value for name, value in self.__dict__.items() if name != "_sizes"}
+        return {name: value for name, value in self.__dict__.items() if name != "_kept"}
 
     def c(self) -> _ProblemC:
-        # a struct of sizes alone is made once and again when a field changes
-        pc = self.__dict__.get("_sizes")
-        if pc is not None:
+        now = _PROBLEM_FIELDS(self)
+        if now[8] is None and now[9] is None and now[10] is None:
+            # a struct of sizes alone is kept with the fields it was made from and what it then held: it serves again
+            # while the fields are the same, whoever set them, and nobody has edited it
+            kept = self.__dict__.get("_kept")
+            if kept is not None and kept[0] == now and bytes(kept[1]) == kept[2]:
+                return kept[1]
+            pc = _ProblemC(*now)
+            self.__dict__["_kept"] = (now, pc, bytes(pc))
             return pc
-        if self.expert_to_rank is None and self.src_rank_offsets is None and self.tuning is None:
-            pc = self.__dict__["_sizes"] = self._struct()
-            return pc
-        return self._struct()
-
-    def _struct(self) -> _ProblemC:
         # the struct keeps its tuning alive for as long as it is referenced
-        pc = _ProblemC(self.num_tokens, self.hidden, self.topk, self.num_experts, self.num_ranks,
-                       self.ranks_per_host, self.num_src_ranks, self.dtype,
-                       _ptr(self.expert_to_rank), _ptr(self.src_rank_offsets), None)
-        if self.tuning is not None:
-            pc._tuning = self.tuning.c()
+        pc = _ProblemC(*now[:8], _ptr(now[8]), _ptr(now[9]), None)
+        if now[10] is not None:
+            pc._tuning = now[10].c()
             pc.tuning = ctypes.pointer(pc._tuning)
         return pc
+
+
+_PROBLEM_FIELDS = operator.attrgetter(*[f.name for f in fields(Problem)])
 
 
 class Layout:

@@ -221,3 +221,33 @@ def test_problem_struct_follows_its_fields(moe):
         assert other == p and other.c().num_tokens == 64
         other.hidden = 2048
         assert p.c().hidden == 1024 and other.c().hidden == 2048
+
+
+def test_problem_struct_is_never_of_other_sizes(moe, monkeypatch):
+    """Fields set past the class, by another thread while the struct is made, and a struct that its holder edited:
+    the next call takes the problem's own fields."""
+    p = _p(moe)
+    p.c()
+    vars(p)["num_tokens"] = 32
+    assert p.c().num_tokens == 32
+    object.__setattr__(p, "num_tokens", 48)
+    assert p.c().num_tokens == 48
+    p.c().hidden = 8
+    p.c().tuning = ctypes.pointer(moe.Tuning(dispatch_sms=3).c())
+    assert p.c().hidden == 1024 and not p.c().tuning
+    make, other = moe._ProblemC, []
+
+    def meanwhile(*args):
+        pc = make(*args)
+        if not other:
+            other.append(1)
+            p.num_tokens = 64                       # what another thread may do here
+        return pc
+    p.num_tokens = 96
+    monkeypatch.setattr(moe, "_ProblemC", meanwhile)
+    p.c()
+    assert p.c().num_tokens == 64
+    p.num_tokens = 96
+    assert p.c().num_tokens == 96
+    with pytest.raises(AttributeError):             # not a field: computed from the others
+        p.num_hosts = 5
