@@ -240,18 +240,31 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None  # torch's own lookup of a device's current stream, without a Stream object around it
+# What calls ask torch for each time, looked up once: a device's current stream without a Stream object around it, the
+# current device without a look at whether CUDA is up, and whether there is one GPU, so that it need not be asked for.
+_raw_stream = _get_device = _one_gpu = None
+
+
+def _look_up():
+    global _raw_stream, _get_device, _one_gpu
+    import torch
+    _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _one_gpu = torch.cuda.device_count() == 1
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream) -> Optional[int]:
-    global _raw_stream
     if stream is None:
-        import torch
         if _raw_stream is None:
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-                lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+            _look_up()
+        return _raw_stream(0 if _one_gpu else _get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_current_gpu(t) -> bool:
+    on = t.get_device()  # -1 on the host
+    return on >= 0 and on == _get_device()
 
 
 @dataclass
@@ -388,6 +401,8 @@ class _Kinds(dict):
 
     def __missing__(self, kinds: str):
         import torch
+        if _raw_stream is None:
+            _look_up()
         found = self[kinds] = tuple(getattr(torch, n) for n in kinds.split("|"))
         return found
 
@@ -396,15 +411,16 @@ _KINDS = _Kinds()
 
 
 def _take(where: str, t, kinds: str, *shape):
-    """Address of a tensor argument that has to be dense, of one of these types
-    and (where given) of this shape."""
+    """Address of a tensor argument that has to be dense, on the current GPU, of
+    one of these types and (where given) of this shape."""
     try:
-        if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous():
+        if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous() and (
+                t.is_cuda if _one_gpu else _on_current_gpu(t)):
             return t.data_ptr()
     except AttributeError:  # NULL, or an object with nothing but an address
         return None if t is None else t.data_ptr()
-    raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {kinds} tensor {list(shape) or ''} is wanted, not "
-                                    f"{t.dtype} {list(t.shape)} with strides {list(t.stride())}")
+    raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {kinds} tensor {list(shape) or ''} on the current GPU is wanted, not "
+                                    f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
 
 def _check(rc: int, where: str):

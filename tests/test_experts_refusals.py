@@ -251,3 +251,89 @@ def test_problem_struct_is_never_of_other_sizes(moe, monkeypatch):
     assert p.c().num_tokens == 96
     with pytest.raises(AttributeError):             # not a field: computed from the others
         p.num_hosts = 5
+
+
+class On:
+    """A tensor-shaped stand-in on a GPU of this number: nothing behind its address is ever read."""
+
+    def __init__(self, dtype, *shape, gpu=0, dense=True):
+        self.dtype, self.shape, self.gpu, self.dense = dtype, tuple(shape), gpu, dense
+        self.device, self.is_cuda = f"cuda:{gpu}", True
+
+    def data_ptr(self):
+        return 0x20000
+
+    def get_device(self):
+        return self.gpu
+
+    def is_contiguous(self):
+        return self.dense
+
+    def stride(self):
+        return (1,) * len(self.shape)
+
+    def numel(self):
+        n = 1
+        for v in self.shape:
+            n *= v
+        return n
+
+
+@pytest.fixture
+def first_gpu(moe, monkeypatch):
+    """The current GPU is number 0 of several, whatever this machine has."""
+    moe._KINDS["float32"]  # (looked up with the types)
+    monkeypatch.setattr(moe, "_get_device", lambda: 0, raising=False)
+    monkeypatch.setattr(moe, "_one_gpu", False, raising=False)
+
+
+def _every_call(moe, p):
+    """(call, arguments of `make` for every tensor in its order, how to call it) of the router's, the experts' and the
+    combine gradient's calls, with good types and shapes."""
+    import torch
+    bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    T, k, E, h, R = 256, 2, 16, 1024, 512
+    lay, r = _lay(moe), moe.Routing()
+
+    def with_weights(call, kind, *dims, **kw):
+        return lambda w, *rest: call(p, lay, moe.Experts(64, 32, w, **kw), *rest, stream=0)
+    x = On(u8, 1 << 20)
+    return [
+        ((f32, T, E), (i32, T, k), (f32, T, k), (f32, E), lambda a, b, c, d: moe.moe_route(p, r, a, b, c, bias=d, stream=0)),
+        ((f32, T, E), (i32, T, k), (f32, T, k), (f32, T, E), lambda *t: moe.moe_route_backward(p, r, *t, stream=0)),
+        ((bf, T, h), (bf, R, h), (f32, T, k), (bf, R, h), (f32, T, k),
+         lambda *t: moe.moe_combine_backward(p, lay, *t, stream=0)),
+        ((bf, E, 32, 64), (bf, R, 64), (bf, R, 32), with_weights(moe.moe_expert_forward, bf)),
+        ((bf, E, 32, 64), (bf, R, 32), (bf, R, 64), with_weights(moe.moe_expert_backward_rows, bf)),
+        ((bf, R, 64), (bf, R, 32), (bf, E, 32, 64),
+         lambda *t: moe.moe_expert_backward_weights(p, lay, moe.Experts(64, 32), *t, stream=0)),
+        ((bf, R, 64), (u8, R, 32), (u8, 1 << 20), lambda *t: moe.moe_quant4_rows(p, lay, *t, stream=0)),
+        ((bf, E, 32, 64), (u8, E, 32, 32), (u8, 1 << 20),
+         lambda w, *t: moe.moe_quant4_weights(p, moe.Experts(64, 32, w), *t, stream=0)),
+        ((u8, E, 32, 32), (u8, R, 32), (u8, 1 << 20), (bf, R, 32), with_weights(moe.moe_expert_forward4, u8, scales=x)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_binding_refuses_tensors_that_are_not_on_the_current_gpu(moe, first_gpu, which):
+    import torch
+    *tensors, call = _every_call(moe, _p(moe))[which]
+    for i in range(len(tensors)):
+        for bad in (torch.zeros(tensors[i][1:], dtype=tensors[i][0]), On(*tensors[i], gpu=1)):
+            args = [On(*t) for t in tensors]
+            args[i] = bad
+            with pytest.raises(moe.MoeError) as ei:
+                call(*args)
+            assert ei.value.code == moe.MOE_ERR_INVALID and "current GPU" in str(ei.value), (i, str(ei.value))
+
+
+def test_one_gpu_takes_no_host_tensor(moe, first_gpu, monkeypatch):
+    import torch
+    monkeypatch.setattr(moe, "_one_gpu", True)
+    *tensors, call = _every_call(moe, _p(moe))[0]
+    for i in range(len(tensors)):
+        args = [On(*t) for t in tensors]
+        args[i] = torch.zeros(tensors[i][1:], dtype=tensors[i][0])
+        with pytest.raises(moe.MoeError) as ei:
+            call(*args)
+        assert ei.value.code == moe.MOE_ERR_INVALID and "current GPU" in str(ei.value)
