@@ -585,16 +585,29 @@ def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy,
     p, where = problem, "moe_combine_backward"
     slots = p.num_tokens * p.topk
     _check((_lib or load_library()).moe_combine_backward(
-        ctypes.byref(p.c()), ctypes.byref(_LayoutC(pos=layout.pos.data_ptr())),
+        ctypes.byref(p.c()), ctypes.byref(_LayoutC(pos=_take_ints(where, layout.pos, "pos", slots))),
         _take(where, dout, "bfloat16", p.num_tokens, p.hidden),
         _take(where, y, "bfloat16", slots, p.hidden), _take(where, weights, "float32", p.num_tokens, p.topk),
         _take(where, dy, "bfloat16", slots, p.hidden), _take(where, dweights, "float32", p.num_tokens, p.topk),
         _stream(stream)), where)
 
 
-def _groups(layout) -> _LayoutC:
+def _take_ints(where: str, t, name: str, size: int):
+    """Address of a layout's array: dense int32 on the current GPU, `size` long at least."""
+    try:
+        if t.numel() >= size and t.dtype is _KINDS["int32"][0] and t.is_contiguous() and (
+                t.is_cuda if _one_gpu else _on_current_gpu(t)):
+            return t.data_ptr()
+    except AttributeError:  # an object with nothing but an address
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID, f"{where}: the layout's {name} has to be dense int32 on the current GPU, {size} values "
+                                    f"or more, not {t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
+
+
+def _groups(where: str, p: Problem, layout) -> _LayoutC:
     """The two layout arrays that the experts' calls read (the struct's first two fields)."""
-    return _LayoutC(layout.expert_count.data_ptr(), layout.expert_offset.data_ptr())
+    return _LayoutC(_take_ints(where, layout.expert_count, "expert_count", p.num_experts),
+                    _take_ints(where, layout.expert_offset, "expert_offset", p.num_experts + 1))
 
 
 def _take_weights(where: str, p: Problem, x: Experts):
@@ -608,7 +621,7 @@ def moe_expert_forward(problem: Problem, layout: Layout, experts: Experts, rows,
     p, x, where = problem, experts, "moe_expert_forward"
     slots = p.num_tokens * p.topk
     _check((_lib or load_library()).moe_expert_forward(
-        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), _take_weights(where, p, x),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, pre, "bfloat16", slots, x.weight_rows),
         _take(where, out, "bfloat16", slots, x.out_cols), _stream(stream)), where)
 
@@ -619,7 +632,7 @@ def moe_expert_backward_rows(problem: Problem, layout: Layout, experts: Experts,
     p, x, where = problem, experts, "moe_expert_backward_rows"
     slots, wide = p.num_tokens * p.topk, x.in_cols * (1 if pre is None else 2)
     _check((_lib or load_library()).moe_expert_backward_rows(
-        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), _take_weights(where, p, x),
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), _take_weights(where, p, x),
         _take(where, dout, "bfloat16", slots, x.weight_rows), _take(where, pre, "bfloat16", slots, wide),
         _take(where, drows, "bfloat16", slots, wide), _stream(stream)), where)
 
@@ -629,7 +642,7 @@ def moe_expert_backward_weights(problem: Problem, layout: Layout, experts: Exper
     p, x, where = problem, experts, "moe_expert_backward_weights"
     slots = p.num_tokens * p.topk
     _check((_lib or load_library()).moe_expert_backward_weights(
-        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), ctypes.byref(x.c()),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, dout, "bfloat16", slots, x.weight_rows),
         _take(where, dweights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols), _stream(stream)), where)
 
@@ -670,9 +683,12 @@ def _take_bytes(where: str, t, size: int):
 def moe_quant4_rows(problem: Problem, layout: Layout, rows, codes, scales, stream=None):
     """Receive rows bf16 [T*k, cols] to 4-bit codes [T*k, cols / 2] and scale blocks."""
     p, where = problem, "moe_quant4_rows"
-    slots, cols = p.num_tokens * p.topk, 2 * int(codes.shape[1])
+    shape = getattr(codes, "shape", ())
+    if len(shape) != 2:
+        raise MoeError(MOE_ERR_INVALID, f"{where}: codes are [T*k, cols / 2], not {list(shape)}")
+    slots, cols = p.num_tokens * p.topk, 2 * int(shape[1])
     _check((_lib or load_library()).moe_quant4_rows(
-        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), cols, _take(where, rows, "bfloat16", slots, cols),
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), cols, _take(where, rows, "bfloat16", slots, cols),
         _take(where, codes, "uint8", slots, cols // 2),
         _take_bytes(where, scales, _row_scale_bytes(p, cols)), _stream(stream)), where)
 
@@ -695,7 +711,7 @@ def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, code
     if x.scales is not None:
         _take_bytes(where, x.scales, _weight_scale_bytes(p, x))
     _check((_lib or load_library()).moe_expert_forward4(
-        ctypes.byref(p.c()), ctypes.byref(_groups(layout)), ctypes.byref(x.c()),
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), ctypes.byref(x.c()),
         _take(where, codes, "uint8", slots, x.in_cols // 2),
         _take_bytes(where, scales, _row_scale_bytes(p, x.in_cols)),
         _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),

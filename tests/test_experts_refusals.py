@@ -337,3 +337,45 @@ def test_one_gpu_takes_no_host_tensor(moe, first_gpu, monkeypatch):
         with pytest.raises(moe.MoeError) as ei:
             call(*args)
         assert ei.value.code == moe.MOE_ERR_INVALID and "current GPU" in str(ei.value)
+
+
+def _layout_calls(moe, p):
+    """The calls that read a layout's arrays, with good tensors: call(layout)."""
+    import torch
+    bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    w, rows, out = On(bf, 16, 32, 64), On(bf, 512, 64), On(bf, 512, 32)
+    x, x4 = moe.Experts(64, 32, w), moe.Experts(64, 32, On(u8, 16, 32, 32), scales=On(u8, 1 << 20))
+    codes, scales, gates, wide = On(u8, 512, 32), On(u8, 1 << 20), On(f32, 256, 2), On(bf, 512, 1024)
+    groups = [lambda l: moe.moe_expert_forward(p, l, x, rows, out, stream=0),
+              lambda l: moe.moe_expert_backward_rows(p, l, x, out, rows, stream=0),
+              lambda l: moe.moe_expert_backward_weights(p, l, x, rows, out, w, stream=0),
+              lambda l: moe.moe_quant4_rows(p, l, rows, codes, scales, stream=0),
+              lambda l: moe.moe_expert_forward4(p, l, x4, codes, scales, out, stream=0)]
+    return groups, lambda l: moe.moe_combine_backward(p, l, On(bf, 256, 1024), wide, gates, wide, gates, stream=0)
+
+
+def test_binding_refuses_layouts_of_other_problems(moe, first_gpu):
+    """A layout array that is too short, of another type, with gaps or not on this GPU is not read."""
+    import torch
+    p, i32 = _p(moe), torch.int32
+    groups, combine = _layout_calls(moe, p)
+
+    def refused(call, **arrays):
+        good = dict(expert_count=On(i32, 16), expert_offset=On(i32, 17), pos=On(i32, 256, 2))
+        with pytest.raises(moe.MoeError) as ei:
+            call(_lay(moe, **{**good, **arrays}))
+        assert ei.value.code == moe.MOE_ERR_INVALID, arrays
+    for name, n in (("expert_count", 16), ("expert_offset", 17)):
+        for bad in (On(i32, n - 1), On(torch.int64, n), On(i32, n, dense=False), On(i32, n, gpu=1),
+                    torch.zeros(n, dtype=i32)):
+            for call in groups:
+                refused(call, **{name: bad})
+    for bad in (On(i32, 255, 2), On(torch.int64, 256, 2), On(i32, 256, 2, dense=False), torch.zeros((256, 2), dtype=i32)):
+        refused(combine, pos=bad)
+
+
+def test_binding_refuses_codes_that_are_no_matrix(moe, first_gpu):
+    import torch
+    p, rows, scales = _p(moe), On(torch.bfloat16, 512, 64), On(torch.uint8, 1 << 20)
+    for codes in (None, On(torch.uint8, 512 * 32), On(torch.uint8, 512, 32, 1)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant4_rows, p, _lay(moe), rows, codes, scales)
