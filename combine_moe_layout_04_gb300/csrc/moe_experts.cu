@@ -266,7 +266,7 @@ struct Link {
     uint32_t ready, seen;              // barriers of this store group
     uint32_t phase;                    // of both
     int part, parts, cta;
-    bool ok, empty;                    // empty: this part has no stage of the tile
+    bool ok;
 };
 // 8 floats of a turned row, added up over the parts of the tile in their order.
 __device__ __forceinline__ void summed8(const float* p, const Link& link, float (&v)[8]) {
@@ -349,10 +349,6 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         const int c = column(b);
         if (!told && b >= shared) tell();
         tc::wait_ld();
-        if (SPLIT && link.empty) {
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) v[i] = 0;
-        }
         if (SPLIT) {
             // the block before has been read by all parts
             if (tid == 0 && !within(kSecond, [&] { return tc::try_wait_cluster(link.seen, link.phase ^ 1u); })) link.ok = false;
@@ -665,7 +661,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
-        Link link{smem_u32(&sh.ready[group]), smem_u32(&sh.seen[group]), 0, part, parts, cta, true, false};
+        Link link{smem_u32(&sh.ready[group]), smem_u32(&sh.seen[group]), 0, part, parts, cta, true};
         Tile t{};
         if (pair < p.tiles) t = tile_at<OP, GLU>(a, p, sh, pair);
         for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
@@ -685,7 +681,6 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             if constexpr (OP == kBackWeights) {
                 store_weights(p, t, &maps.out, sums, smem_u32(turn) + group * 32 * kHalf * 2, cta, group, quarter * 32 + lane);
             } else {
-                if (SPLIT) link.empty = begin_of(t) >= end_of(t);
                 store_tile<OP, GLU, SPLIT>(a, p, t, sums, mine, cta, group, quarter * 32 + lane, (n & 1) != 0, shared,
                                            tc::in_rank(smem_u32(&sh.over[n & 1]), lead), link);
                 if (SPLIT && !link.ok) {
@@ -777,11 +772,14 @@ Cut make_cut(const ExpertArgs& a) {
 // Pairs that share a tile: the fewest rounds of tiles times stages of a round.  Sharing costs a round about as long as 14
 // stages (two meetings of the parts per 16 columns): one row of one expert, 7168 -> 2 x 1024 (8 tiles of 112 stages), takes
 // 17.4 us in four parts and 31.6 us in one; the same in 4 bits (28 stages) 15.2 us either way.
+// Shorter contractions are never shared, so that every part has stages of its own.
 // *all: the teams of pairs that run at once; left alone where a tile is one pair's (so too where the device cannot say).
+constexpr int kLeastShared = 29, kMostParts = 4;
+static_assert(kLeastShared >= kMostParts);
 int parts_of(const void* split, int threads, int smem, int64_t tiles, int steps, int64_t pairs, int64_t* all) {
     int best = 1;
     int64_t least = (tiles + pairs - 1) / pairs * steps;
-    for (int parts = 2; parts <= 4 && steps > 28; parts *= 2) {
+    for (int parts = 2; parts <= kMostParts && steps >= kLeastShared; parts *= 2) {
         const int64_t teams = active_clusters(split, threads, smem, 2 * parts);
         if (teams < 1) continue;
         const int64_t cost = (tiles + teams - 1) / teams * ((steps + parts - 1) / parts + 14);
