@@ -153,8 +153,8 @@ __device__ __forceinline__ Boxes boxes_of(const Maps& maps, int rows) {
 }
 
 // A bounded wait of a whole warp: it gives up together.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_second(bar, parity)) != 0;
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns = kSecond) {
+    return __all_sync(0xffffffffu, wait_second(bar, parity, limit_ns)) != 0;
 }
 
 // The same for barriers on which other CTAs arrive for memory that they hand over.
@@ -179,6 +179,13 @@ struct Plan {
     int across;    // tiles of features
     int columns;   // most rows of a tile
 };
+
+// How long the end of a contraction of so many stages is waited for: the weights' gradient sums over an expert's rows, of
+// which there may be so many that this takes seconds (0.23 us a stage; other contractions have 2^14 stages at most).
+template <int OP>
+__device__ __forceinline__ uint64_t limit_of(int64_t stages) {
+    return OP == kBackWeights ? kSecond + 4000ull * stages : kSecond;
+}
 
 template <int OP, bool GLU>
 __device__ __forceinline__ Plan make_plan(const ExpertArgs& a, const Cut& cut, const int* base) {
@@ -671,7 +678,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             // One warp of a group watches the sums' barrier, the others sleep at the group's own: sixteen watching
             // warps would take issue slots from the two that feed the tensor core.  A group gives up together.
             const bool got = ((warp - 2) & 3) != 0 ||
-                             wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1));
+                             wait_second(smem_u32(&sh.done[n & 1]), (uint32_t)((n >> 1) & 1),
+                                         limit_of<OP>(t.length / kStep<OP>));
             if (!store_all(group, got)) {
                 ok = false;
                 break;
@@ -702,16 +710,19 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         const uint32_t full0 = tc::in_rank(full, lead);
         uint32_t phases = 0;           // of the tail barriers, a bit each
         int stage = 0;
+        int64_t since = 0;             // stages after the last one that was waited for here
         for (int64_t i = pair; i < p.tiles; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const int steps = (t.length + kStep<OP> - 1) / kStep<OP>;
+            since += steps;
             if ((t.length & 15) != 0) {
                 const int at = (stage + steps - 1) % cut.stages;
-                if (!warp_wait(smem_u32(&sh.tail[at]), (phases >> at) & 1)) {
+                if (!warp_wait(smem_u32(&sh.tail[at]), (phases >> at) & 1, limit_of<OP>(since))) {
                     ok = false;
                     break;
                 }
                 phases ^= 1u << at;
+                since = 0;
                 const int left = t.length - (steps - 1) * kStep<OP>;
                 const int from = left * 8, to = ((left + 15) & ~15) * 8;      // 16-byte pieces of a box
                 for (int k = 0; k < cut.bytes / kBoxBytes; ++k)

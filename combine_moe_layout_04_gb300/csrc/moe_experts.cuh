@@ -22,8 +22,8 @@ __device__ __forceinline__ bool within(uint64_t limit_ns, F attempt) {
     }
 }
 constexpr uint64_t kSecond = 1000000000ull;
-__device__ __forceinline__ bool wait_second(uint32_t bar, uint32_t parity) {
-    return within(kSecond, [&] { return mbar_try_wait(bar, parity); });
+__device__ __forceinline__ bool wait_second(uint32_t bar, uint32_t parity, uint64_t limit_ns = kSecond) {
+    return within(limit_ns, [&] { return mbar_try_wait(bar, parity); });
 }
 
 // Rows of one expert, kept inside [0, R) whatever the layout holds.

@@ -157,3 +157,25 @@ def test_rows_past_the_plain_sums_of_counts(moe):
         b = values4(*quantise4(w.weights[owner[r]]))
         close(out[r], b @ value[i], sum_slack(b.abs() @ value[i].abs(), K))
     assert bool(torch.isfinite(out).all())
+
+
+def test_weight_gradient_of_experts_that_take_seconds(moe):
+    """Experts whose sums over their rows take longer than a second (0.23 us for 64 rows): nothing that waits for them
+    gives up, nor what waits for a later expert on the same SMs (77 experts, a tile each, on at most 76 pairs of SMs)."""
+    import torch
+    counts, K = [300_000_000, 300_000_003] + [0] * 73 + [7, 5], 8
+    R, E = sum(counts), len(counts)
+    prob = moe.Problem(R, 1024, 1, E, 1, 1)
+    lay = moe.Layout.__new__(moe.Layout)
+    lay.expert_count = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    lay.expert_offset = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    lay.expert_offset[1:] = lay.expert_count.cumsum(0)
+    rows, dout = (torch.zeros((R, K), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    at = torch.tensor([0, 63, 64, 1 << 20, (1 << 28) + 1, counts[0] - 70, counts[0] - 1], device="cuda")
+    rows[at], dout[at], rows[counts[0] + at], dout[counts[0] + at] = 2.0, 1.0, 3.0, 1.0
+    rows[R - 12:], dout[R - 12:] = 1.0, 5.0
+    dw = torch.full((E, K, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.moe_expert_backward_weights(prob, lay, moe.Experts(K, K), rows, dout, dw)
+    assert moe.moe_move_faults() == 0
+    for e, want in ((0, 2 * len(at)), (1, 3 * len(at)), (2, 0), (E - 2, 35), (E - 1, 25)):
+        assert bool((dw[e] == want).all()), e
