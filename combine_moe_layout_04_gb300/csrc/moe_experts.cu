@@ -749,20 +749,25 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 }
 
 // The cut of a launch, from the mean rows of an expert (all the host knows of them); routing spreads an expert's rows by
-// about the square root of their mean, and 3.5 of that hold almost all experts.
+// about the square root of their mean, and 3.5 of that hold almost all experts.  The bounds below were each timed on both
+// sides for four widths, 8 and 32 experts, even routing and one whose experts' shares fall as rank^-0.4 (in brackets).
 //  * A tile that takes all rows of its expert reads the weights once, and the narrower it is the more stages are in
 //    flight: 2 rows an expert (64 experts, 7168 -> 2 x 2048) take 528 us with 64 columns, 548 with 256, 588 with 512; but
 //    128 rows take 677 us cut at 64 columns and 582 us cut at 256.
-//  * Tiles of more than 256 columns win where they save one: 272 rows take 682 us cut at 320 and 858 us cut at 256, 360
-//    rows (32 experts) 421 us at 384 and 478 at 256, 600 rows (7168 -> 2048) 333 us at 320 and 387 at 256.
+//  * Tiles of more than 256 columns win where they save one: 272 rows take 682 us cut at 320 and 858 us cut at 256, 600
+//    rows (32 experts) 702 us at 320 and 773 at 256 [747 and 744].
+//  * 384 columns win where most experts fit them and not 320 (32 experts, 384 against 320): 305 rows take 399 and 406 us
+//    [461 and 447], 312 rows 406 and 433 [444 and 440], 330 rows 429 and 490 [480 and 448], 360 rows 450 and 525 [491 and
+//    488], 375 rows 486 and 521 [530 and 512], 400 rows 594 and 540 [537 and 521].  Over all widths they take 0.91 of the
+//    time at 312 to 360 rows [1.02], and 1.07 on either side [1.06].
 //  * Many tiles an expert waste little of either, and 256 columns issue fewer instructions: 3000 rows (8 experts) take
-//    388 us at 256 and 406 at 320; 1040 rows 594 and 600.
-//  * In 4 bits tensor memory also holds scales, so the next tile's sums wait for most of a wide one's store half; wide tiles
-//    pay where they save one of two or of four (7168 -> 2 x 2048): 256 rows (32 experts) take 116 us cut at 384 and 129 at
-//    256, 340 rows 133 and 152, but 400 rows 172 and 159, 700 rows 239 and 234; 850 rows (16 experts) 150 and 159.  Three
-//    for four and a half, at 1024 rows, pay where the contraction is long and rounds of tiles are many: 32 experts 326 us
-//    cut at 384 and 337 at 256, 16 experts 176 and 175; 32 experts with 4096 columns 224 and 224, with 2048 158 and 151.
-//    1300 rows (16 experts) take 230 and 222; 170 rows 129 cut at 128 and 97 at 256.
+//    388 us at 256 and 406 at 320; 1040 rows 594 and 600.  Over all widths 320 columns take 0.99 to 1.02 of 256's time at 700 to
+//    900 rows [0.97 to 1.03] and 0.99 to 1.06 from 950 up [0.98 to 1.06].
+//  * In 4 bits tensor memory also holds scales, so the next tile's sums wait for most of a wide one's store half; 384 columns
+//    pay where they take all rows in one tile or in three (7168 -> 2 x 2048, 32 experts, 384 against 256): 260 rows 131 and
+//    145 us, 360 rows 150 and 172, 400 rows 178 and 174, 700 rows 253 and 254, 800 rows 281 and 312, 1024 rows 340 and 355,
+//    1150 rows 379 and 383, 1300 rows 449 and 447.  Over all widths one tile of 384 takes 0.89 of the time of 256 [0.97],
+//    three 0.987 of four or five [1.004], and those between 1.017 [1.018].  170 rows (16 experts) take 129 us cut at 128 and 97 at 256.
 //    The stages in flight count: 384 columns take 330 us with four and 353 with three (1024 rows), 256 columns 129 with five
 //    and 142 with four (256 rows).
 template <int OP>
@@ -771,9 +776,8 @@ Cut make_cut(const ExpertArgs& a) {
     Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
-        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 330 && mean <= 365 ? 384 : 320;
-        const bool many = a.K >= 24 * kStep<kForward4> && (int64_t)a.E * a.N >= (a.glu ? 400 : 800) * kHalf;
-        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean < (many ? 1200 : 900)))) cut.columns = 384;
+        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
+        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
     cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
