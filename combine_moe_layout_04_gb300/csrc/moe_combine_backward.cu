@@ -6,7 +6,7 @@
 // HBM-bound: per token it reads one row and k rows and writes k rows, 4 flops
 // an element: 16384 tokens, top-8, h = 7168 (4.0 GB) take 588 us, 6.78 TB/s, what a
 // plain copy moves.  A block owns a token, so that dout is read once and the dot
-// products end in the block, in an order that only the sizes fix: a thread takes
+// products end in the block, in an order that the sizes and the device's SMs fix: a thread takes
 // every THREADS-th group of 8 columns, then come the lanes, then the warps.  Two,
 // four or eight slots' loads are issued together, by the least that takes k: registers for slots that are not
 // there would leave room for fewer blocks (16384 tokens, h = 7168: top-1 105 us with two slots and 165 with eight, top-2

@@ -36,11 +36,14 @@
 // each over its part of the contraction, and its CTAs' store halves add the parts up
 // through distributed shared memory, in part order.
 //
-// What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows: the stages, which arrive at 52 to
-// 54 bytes a clock and SM whatever the tile (16 KB of weights and 16 KB of rows against 512 clocks of products for 256
+// What bounds it.  Few rows an expert: HBM (the weights arrive at 7.0 TB/s).  Many rows, forward: the stages, which arrive
+// at up to 54 bytes a clock and SM (16 KB of weights and 16 KB of rows against 512 clocks of products for 256
 // columns), and then the power limit: 1024 rows of 32 experts, 7168 -> 2048, run at 1800 TFLOP/s in a burst (the
-// library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  In 4 bits a stage is 35 KB for the same 512
-// clocks: 6 PFLOP/s, a stage in some 740 clocks, and in 620 with a quarter of its products.  It is not L2: two pairs
+// library's plain bf16 product: 1920) and 1.4 PFLOP/s in a long run (1690).  Over a whole launch of a few rounds of tiles
+// the other products are at neither bound: 44 bytes a clock and SM and 67 % of the tensor pipe for the rows' gradient (which
+// reads and writes (g, u) besides), 45 and 71 % for the weights' gradient, 31 and 51 % in 4 bits, where a stage of 256
+// columns is 35 KB for 512 clocks: a stage in some 740 clocks, and in 620 with a quarter of its products.  What
+// holds the stages back was looked for and not found.  It is not L2: two pairs
 // that share their rows by multicast, a quarter fewer bytes out of L2, fill their stages no faster (and clusters of four
 // CTAs leave 8 SMs idle: 681 -> 705 us at 272 rows of 64 experts).  Nor is it one warp's issuing: a second copying warp
 // changed nothing in 4 bits.  Keeping the weights beside the tensor core between the two products of a wide tile did not
@@ -749,8 +752,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 }
 
 // The cut of a launch, from the mean rows of an expert (all the host knows of them); routing spreads an expert's rows by
-// about the square root of their mean, and 3.5 of that hold almost all experts.  The bounds below were each timed on both
-// sides for four widths, 8 and 32 experts, even routing and one whose experts' shares fall as rank^-0.4 (in brackets).
+// about the square root of their mean, and 3.5 of that hold almost all experts.  The bounds above 256 rows were each timed
+// on both sides for three to four widths, 8 and 32 experts, even routing and one whose experts' shares fall as rank^-0.4 (in brackets).
 //  * A tile that takes all rows of its expert reads the weights once, and the narrower it is the more stages are in
 //    flight: 2 rows an expert (64 experts, 7168 -> 2 x 2048) take 528 us with 64 columns, 548 with 256, 588 with 512; but
 //    128 rows take 677 us cut at 64 columns and 582 us cut at 256.
@@ -786,8 +789,9 @@ Cut make_cut(const ExpertArgs& a) {
 
 // Pairs that share a tile: the fewest rounds of tiles times stages of a round.  Sharing costs a round about as long as 14
 // stages (two meetings of the parts per 16 columns): one row of one expert, 7168 -> 2 x 1024 (8 tiles of 112 stages), takes
-// 17.4 us in four parts and 31.6 us in one; the same in 4 bits (28 stages) 15.2 us either way.
-// Shorter contractions are never shared, so that every part has stages of its own.
+// 13.6 us in four parts, 19.1 in two and 28.4 in one, 300 rows 31.1, 36.6 and 42.9.  Contractions of 28 stages and fewer
+// are never shared, so that every part has stages of its own (one row of one expert, 28 stages: 9.1 us in four parts and
+// 10.9 in one, in 4 bits 12.6 and 15.0: there is something left here).
 // *all: the teams of pairs that run at once; left alone where a tile is one pair's (so too where the device cannot say).
 constexpr int kLeastShared = 29, kMostParts = 4;
 static_assert(kLeastShared >= kMostParts);

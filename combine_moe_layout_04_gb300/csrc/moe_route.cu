@@ -16,7 +16,7 @@
 // 2.4), beyond that runs of 4: sorting longer ones costs more than its rounds save, shorter ones leave
 // more heads to a round (16384 x 512, top-8: 17.3 us with runs of 4, 19.9 with 8, 21.2 with 2, and 26.3 when the
 // winner looks through its unsorted keys again).  16384 x 128, top-8: 7.8 us forward (floor 1.3 us) and
-// 4.8 us backward.  Eight lanes a token, four tokens a warp, measured no faster.
+// 4.8 us backward, with renormalised sigmoids 8.1 and 5.0.  Eight lanes a token, four tokens a warp, measured no faster.
 //
 // Softmax sums, sigmoids and gradients are fp32 throughout; bf16 logits widen
 // exactly, and a bf16 gradient is rounded once, when it is stored.

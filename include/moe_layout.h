@@ -510,7 +510,8 @@ int moe_route_backward(const moe_problem* problem, const moe_routing* routing, c
  * for the 4-bit calls.  E * W < 2^31; T*k <= MOE_MAX_EXPERT_ROWS, in these calls
  * and the 4-bit ones below.  Every array 16-byte aligned; no output
  * overlaps an input or another output, in these calls and those below.
- * Products are summed in fp32 and rounded once to bf16. */
+ * Products are summed in fp32, in an order that the sizes, the counts of rows and
+ * the device fix, and rounded once to bf16. */
 #define MOE_MAX_EXPERT_ROWS 2147483136  /* 2^31 - 512 */
 #define MOE_ACT_NONE   0
 #define MOE_ACT_SWIGLU 1
@@ -555,7 +556,7 @@ int moe_expert_backward_weights(const moe_problem* problem, const moe_layout_t* 
  * sum; the pages have no counterpart of its gradient):
  *   dy[pos[t, j]] = bf16_rne(weights[t, j] * dout[t]),
  *   dweights[t, j] = sum over the columns of dout[t] * y[pos[t, j]], fp32, in
- *   an order that depends on the sizes only.
+ *   an order that depends on the sizes and the device's number of SMs only.
  *   dout: bf16 [T, h]; y, dy: bf16 [T*k, h]; weights, dweights: fp32 [T, k].
  * Row buffers 16-byte aligned.  Only pos is read from the layout; a position
  * out of [0, T*k) is skipped (its dweights is 0). */
