@@ -9,13 +9,13 @@ mirror the C-ABI declared in ``include/moe_layout.h``:
     moe_status_string, moe_layout_noalloc,
     moe_relay_layout, moe_dispatch_relay, moe_combine_relay (the Mode 2 relay),
     moe_expert_groups, moe_dispatch_group, moe_combine_group (per-expert groups),
-    moe_route, moe_route_backward (the router),
+    moe_route, moe_route_groups, moe_route_backward (the router),
     moe_expert_forward, moe_expert_backward_rows, moe_expert_backward_weights
     (the experts' products), moe_combine_backward,
     moe_quant4_row_scale_bytes, moe_quant4_weight_scale_bytes, moe_quant4_rows,
     moe_quant4_weights, moe_expert_forward4 (the experts in 4 bits)
 
-``Problem``, ``Layout``, ``Routing`` and ``Experts`` are conveniences that build the C structs and
+``Problem``, ``Layout``, ``Routing``, ``Grouping`` and ``Experts`` are conveniences that build the C structs and
 allocate the caller-owned device buffers.  If the shared library has not been
 built, every call raises ``MoeLibraryMissing``; there is no fallback path.
 """
@@ -66,7 +66,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_layout", "moe_stats_words", "moe_stats",
             "moe_move_faults", "moe_selftest_bounded_waits", "moe_dispatch_quant", "moe_swap_plan",
             "moe_relay_layout", "moe_dispatch_relay", "moe_combine_relay",
             "moe_expert_groups", "moe_dispatch_group", "moe_combine_group",
-            "moe_route", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
+            "moe_route", "moe_route_groups", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
             "moe_expert_backward_weights", "moe_combine_backward", "moe_quant4_row_scale_bytes",
             "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4")
 
@@ -155,6 +155,11 @@ class _RoutingC(ctypes.Structure):
                 ("logits_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 4)]
 
 
+class _GroupingC(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("kept", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class _ExpertsC(ctypes.Structure):
     _fields_ = [("in_cols", ctypes.c_int32), ("out_cols", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("weights", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
@@ -208,6 +213,7 @@ def load_library(path: str = LIB_PATH):
     G, X = ctypes.POINTER(_RoutingC), ctypes.POINTER(_ExpertsC)
     bytes_out = ctypes.POINTER(ctypes.c_size_t)
     for name, args in (("moe_route", [P, G, vp, vp, vp, vp, vp]),
+                       ("moe_route_groups", [P, G, ctypes.POINTER(_GroupingC), vp, vp, vp, vp, vp]),
                        ("moe_route_backward", [P, G, vp, vp, vp, vp, vp]),
                        ("moe_combine_backward", [P, L, vp, vp, vp, vp, vp, vp]),
                        ("moe_expert_forward", [P, L, X, vp, vp, vp, vp]),
@@ -374,6 +380,18 @@ class Routing:
     def c(self, logits) -> _RoutingC:
         return _RoutingC(self.score, bool(self.renormalise), self.scale,
                          MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32)
+
+
+@dataclass
+class Grouping:
+    """Groups that limit a token's choice of experts (moe_grouping in include/moe_layout.h): the
+    `kept` of `groups` whose `top` largest keys sum to most."""
+    groups: int
+    kept: int
+    top: int = 2
+
+    def c(self) -> _GroupingC:
+        return _GroupingC(self.groups, self.kept, self.top, 0)
 
 
 @dataclass
@@ -563,6 +581,16 @@ def moe_route(problem: Problem, routing: Routing, logits, ids, gates, bias=None,
     p, where = problem, "moe_route"
     _check((_lib or load_library()).moe_route(
         ctypes.byref(p.c()), ctypes.byref(routing.c(logits)),
+        _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
+        _take(where, bias, "float32", p.num_experts), _take(where, ids, "int32", p.num_tokens, p.topk),
+        _take(where, gates, "float32", p.num_tokens, p.topk), _stream(stream)), where)
+
+
+def moe_route_groups(problem: Problem, routing: Routing, grouping: Grouping, logits, ids, gates, bias=None, stream=None):
+    """moe_route with every token's choice limited to `grouping.kept` groups of experts; keys are scores (+ bias)."""
+    p, where = problem, "moe_route_groups"
+    _check((_lib or load_library()).moe_route_groups(
+        ctypes.byref(p.c()), ctypes.byref(routing.c(logits)), ctypes.byref(grouping.c()),
         _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
         _take(where, bias, "float32", p.num_experts), _take(where, ids, "int32", p.num_tokens, p.topk),
         _take(where, gates, "float32", p.num_tokens, p.topk), _stream(stream)), where)

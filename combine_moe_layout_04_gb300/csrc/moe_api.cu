@@ -521,6 +521,32 @@ int moe_route(const moe_problem* problem, const moe_routing* routing, const void
     return guarded([&] { return moe::launch_route(a, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
+int moe_route_groups(const moe_problem* problem, const moe_routing* routing, const moe_grouping* grouping,
+                     const void* logits, const float* bias, int32_t* ids, float* gates, moe_stream_t stream) {
+    MOE_NVTX("moe_route_groups");
+    Dims d;
+    moe::RouteArgs a;
+    const int rc = check_routing(problem, routing, &d, &a);
+    if (rc != MOE_OK) return rc;
+    if (grouping == nullptr || grouping->reserved != 0) return MOE_ERR_INVALID;
+    const int groups = grouping->groups, kept = grouping->kept;
+    if (groups < 1 || groups > MOE_MAX_ROUTE_GROUPS || d.E % groups != 0) return MOE_ERR_INVALID;
+    if (kept < 1 || kept > groups || d.k > kept * (d.E / groups)) return MOE_ERR_INVALID;
+    if (grouping->top != 1 && grouping->top != 2) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (logits == nullptr || ids == nullptr || gates == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(logits, a.bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
+        return MOE_ERR_ALIGN;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.gates = gates;
+    a.groups = groups;
+    a.kept = kept;
+    a.top = grouping->top;
+    return guarded([&] { return moe::launch_route_groups(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
 int moe_route_backward(const moe_problem* problem, const moe_routing* routing, const void* logits,
                        const int32_t* ids, const float* dgates, void* dlogits, moe_stream_t stream) {
     MOE_NVTX("moe_route_backward");

@@ -193,6 +193,7 @@ struct RouteArgs {
     int score;
     bool renorm, bf16;
     float scale;
+    int groups, kept, top;   // choice limited to groups of experts
 };
 
 // ---- inline PTX helpers --------------------------------------------------
@@ -485,6 +486,7 @@ cudaError_t read_expert_faults(uint32_t* bits, cudaStream_t s);
 cudaError_t launch_swap_plan(const int32_t* count, const int32_t* e2r, int E, int R, int P, int tau,
                              int32_t* new_e2r, int32_t* swaps, cudaStream_t s);
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_groups(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s);

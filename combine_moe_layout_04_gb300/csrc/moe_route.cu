@@ -105,22 +105,10 @@ __device__ __forceinline__ float weight_of(const RouteArgs& a, const float (&all
     return sum != 0.0f ? s / sum : 0.0f;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_launch_dependents();
-    if (t >= a.T) return;
-    const int E = a.E;
-    float l[V];
-    load_row<T, V>(static_cast<const T*>(a.logits) + t * a.E, E, lane, l);
-    unsigned key[V], id[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        id[i] = 32 * i + lane;
-        key[i] = (int)id[i] < E ? key_of(a.bias != nullptr ? l[i] + a.bias[id[i]] : l[i]) : kTaken;
-    }
+// The ids of the k largest keys of the warp's, the j-th on lane j: equal keys by the lower id.  A lane's ids rise with
+// their index.
+template <int V>
+__device__ __forceinline__ int take_largest(unsigned (&key)[V], unsigned (&id)[V], int k, int lane) {
     // runs, each sorted: neighbours change places only when the later one is larger, so equal keys stay in
     // the order of their ids, and so do equal heads of the runs
     constexpr int kRun = V <= 8 ? V : 4;
@@ -131,14 +119,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
 #pragma unroll
             for (int i = r; i < r + n; ++i)
                 if (key[i + 1] > key[i]) {
-                    const unsigned k = key[i], e = id[i];
+                    const unsigned x = key[i], e = id[i];
                     key[i] = key[i + 1];
                     id[i] = id[i + 1];
-                    key[i + 1] = k;
+                    key[i + 1] = x;
                     id[i + 1] = e;
                 }
     int chosen = 0;
-    for (int j = 0; j < a.k; ++j) {
+    for (int j = 0; j < k; ++j) {
         unsigned best = key[0], at = id[0];        // of this lane
 #pragma unroll
         for (int r = kRun; r < V; r += kRun)
@@ -162,10 +150,140 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
         }
         if (lane == j) chosen = (int)won;
     }
+    return chosen;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t >= a.T) return;
+    const int E = a.E;
+    float l[V];
+    load_row<T, V>(static_cast<const T*>(a.logits) + t * a.E, E, lane, l);
+    unsigned key[V], id[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        id[i] = 32 * i + lane;
+        key[i] = (int)id[i] < E ? key_of(a.bias != nullptr ? l[i] + a.bias[id[i]] : l[i]) : kTaken;
+    }
+    const int chosen = take_largest<V>(key, id, a.k, lane);
     const float mine = lane < a.k ? widen(static_cast<const T*>(a.logits)[t * a.E + chosen]) : -INFINITY;
     const bool on = lane < a.k;
     float rest;
     const float w = weight_of<V>(a, l, mine, on, &rest);
+    if (on) {
+        a.ids[t * a.k + lane] = chosen;
+        a.gates[t * a.k + lane] = a.scale * w;
+    }
+}
+
+// ---- choice limited to groups ---------------------------------------------------------
+//
+// As above, but lanes divide among the groups: the largest power of two of them that 32 / groups holds to each, so
+// that a group's two largest keys meet in a few exchanges.  A warp ranks the groups by comparing every
+// group's value with every other's, and takes the k largest keys of those that stay.
+
+constexpr unsigned kMasked = 0x007fffffu;  // the key of -infinity
+
+// The float of a key; -infinity for a NaN's and for none.
+__device__ __forceinline__ float value_of(unsigned key) {
+    if (key <= kMasked) return -INFINITY;
+    return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
+}
+
+// Sum of one value a lane and V each, rounded once: every addition's error is kept and added at the end.  Keys are made
+// of it, and with the bias they must not depend on an order of additions.
+template <int V>
+__device__ __forceinline__ float sum_once(const float (&v)[V]) {
+    float s = 0.0f, err = 0.0f;
+    auto add = [&](float x, float more) {
+        const float t = s + x, b = t - s;
+        err += (s - (t - b)) + (x - b) + more;
+        s = t;
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) add(v[i], 0.0f);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_xor_sync(kFull, s, d), more = __shfl_xor_sync(kFull, err, d);
+        add(x, more);
+    }
+    return s + err;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t >= a.T) return;
+    const int size = a.E / a.groups;                         // experts of a group
+    const int wide = 1 << (31 - __clz(32 / a.groups));       // lanes of a group
+    const int group = lane / wide, sub = lane % wide;
+    const T* row = static_cast<const T*>(a.logits) + t * a.E;
+    float l[V], score[V];
+    unsigned key[V], id[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = i * wide + sub;
+        const bool live = group < a.groups && at < size;
+        id[i] = live ? group * size + at : a.E + i;
+        l[i] = live ? widen(row[id[i]]) : -INFINITY;
+    }
+    if (a.score == MOE_SCORE_SOFTMAX) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+        top = warp_max(top);
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] = soft(l[i], top);
+        const float sum = sum_once<V>(score);
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] = sum != 0.0f ? score[i] / sum : 0.0f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] = sigmoid(l[i]);
+    }
+    unsigned first = kTaken, second = kTaken;                // the two largest keys of this lane, then of its group
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if ((int)id[i] >= a.E) {
+            key[i] = kTaken;
+        } else {
+            const float k = score[i] == 0.0f ? -INFINITY : a.bias != nullptr ? score[i] + a.bias[id[i]] : score[i];
+            key[i] = key_of(k);
+        }
+        second = max(second, min(first, key[i]));
+        first = max(first, key[i]);
+    }
+    for (int d = wide >> 1; d > 0; d >>= 1) {
+        const unsigned x = __shfl_xor_sync(kFull, first, d), y = __shfl_xor_sync(kFull, second, d);
+        second = max(min(first, x), max(second, y));
+        first = max(first, x);
+    }
+    float value = value_of(first);
+    if (a.top == 2) {
+        const float more = value_of(second);
+        if (more != -INFINITY) value += more;
+    }
+    const unsigned mine = key_of(value);
+    int before = 0;                                          // groups that come before this one
+    for (int g = 0; g < a.groups; ++g) {
+        const unsigned other = __shfl_sync(kFull, mine, g * wide);
+        before += other > mine || (other == mine && g < group);
+    }
+    if (before >= a.kept)
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = kTaken;
+    const int chosen = take_largest<V>(key, id, a.k, lane);
+    const bool on = lane < a.k;
+    const float logit = on ? widen(row[chosen]) : -INFINITY;
+    float rest;
+    const float w = weight_of<V>(a, l, logit, on, &rest);
     if (on) {
         a.ids[t * a.k + lane] = chosen;
         a.gates[t * a.k + lane] = a.scale * w;
@@ -245,7 +363,33 @@ cudaError_t pick(const RouteArgs& a, bool back, cudaStream_t s) {
     return launch<T, 32>(a, back, s);
 }
 
+template <typename T, int V>
+cudaError_t launch_grouped(const RouteArgs& a, cudaStream_t s) {
+    constexpr int per = kRouteThreads / 32;
+    const dim3 grid((unsigned)((a.T + (int64_t)per - 1) / per));
+    return launch_pdl(route_groups_kernel<T, V>, grid, dim3(kRouteThreads), 0, s, a);
+}
+
+// By the experts of a lane: those of a group over its lanes (up to 60, where a group has one lane).
+template <typename T>
+cudaError_t pick_grouped(const RouteArgs& a, cudaStream_t s) {
+    int wide = 1;
+    while (2 * wide * a.groups <= 32) wide *= 2;
+    const int each = (a.E / a.groups + wide - 1) / wide;
+    if (each <= 1) return launch_grouped<T, 1>(a, s);
+    if (each <= 2) return launch_grouped<T, 2>(a, s);
+    if (each <= 4) return launch_grouped<T, 4>(a, s);
+    if (each <= 8) return launch_grouped<T, 8>(a, s);
+    if (each <= 16) return launch_grouped<T, 16>(a, s);
+    if (each <= 32) return launch_grouped<T, 32>(a, s);
+    return launch_grouped<T, 64>(a, s);
+}
+
 }  // namespace
+
+cudaError_t launch_route_groups(const RouteArgs& a, cudaStream_t s) {
+    return a.bf16 ? pick_grouped<__nv_bfloat16>(a, s) : pick_grouped<float>(a, s);
+}
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
     return a.bf16 ? pick<__nv_bfloat16>(a, false, s) : pick<float>(a, false, s);

@@ -16,9 +16,10 @@
  *
  * Call order per MoE layer: (moe_route ->) moe_layout -> (moe_stats) ->
  * moe_dispatch -> experts (moe_expert_forward, or moe_quant4_rows and
- * moe_expert_forward4) -> moe_combine; the way back is moe_combine_backward ->
- * moe_expert_backward_weights and moe_expert_backward_rows -> moe_combine with
- * unit weights (the gradient of a dispatch) and moe_route_backward.  All calls are asynchronous on the given stream;
+ * moe_expert_forward4) -> moe_combine;
+ * the way back is moe_combine_backward -> moe_expert_backward_weights and
+ * moe_expert_backward_rows -> moe_combine with unit weights (the gradient of a
+ * dispatch) and moe_route_backward.  All calls are asynchronous on the given stream;
  * only moe_stats, moe_status, moe_move_faults and moe_selftest_bounded_waits
  * synchronise it.  Every entry
  * point opens an NVTX range of its own name (header-only NVTX 3: free when no
@@ -478,6 +479,37 @@ typedef struct moe_routing {
  *   ids: int32 [T, k]; gates: fp32 [T, k]; k <= E. */
 int moe_route(const moe_problem* problem, const moe_routing* routing, const void* logits, const float* bias,
               int32_t* ids, float* gates, moe_stream_t stream);
+
+/* How the choice of a token's experts is limited to a few groups of them.  The
+ * experts form `groups` groups of num_experts / groups neighbours; a token chooses
+ * from the `kept` groups with the largest values, a group's value being its largest
+ * key (top = 1) or the sum of its two largest (top = 2).
+ *   groups in [1, MOE_MAX_ROUTE_GROUPS], a divisor of num_experts; kept in
+ *   [1, groups], with topk <= kept * num_experts / groups. */
+#define MOE_MAX_ROUTE_GROUPS 32
+typedef struct moe_grouping {
+    int32_t groups;
+    int32_t kept;
+    int32_t top;
+    int32_t reserved;             /* must be 0 */
+} moe_grouping;
+
+/* moe_route with the choice limited to groups of experts ("Balancing and Beyond",
+ * section 3.2, sends a token to the hosts that hold its experts: with a group per
+ * host, to `kept` of them at most).  Keys are made of scores here, not of logits:
+ *   score = softmax over all E logits, or 1 / (1 + exp(-logit)), in fp32, with the
+ *     softmax's sum rounded once from a sum of twice that precision;
+ *   key = score, or score + bias (one fp32 addition); a score of 0 (a logit of
+ *     -infinity, or too low for its exponential) has key -infinity whatever its bias;
+ *   value of a group: its largest key, or that plus the second largest unless that is
+ *     -infinity; a NaN key counts as -infinity here.
+ * The kept groups are those with the largest values, equal values by the lower
+ * index.  ids[t] = the k experts of kept groups with the largest key, in falling
+ * order, equal keys by the lower index, a NaN key after every number: in range and
+ * distinct.  gates, arguments and types as for moe_route; moe_route_backward takes
+ * the ids as they are (the choice itself has no gradient). */
+int moe_route_groups(const moe_problem* problem, const moe_routing* routing, const moe_grouping* grouping,
+                     const void* logits, const float* bias, int32_t* ids, float* gates, moe_stream_t stream);
 
 /* Gradient of the gates with respect to the logits (the pages have
  * no counterpart: they name training only by its traffic).  With a = scale *
