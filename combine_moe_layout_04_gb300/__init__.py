@@ -11,7 +11,8 @@ mirror the C-ABI declared in ``include/moe_layout.h``:
     moe_expert_groups, moe_dispatch_group, moe_combine_group (per-expert groups),
     moe_route, moe_route_groups, moe_route_backward (the router),
     moe_expert_forward, moe_expert_backward_rows, moe_expert_backward_weights
-    (the experts' products), moe_combine_backward,
+    (the experts' products), moe_expert_forward_kept, moe_expert_backward_kept
+    (with pre-activations kept in 8 bits), moe_combine_backward,
     moe_quant4_row_scale_bytes, moe_quant4_weight_scale_bytes, moe_quant4_rows,
     moe_quant4_weights, moe_expert_forward4 (the experts in 4 bits)
 
@@ -67,7 +68,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_layout", "moe_stats_words", "moe_stats",
             "moe_relay_layout", "moe_dispatch_relay", "moe_combine_relay",
             "moe_expert_groups", "moe_dispatch_group", "moe_combine_group",
             "moe_route", "moe_route_groups", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
-            "moe_expert_backward_weights", "moe_combine_backward", "moe_quant4_row_scale_bytes",
+            "moe_expert_backward_weights", "moe_expert_forward_kept", "moe_expert_backward_kept", "moe_combine_backward", "moe_quant4_row_scale_bytes",
             "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4")
 
 
@@ -219,6 +220,8 @@ def load_library(path: str = LIB_PATH):
                        ("moe_expert_forward", [P, L, X, vp, vp, vp, vp]),
                        ("moe_expert_backward_rows", [P, L, X, vp, vp, vp, vp]),
                        ("moe_expert_backward_weights", [P, L, X, vp, vp, vp, vp]),
+                       ("moe_expert_forward_kept", [P, L, X, vp, vp, vp, vp, vp]),
+                       ("moe_expert_backward_kept", [P, L, X, vp, vp, vp, vp, vp, vp]),
                        ("moe_quant4_row_scale_bytes", [P, i32, bytes_out]),
                        ("moe_quant4_weight_scale_bytes", [P, X, bytes_out]),
                        ("moe_quant4_rows", [P, L, i32, vp, vp, vp, vp]),
@@ -673,6 +676,33 @@ def moe_expert_backward_weights(problem: Problem, layout: Layout, experts: Exper
         ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), ctypes.byref(x.c()),
         _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, dout, "bfloat16", slots, x.weight_rows),
         _take(where, dweights, "bfloat16", p.num_experts, x.weight_rows, x.in_cols), _stream(stream)), where)
+
+
+def moe_expert_forward_kept(problem: Problem, layout: Layout, experts: Experts, rows, out, kept, scales, stream=None):
+    """moe_expert_forward with MOE_ACT_SWIGLU that keeps pre in 8 bits: e4m3 codes [T*k, 2 * out_cols] (uint8 or
+    float8_e4m3fn) and e8m0 scales [T*k, 2, ceil(out_cols / 32)] (uint8 or float8_e8m0fnu)."""
+    p, x, where = problem, experts, "moe_expert_forward_kept"
+    slots = p.num_tokens * p.topk
+    _check((_lib or load_library()).moe_expert_forward_kept(
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), _take_weights(where, p, x),
+        _take(where, rows, "bfloat16", slots, x.in_cols), _take(where, out, "bfloat16", slots, x.out_cols),
+        _take(where, kept, "uint8|float8_e4m3fn", slots, 2 * x.out_cols),
+        _take(where, scales, "uint8|float8_e8m0fnu", slots, 2, -(-x.out_cols // 32)), _stream(stream)), where)
+
+
+def moe_expert_backward_kept(problem: Problem, layout: Layout, experts: Experts, dout, kept, scales, drows, act=None,
+                             stream=None):
+    """drows [T*k, 2 * in_cols]: the gradient of the (g, u) that was kept, from dout [T*k, W] of the product whose rows
+    were silu(g) * u; act [T*k, in_cols] receives those rows made anew."""
+    p, x, where = problem, experts, "moe_expert_backward_kept"
+    slots = p.num_tokens * p.topk
+    _check((_lib or load_library()).moe_expert_backward_kept(
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), _take_weights(where, p, x),
+        _take(where, dout, "bfloat16", slots, x.weight_rows),
+        _take(where, kept, "uint8|float8_e4m3fn", slots, 2 * x.in_cols),
+        _take(where, scales, "uint8|float8_e8m0fnu", slots, 2, -(-x.in_cols // 32)),
+        _take(where, drows, "bfloat16", slots, 2 * x.in_cols), _take(where, act, "bfloat16", slots, x.in_cols),
+        _stream(stream)), where)
 
 
 def moe_quant4_row_scale_bytes(problem: Problem, cols: int) -> int:

@@ -644,6 +644,52 @@ int moe_expert_backward_weights(const moe_problem* problem, const moe_layout_t* 
     return guarded([&] { return moe::launch_expert_backward_weights(a, s); });
 }
 
+int moe_expert_forward_kept(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                            const void* rows, void* out, void* kept, void* scales, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_forward_kept");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 8, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (!a.glu) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || rows == nullptr || out == nullptr || kept == nullptr || scales == nullptr)
+        return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(rows, 16) || !aligned(out, 16) || !aligned(kept, 16) || !aligned(scales, 4))
+        return MOE_ERR_ALIGN;
+    a.rows = rows;
+    a.out = out;
+    a.kept = kept;
+    a.kept_scales = scales;
+    return guarded([&] { return moe::launch_expert_forward_kept(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
+int moe_expert_backward_kept(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                             const void* dout, const void* kept, const void* scales, void* drows, void* act,
+                             moe_stream_t stream) {
+    MOE_NVTX("moe_expert_backward_kept");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 8, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || dout == nullptr || kept == nullptr || scales == nullptr || drows == nullptr)
+        return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(dout, 16) || !aligned(kept, 16) || !aligned(scales, 4) ||
+        !aligned(drows, 16) || !aligned(act, 16))
+        return MOE_ERR_ALIGN;
+    a.dout = dout;
+    a.out = drows;
+    a.kept = const_cast<void*>(kept);
+    a.kept_scales = const_cast<void*>(scales);
+    a.act = act;
+    return guarded([&] { return moe::launch_expert_backward_kept(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
 int moe_quant4_row_scale_bytes(const moe_problem* problem, int32_t cols, size_t* bytes) {
     MOE_NVTX("moe_quant4_row_scale_bytes");
     Dims d;

@@ -58,6 +58,7 @@
 
 #include <cmath>
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "moe_clusters.cuh"
@@ -261,6 +262,40 @@ __device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]
     v[0] = swap ? b.x : a.x; v[1] = swap ? b.y : a.y; v[2] = swap ? b.z : a.z; v[3] = swap ? b.w : a.w;
     v[4] = swap ? a.x : b.x; v[5] = swap ? a.y : b.y; v[6] = swap ? a.z : b.z; v[7] = swap ? a.w : b.w;
 }
+// ---- pre-activations kept in 8 bits: e4m3 codes, a power of two (E8M0) for 32 columns ----
+
+// 8 of 32 columns on each of 4 lanes to codes; returns the scale byte: the least power of two with no value over 448 of
+// it (448 = 1.75 * 2^8, so a mantissa over 1.75 takes the next).  All lanes of the warp call it.
+__device__ __forceinline__ uint32_t keep8(const float (&v)[8], uint2* codes) {
+    uint32_t top = 0;                  // magnitudes as integers order as the floats do, infinity and NaN above all
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool bad = top >= 0x7f800000u;
+    const uint32_t b = max((top + 0x1fffffu) >> 23, 8u) - 8;
+    const float inv = __uint_as_float((254u - min(b, 253u)) << 23);  // 2^(127 - b)
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    *codes = bad ? make_uint2(0u, 0u) : make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    return bad ? 255u : b;
+}
+
+// What 8 codes and their scale byte stand for.
+__device__ __forceinline__ void kept8(uint2 codes, uint32_t b, float (&v)[8]) {
+    const float x = b == 255u ? NAN : __uint_as_float(b == 0u ? 1u << 22 : b << 23);  // 2^(b - 127)
+    const uint32_t w[2] = {codes.x, codes.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        v[2 * i] = f.x * x;
+        v[2 * i + 1] = f.y * x;
+    }
+}
+
 // The 128 threads of a store group (barriers 1 and up).
 __device__ __forceinline__ void store_sync(int group) { asm volatile("bar.sync %0, 128;" :: "r"(1 + group) : "memory"); }
 // The same, and whether all of them say yes.
@@ -331,8 +366,8 @@ __device__ __forceinline__ void store_weights(const Plan& p, const Tile& t, cons
 // block of shared memory, and fetch the next one while they write.  sums: tensor memory of this warp's lanes; cta: which
 // half of the features; tid: of 128; link: how the parts of a tile meet (SPLIT).  up: from the first column to the last,
 // else the other way; after `shared` blocks (the columns the next tile's sums take over) this warp arrives on the barrier
-// `over`.
-template <int OP, bool GLU, bool SPLIT>
+// `over`.  KEPT: pre is written, or read, as 8-bit codes.
+template <int OP, bool GLU, bool SPLIT, bool KEPT>
 __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, const Tile& t, uint32_t sums, float* turn,
                                            int cta, int group, int tid, bool up, int shared, uint32_t over, Link& link) {
     constexpr int kMine = GLU ? kHalf / 2 : kHalf;      // features of this CTA
@@ -340,7 +375,8 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     const int f = t.f0 + cta * kMine + (tid % kEights) * 8;
     const bool live = f < p.features;
     const bool swap = (tid & 4) != 0;
-    const bool through = OP == kBackRows && a.pre_in != nullptr;
+    const bool through = OP == kBackRows && (KEPT || a.pre_in != nullptr);
+    const int groups = (p.features + 31) >> 5;          // scales of half a kept row
     const int64_t pitch = through ? 2 * (int64_t)p.features : p.features;
     const int64_t r0 = (int64_t)t.first + t.m0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
@@ -379,9 +415,41 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
-            if (!live || c + row >= t.rows || (SPLIT && row % link.parts != link.part)) continue;
+            const bool mine = live && c + row < t.rows && !(SPLIT && row % link.parts != link.part);
             const float* from = turn + row * kTurnPitch + (tid % kEights) * 8;
             float x[8];
+            if constexpr (GLU && KEPT) {
+                // the lanes of a scale meet, whether they have columns or not
+                float u[8] = {};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = 0.0f;
+                if (mine) {
+                    if (SPLIT) {
+                        summed8(from, link, x);
+                        summed8(from + kHalf / 2, link, u);
+                    } else {
+                        turned8(from, swap, x);
+                        turned8(from + kHalf / 2, swap, u);
+                    }
+                }
+                uint2 gate, up;
+                const uint32_t gate_scale = keep8(x, &gate), up_scale = keep8(u, &up);
+                if (!mine) continue;
+                const int64_t r = r0 + c + row;
+                uint8_t* codes = static_cast<uint8_t*>(a.kept) + r * a.W + f;
+                *reinterpret_cast<uint2*>(codes) = gate;
+                *reinterpret_cast<uint2*>(codes + a.N) = up;
+                if ((tid & 3) == 0) {
+                    uint8_t* scales = static_cast<uint8_t*>(a.kept_scales) + r * 2 * groups + (f >> 5);
+                    scales[0] = (uint8_t)gate_scale;
+                    scales[groups] = (uint8_t)up_scale;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = x[k] * sigmoid(x[k]) * u[k];
+                store8(out + (c + row) * pitch, x);
+                continue;
+            }
+            if (!mine) continue;
             if (SPLIT) summed8(from, link, x);
             else turned8(from, swap, x);
             const int64_t at = (c + row) * pitch;
@@ -398,10 +466,24 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
                 for (int k = 0; k < 8; ++k) x[k] = x[k] * sigmoid(x[k]) * u[k];
                 store8(out + at, x);
             } else if (through) {
-                const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(a.pre_in) + (r0 + c + row) * pitch + f;
+                const int64_t r = r0 + c + row;
                 float g[8], u[8];
-                load8(pre, g);
-                load8(pre + p.features, u);
+                if constexpr (KEPT) {
+                    const uint8_t* codes = static_cast<const uint8_t*>(a.kept) + r * pitch + f;
+                    const uint8_t* scales = static_cast<const uint8_t*>(a.kept_scales) + r * 2 * groups + (f >> 5);
+                    kept8(__ldg(reinterpret_cast<const uint2*>(codes)), __ldg(scales), g);
+                    kept8(__ldg(reinterpret_cast<const uint2*>(codes + p.features)), __ldg(scales + groups), u);
+                    if (a.act != nullptr) {
+                        float act[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) act[k] = g[k] * sigmoid(g[k]) * u[k];
+                        store8(static_cast<__nv_bfloat16*>(a.act) + r * p.features + f, act);
+                    }
+                } else {
+                    const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(a.pre_in) + r * pitch + f;
+                    load8(pre, g);
+                    load8(pre + p.features, u);
+                }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float s = sigmoid(g[k]);
@@ -429,7 +511,7 @@ template <int OP, bool GLU>
 constexpr bool kOneBox = (OP == kForward || OP == kForward4) && !GLU;
 
 // The weights (dout, in the weights' gradient) come through map_a, the rows through maps.
-template <int OP, bool GLU, bool SPLIT>
+template <int OP, bool GLU, bool SPLIT, bool KEPT>
 __global__ void __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
@@ -692,7 +774,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             if constexpr (OP == kBackWeights) {
                 store_weights(p, t, &maps.out, sums, smem_u32(turn) + group * 32 * kHalf * 2, cta, group, quarter * 32 + lane);
             } else {
-                store_tile<OP, GLU, SPLIT>(a, p, t, sums, mine, cta, group, quarter * 32 + lane, (n & 1) != 0, shared,
+                store_tile<OP, GLU, SPLIT, KEPT>(a, p, t, sums, mine, cta, group, quarter * 32 + lane, (n & 1) != 0, shared,
                                            tc::in_rank(smem_u32(&sh.over[n & 1]), lead), link);
                 if (SPLIT && !link.ok) {
                     ok = false;
@@ -831,7 +913,7 @@ cudaError_t start(K* kern, const ExpertArgs& a, const Cut& cut, int64_t tiles, i
     return cudaLaunchKernelEx(&cfg, kern, a, cut, ma, mb);
 }
 
-template <int OP, bool GLU>
+template <int OP, bool GLU, bool KEPT = false>
 cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     CUtensorMap ma;
     Maps mb{};
@@ -859,11 +941,11 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.K + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    auto* whole = pair_kernel<OP, GLU, false>;
+    auto* whole = pair_kernel<OP, GLU, false, KEPT>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(whole), kSmem<OP>);
     if (e != cudaSuccess) return e;
     if constexpr (OP != kBackWeights) {
-        auto* split = pair_kernel<OP, GLU, true>;
+        auto* split = pair_kernel<OP, GLU, true, KEPT>;
         e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
         if (e != cudaSuccess) return e;
         const int steps = ((OP == kBackRows ? a.W : a.K) + kStep<OP> - 1) / kStep<OP>;
@@ -880,6 +962,10 @@ cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s) {
     return a.glu ? launch<kForward, true>(a, s) : launch<kForward, false>(a, s);
 }
 cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s) { return launch<kBackRows, false>(a, s); }
+cudaError_t launch_expert_forward_kept(const ExpertArgs& a, cudaStream_t s) { return launch<kForward, true, true>(a, s); }
+cudaError_t launch_expert_backward_kept(const ExpertArgs& a, cudaStream_t s) {
+    return launch<kBackRows, false, true>(a, s);
+}
 cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s) {
     return launch<kBackWeights, false>(a, s);
 }

@@ -180,6 +180,9 @@ struct ExpertArgs {
     const void* dout;
     void* pre;
     void* out;
+    void* kept;              // (g, u) kept in 8 bits: codes, written or read
+    void* kept_scales;       // and their scales
+    void* act;               // the activation made anew from them
 };
 
 struct RouteArgs {
@@ -491,6 +494,8 @@ cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_expert_forward(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_expert_backward_rows(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_expert_forward_kept(const ExpertArgs& a, cudaStream_t s);
+cudaError_t launch_expert_backward_kept(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);
 cudaError_t launch_quant4_weights(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);

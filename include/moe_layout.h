@@ -19,7 +19,9 @@
  * moe_expert_forward4) -> moe_combine;
  * the way back is moe_combine_backward -> moe_expert_backward_weights and
  * moe_expert_backward_rows -> moe_combine with unit weights (the gradient of a
- * dispatch) and moe_route_backward.  All calls are asynchronous on the given stream;
+ * dispatch) and moe_route_backward.  moe_route_groups stands for moe_route, and
+ * moe_expert_forward_kept with moe_expert_backward_kept for the plain pair where
+ * memory is short.  All calls are asynchronous on the given stream;
  * only moe_stats, moe_status, moe_move_faults and moe_selftest_bounded_waits
  * synchronise it.  Every entry
  * point opens an NVTX range of its own name (header-only NVTX 3: free when no
@@ -583,6 +585,41 @@ int moe_expert_backward_rows(const moe_problem* problem, const moe_layout_t* lay
  *   rows: bf16 [T*k, in_cols]; dout: bf16 [T*k, W]. */
 int moe_expert_backward_weights(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
                                 const void* rows, const void* dout, void* dweights, moe_stream_t stream);
+
+/* ---- Pre-activations kept in 8 bits --------------------------------------------
+ * What the gradient of a gated activation needs of the forward products is (g, u) =
+ * pre, W = 2 * out_cols columns a receive row.  Kept form, 33 bytes for 32 values: of
+ * either half, every 32 columns share one scale X = 2^(b - 127), held as the byte b
+ * (E8M0), and each column holds an e4m3 code (OCP 8-bit floating point; 1 sign, 4
+ * exponent and 3 mantissa bits, largest value 448).
+ *   b = the least in 0 .. 254 with |p| <= 448 X for all 32 (for those that there are,
+ *     at the end of a half), p the fp32 sums: nothing is saturated;
+ *   code = p / X (exact: a power of two) rounded to nearest, ties to even;
+ *   an infinity or NaN among the 32: b = 255 (the scale is NaN), codes 0.
+ *   kept: [T*k, 2 * N] codes, first the gate's columns, then the up's;
+ *   scales: [T*k, 2, ceil(N / 32)] bytes.
+ * A value is off by half a step: 2^-4 of itself, or 2^-10 X where that is more. */
+
+/* moe_expert_forward that keeps pre in 8 bits ("Balancing and Beyond", section 1,
+ * names the experts' products; the pages have no counterpart of what is kept).
+ * experts->act must be MOE_ACT_SWIGLU; out is made of the unrounded sums.
+ *   rows, out: as for moe_expert_forward; kept, scales: as above, N = out_cols.
+ * kept 16-byte aligned, scales 4-byte. */
+int moe_expert_forward_kept(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                            const void* rows, void* out, void* kept, void* scales, moe_stream_t stream);
+
+/* moe_expert_backward_rows through an activation whose (g, u) was kept in 8 bits, and
+ * the activation made anew; the pages have no counterpart.  With g and u the values
+ * that codes and scales stand for:
+ *   drows[r] = (dh u s (1 + g (1 - s)), dh g s), dh = dout[r] W[e],
+ *     s = 1 / (1 + exp(-g)), bf16 [T*k, 2 * in_cols];
+ *   act[r] = silu(g) u, bf16 [T*k, in_cols]: the rows that the weights' gradient
+ *     takes (moe_expert_backward_weights), or NULL.
+ * experts describes the product whose rows were silu(g) * u.
+ *   dout: bf16 [T*k, W]; kept, scales: as above, N = in_cols. */
+int moe_expert_backward_kept(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                             const void* dout, const void* kept, const void* scales, void* drows, void* act,
+                             moe_stream_t stream);
 
 /* Gradient of moe_combine ("Balancing and Beyond", section 1, defines the
  * sum; the pages have no counterpart of its gradient):

@@ -79,3 +79,44 @@ def test_binding_refuses_tensors_of_the_grouped_router(moe, first_gpu):
     f32, i32 = torch.float32, torch.int32
     _tensors_refused(moe, [(f32, 256, 16), (i32, 256, 2), (f32, 256, 2), (f32, 16)],
                      lambda a, b, c, d: moe.moe_route_groups(_p(moe), moe.Routing(), moe.Grouping(4, 2), a, b, c, bias=d, stream=0))
+
+
+def test_kept_refusals(moe):
+    p, lay = _p(moe), _lay(moe)
+    x, down = moe.Experts(64, 64, GOOD, act=moe.MOE_ACT_SWIGLU), moe.Experts(64, 64, GOOD)
+    forward = (moe.moe_expert_forward_kept, x, [GOOD] * 4)
+    backward = (moe.moe_expert_backward_kept, down, [GOOD] * 4)
+    for call, experts, good in (forward, backward):
+        for i in range(4):
+            _refused(moe, moe.MOE_ERR_INVALID, call, p, lay, experts, *good[:i], None, *good[i + 1:])
+            odd = At(0x20002) if i == (3 if call is forward[0] else 2) else ODD     # scales: 4 bytes
+            _refused(moe, moe.MOE_ERR_ALIGN, call, p, lay, experts, *good[:i], odd, *good[i + 1:])
+        for bad in (dict(weights=None), dict(in_cols=12), dict(out_cols=4), dict(act=2), dict(in_cols=(1 << 20) + 8)):
+            kw = {**dict(in_cols=64, out_cols=64, weights=GOOD, act=experts.act), **bad}
+            _refused(moe, moe.MOE_ERR_INVALID, call, p, lay, moe.Experts(**kw), *good)
+        _refused(moe, moe.MOE_ERR_ALIGN, call, p, lay, moe.Experts(64, 64, ODD, act=experts.act), *good)
+        _refused(moe, moe.MOE_ERR_INVALID, call, p, _lay(moe, expert_count=At(None)), experts, *good)
+        _refused(moe, moe.MOE_ERR_INVALID, call, _p(moe, topk=0), lay, experts, *good)
+        call(_p(moe, num_tokens=0), lay, experts, None, None, None, None, stream=0)
+    # kept pre-activations are a gated activation's
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward_kept, p, lay, down, *[GOOD] * 4)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_expert_backward_kept, p, lay, down, *[GOOD] * 4, act=ODD)
+
+
+def test_binding_refuses_tensors_of_kept_calls(moe, first_gpu):
+    import torch
+    bf, u8, p = torch.bfloat16, torch.uint8, _p(moe)
+    lay = _lay(moe, expert_count=On(torch.int32, 16), expert_offset=On(torch.int32, 17))
+    _tensors_refused(moe, [(bf, 16, 80, 64), (bf, 512, 64), (bf, 512, 40), (u8, 512, 80), (u8, 512, 2, 2)],
+                     lambda w, *t: moe.moe_expert_forward_kept(p, lay, moe.Experts(64, 40, w, act=moe.MOE_ACT_SWIGLU), *t, stream=0))
+    _tensors_refused(moe, [(bf, 16, 64, 40), (bf, 512, 64), (u8, 512, 80), (u8, 512, 2, 2), (bf, 512, 80), (bf, 512, 40)],
+                     lambda w, *t: moe.moe_expert_backward_kept(p, lay, moe.Experts(40, 64, w), *t[:4], act=t[4], stream=0))
+    for call in (lambda l: moe.moe_expert_forward_kept(p, l, moe.Experts(64, 40, On(bf, 16, 80, 64), act=moe.MOE_ACT_SWIGLU),
+                                                       On(bf, 512, 64), On(bf, 512, 40), On(u8, 512, 80), On(u8, 512, 2, 2), stream=0),
+                 lambda l: moe.moe_expert_backward_kept(p, l, moe.Experts(40, 64, On(bf, 16, 64, 40)), On(bf, 512, 64),
+                                                        On(u8, 512, 80), On(u8, 512, 2, 2), On(bf, 512, 80), stream=0)):
+        for bad in (dict(expert_count=On(torch.int32, 15)), dict(expert_offset=On(torch.int32, 16)),
+                    dict(expert_offset=On(torch.int64, 17)), dict(expert_count=On(torch.int32, 16, gpu=1))):
+            with pytest.raises(moe.MoeError) as ei:
+                call(_lay(moe, **{**dict(expert_count=On(torch.int32, 16), expert_offset=On(torch.int32, 17)), **bad}))
+            assert ei.value.code == moe.MOE_ERR_INVALID
