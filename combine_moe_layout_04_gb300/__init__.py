@@ -14,7 +14,8 @@ mirror the C-ABI declared in ``include/moe_layout.h``:
     (the experts' products), moe_expert_forward_kept, moe_expert_backward_kept
     (with pre-activations kept in 8 bits), moe_combine_backward,
     moe_quant4_row_scale_bytes, moe_quant4_weight_scale_bytes, moe_quant4_rows,
-    moe_quant4_weights, moe_expert_forward4 (the experts in 4 bits)
+    moe_quant4_weights, moe_expert_forward4 (the experts in 4 bits),
+    moe_quant8_rows, moe_quant8_weights, moe_expert_forward8 (in 8-bit integers)
 
 ``Problem``, ``Layout``, ``Routing``, ``Grouping`` and ``Experts`` are conveniences that build the C structs and
 allocate the caller-owned device buffers.  If the shared library has not been
@@ -69,7 +70,8 @@ EXPORTED = ("moe_workspace_bytes", "moe_layout", "moe_stats_words", "moe_stats",
             "moe_expert_groups", "moe_dispatch_group", "moe_combine_group",
             "moe_route", "moe_route_groups", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
             "moe_expert_backward_weights", "moe_expert_forward_kept", "moe_expert_backward_kept", "moe_combine_backward", "moe_quant4_row_scale_bytes",
-            "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4")
+            "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4",
+            "moe_quant8_rows", "moe_quant8_weights", "moe_expert_forward8")
 
 
 class MoeLibraryMissing(RuntimeError):
@@ -226,7 +228,10 @@ def load_library(path: str = LIB_PATH):
                        ("moe_quant4_weight_scale_bytes", [P, X, bytes_out]),
                        ("moe_quant4_rows", [P, L, i32, vp, vp, vp, vp]),
                        ("moe_quant4_weights", [P, X, vp, vp, vp]),
-                       ("moe_expert_forward4", [P, L, X, vp, vp, vp, vp, vp])):
+                       ("moe_expert_forward4", [P, L, X, vp, vp, vp, vp, vp]),
+                       ("moe_quant8_rows", [P, i32, vp, vp, vp, vp]),
+                       ("moe_quant8_weights", [P, X, vp, vp, vp]),
+                       ("moe_expert_forward8", [P, L, X, vp, vp, vp, vp, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
     lib.moe_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
@@ -400,8 +405,8 @@ class Grouping:
 @dataclass
 class Experts:
     """The experts of a layer (moe_experts in include/moe_layout.h): weights
-    bf16 [E, W, in_cols], or 4-bit codes [E, W, in_cols / 2] with their scale
-    blocks; W = out_cols, or 2 * out_cols (gate rows, then up rows) with
+    bf16 [E, W, in_cols], 4-bit codes [E, W, in_cols / 2] with their scale
+    blocks, or int8 [E, W, in_cols] with fp32 scales [E, W]; W = out_cols, or 2 * out_cols (gate rows, then up rows) with
     MOE_ACT_SWIGLU."""
     in_cols: int
     out_cols: int
@@ -772,6 +777,41 @@ def moe_expert_forward4(problem: Problem, layout: Layout, experts: Experts, code
         ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), ctypes.byref(x.c()),
         _take(where, codes, "uint8", slots, x.in_cols // 2),
         _take_bytes(where, scales, _row_scale_bytes(p, x.in_cols)),
+        _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),
+        _stream(stream)), where)
+
+
+def moe_quant8_rows(problem: Problem, rows, codes, scales, stream=None):
+    """Receive rows bf16 [T*k, cols] to 8-bit integers [T*k, cols] and one fp32 scale a row."""
+    p, where = problem, "moe_quant8_rows"
+    shape = getattr(codes, "shape", ())
+    if len(shape) != 2:
+        raise MoeError(MOE_ERR_INVALID, f"{where}: codes are [T*k, cols], not {list(shape)}")
+    slots, cols = p.num_tokens * p.topk, int(shape[1])
+    _check((_lib or load_library()).moe_quant8_rows(
+        ctypes.byref(p.c()), cols, _take(where, rows, "bfloat16", slots, cols), _take(where, codes, "int8", slots, cols),
+        _take(where, scales, "float32", slots), _stream(stream)), where)
+
+
+def moe_quant8_weights(problem: Problem, experts: Experts, codes, scales, stream=None):
+    """The experts' bf16 weights to 8-bit integers [E, W, in_cols] and fp32 scales [E, W]."""
+    p, x, where = problem, experts, "moe_quant8_weights"
+    _check((_lib or load_library()).moe_quant8_weights(
+        ctypes.byref(p.c()), _take_weights(where, p, x),
+        _take(where, codes, "int8", p.num_experts, x.weight_rows, x.in_cols),
+        _take(where, scales, "float32", p.num_experts, x.weight_rows), _stream(stream)), where)
+
+
+def moe_expert_forward8(problem: Problem, layout: Layout, experts: Experts, codes, scales, out, pre=None, stream=None):
+    """moe_expert_forward from 8-bit integer rows (moe_quant8_rows) and weights (experts.weights,
+    experts.scales of moe_quant8_weights); out and pre are bf16."""
+    p, x, where = problem, experts, "moe_expert_forward8"
+    slots = p.num_tokens * p.topk
+    _take(where, x.weights, "int8", p.num_experts, x.weight_rows, x.in_cols)
+    _take(where, x.scales, "float32", p.num_experts, x.weight_rows)
+    _check((_lib or load_library()).moe_expert_forward8(
+        ctypes.byref(p.c()), ctypes.byref(_groups(where, p, layout)), ctypes.byref(x.c()),
+        _take(where, codes, "int8", slots, x.in_cols), _take(where, scales, "float32", slots),
         _take(where, pre, "bfloat16", slots, x.weight_rows), _take(where, out, "bfloat16", slots, x.out_cols),
         _stream(stream)), where)
 

@@ -772,6 +772,59 @@ int moe_expert_forward4(const moe_problem* problem, const moe_layout_t* layout, 
     return guarded([&] { return moe::launch_expert_forward4(a, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
+int moe_quant8_rows(const moe_problem* problem, int32_t cols, const void* rows, int8_t* codes, float* scales,
+                    moe_stream_t stream) {
+    MOE_NVTX("moe_quant8_rows");
+    Dims d;
+    const int rc = check_problem(problem, &d);
+    if (rc != MOE_OK) return rc;
+    if (cols < 16 || cols > MOE_MAX_HIDDEN || cols % 16 != 0 || d.T * d.k > MOE_MAX_EXPERT_ROWS) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (rows == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
+    return guarded([&] {
+        return moe::launch_quant8(rows, (int64_t)d.T * d.k, cols, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int moe_quant8_weights(const moe_problem* problem, const moe_experts* experts, int8_t* codes, float* scales,
+                       moe_stream_t stream) {
+    MOE_NVTX("moe_quant8_weights");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 16, &a);
+    if (rc != MOE_OK) return rc;
+    if (a.weights == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_ALIGN;
+    return guarded([&] {
+        return moe::launch_quant8(a.weights, (int64_t)a.E * a.W, a.K, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+int moe_expert_forward8(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                        const int8_t* codes, const float* scales, void* pre, void* out, moe_stream_t stream) {
+    MOE_NVTX("moe_expert_forward8");
+    Dims d;
+    moe::ExpertArgs a;
+    int rc = check_problem(problem, &d);
+    if (rc == MOE_OK) rc = check_experts(experts, d, 16, &a);
+    if (rc == MOE_OK) rc = check_expert_layout(layout, &a);
+    if (rc != MOE_OK) return rc;
+    if (pre != nullptr && !a.glu) return MOE_ERR_INVALID;
+    if (d.T == 0) return MOE_OK;
+    if (a.weights == nullptr || a.weight_scales == nullptr || codes == nullptr || scales == nullptr || out == nullptr)
+        return MOE_ERR_INVALID;
+    if (!aligned(a.weights, 16) || !aligned(a.weight_scales, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
+        !aligned(pre, 16) || !aligned(out, 16))
+        return MOE_ERR_ALIGN;
+    a.rows = codes;
+    a.row_scales = scales;
+    a.pre = pre;
+    a.out = out;
+    return guarded([&] { return moe::launch_expert_forward8(a, reinterpret_cast<cudaStream_t>(stream)); });
+}
+
 int moe_status(const void* workspace, uint32_t* status_bits, moe_stream_t stream) {
     MOE_NVTX("moe_status");
     if (workspace == nullptr || status_bits == nullptr) return MOE_ERR_INVALID;

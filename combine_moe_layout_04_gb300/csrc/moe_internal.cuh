@@ -172,8 +172,8 @@ struct ExpertArgs {
     int N;                   // out_cols
     int W;                   // rows of an expert's weights: N, or 2 N with a gated activation
     bool glu;
-    const void* rows;        // bf16 rows, or 4-bit codes
-    const void* row_scales;  // scale blocks of 4-bit rows
+    const void* rows;        // bf16 rows, 4-bit codes or 8-bit integers
+    const void* row_scales;  // scale blocks of 4-bit rows, fp32 scales of integer rows
     const void* weights;
     const void* weight_scales;
     const void* pre_in;      // backward through the activation: (g, u)
@@ -499,6 +499,8 @@ cudaError_t launch_expert_backward_kept(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_quant4_rows(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);
 cudaError_t launch_quant4_weights(const ExpertArgs& a, void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_quant8(const void* rows, int64_t count, int cols, int8_t* codes, float* scales, cudaStream_t s);
+cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s);
 cudaError_t launch_combine_backward(const int32_t* pos, int T, int k, int h, const void* dout, const void* y,
                                     const float* weights, void* dy, float* dweights, cudaStream_t s);
 cudaError_t run_wait_selftest(uint32_t* bits, cudaStream_t s);

@@ -16,7 +16,7 @@
  *
  * Call order per MoE layer: (moe_route ->) moe_layout -> (moe_stats) ->
  * moe_dispatch -> experts (moe_expert_forward, or moe_quant4_rows and
- * moe_expert_forward4) -> moe_combine;
+ * moe_expert_forward4, or moe_quant8_rows and moe_expert_forward8) -> moe_combine;
  * the way back is moe_combine_backward -> moe_expert_backward_weights and
  * moe_expert_backward_rows -> moe_combine with unit weights (the gradient of a
  * dispatch) and moe_route_backward.  moe_route_groups stands for moe_route, and
@@ -620,6 +620,38 @@ int moe_expert_forward_kept(const moe_problem* problem, const moe_layout_t* layo
 int moe_expert_backward_kept(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
                              const void* dout, const void* kept, const void* scales, void* drows, void* act,
                              moe_stream_t stream);
+
+/* ---- The experts' products in 8-bit integers ------------------------------------
+ * A row of x (a receive row, or one row of an expert's weights) is held as integers
+ * c in -127 .. 127 and one fp32 scale s:
+ *   m = the row's largest |x|;  s = m / 127 (fp32 division; 1 when m is 0);
+ *   c = x * (127 / m) rounded to nearest, ties to even (fp32 division and product; where
+ *     m < 2^-100 both x and m are taken times 2^100 first, which is exact);
+ *   an infinity or NaN in the row: s = NaN, codes 0.
+ * in_cols: a multiple of 16 in [16, 2^20] in these calls. */
+
+/* Receive rows to 8-bit integers (the pages stop at the FP8 conversion of
+ * "Balancing and Beyond", section 3.1).  Every row is taken by itself: no layout is read.
+ *   rows: bf16 [T*k, cols]; codes: int8 [T*k, cols]; scales: fp32 [T*k].
+ * rows and codes 16-byte aligned, scales 4-byte. */
+int moe_quant8_rows(const moe_problem* problem, int32_t cols, const void* rows, int8_t* codes, float* scales,
+                    moe_stream_t stream);
+
+/* The experts' bf16 weights to 8-bit integers, once per model; the pages
+ * have no counterpart.  experts describes the bf16 weights; codes: int8 [E, W, in_cols];
+ * scales: fp32 [E, W]. */
+int moe_quant8_weights(const moe_problem* problem, const moe_experts* experts, int8_t* codes, float* scales,
+                       moe_stream_t stream);
+
+/* The experts' forward products from 8-bit integers; the pages have no counterpart
+ * (their rows stop at FP8).  p = scales[r] * weight_scale * sum of c_row * c_weight
+ * for every receive row r and row of its expert's weights, integers summed in fp32, then
+ * as moe_expert_forward: out[r] = p or silu(g) * u, pre (NULL unless MOE_ACT_SWIGLU) = p.
+ *   codes: int8 [T*k, in_cols] (any value, -128 among them); scales: fp32 [T*k];
+ *   experts->weights: int8 [E, W, in_cols], experts->scales: fp32 [E, W], 16-byte
+ *   aligned as the other arrays (scales of rows 4-byte); out, pre: bf16. */
+int moe_expert_forward8(const moe_problem* problem, const moe_layout_t* layout, const moe_experts* experts,
+                        const int8_t* codes, const float* scales, void* pre, void* out, moe_stream_t stream);
 
 /* Gradient of moe_combine ("Balancing and Beyond", section 1, defines the
  * sum; the pages have no counterpart of its gradient):

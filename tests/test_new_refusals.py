@@ -120,3 +120,60 @@ def test_binding_refuses_tensors_of_kept_calls(moe, first_gpu):
             with pytest.raises(moe.MoeError) as ei:
                 call(_lay(moe, **{**dict(expert_count=On(torch.int32, 16), expert_offset=On(torch.int32, 17)), **bad}))
             assert ei.value.code == moe.MOE_ERR_INVALID
+
+
+def test_int8_refusals(moe):
+    p, lay = _p(moe), _lay(moe)
+    codes = At(0x30000, (512, 64))
+    for args in ((None, codes, GOOD), (GOOD, At(None, (512, 64)), GOOD), (GOOD, codes, None)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_rows, p, *args)
+    for args in ((ODD, codes, GOOD), (GOOD, At(0x30008, (512, 64)), GOOD), (GOOD, codes, At(0x20002))):
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_quant8_rows, p, *args)
+    for cols in (0, 8, 24, -16, (1 << 20) + 16):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_rows, p, GOOD, At(0x30000, (512, cols)), GOOD)
+    for shape in ((), (512 * 64,), (512, 64, 1)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_rows, p, GOOD, At(0x30000, shape), GOOD)
+    most = _p(moe, num_tokens=(1 << 31) - 256, topk=1, num_ranks=1, ranks_per_host=1)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_rows, most, GOOD, codes, GOOD)
+    moe.moe_quant8_rows(_p(moe, num_tokens=0), None, At(None, (0, 64)), None, stream=0)
+
+    x = moe.Experts(64, 64, GOOD, scales=GOOD)
+    for bad in (dict(in_cols=8), dict(in_cols=72), dict(in_cols=0), dict(in_cols=(1 << 20) + 16), dict(out_cols=4), dict(act=2)):
+        kw = {**dict(in_cols=64, out_cols=64, weights=GOOD, scales=GOOD), **bad}
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward8, p, lay, moe.Experts(**kw), GOOD, GOOD, GOOD)
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_weights, p, moe.Experts(**kw), GOOD, GOOD)
+    for i in range(3):
+        good = [GOOD] * 3
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward8, p, lay, x, *good[:i], None, *good[i + 1:])
+        odd = At(0x20002) if i == 1 else ODD
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_expert_forward8, p, lay, x, *good[:i], odd, *good[i + 1:])
+    for kw, code in ((dict(weights=None, scales=GOOD), "INVALID"), (dict(weights=GOOD, scales=None), "INVALID"),
+                     (dict(weights=ODD, scales=GOOD), "ALIGN"), (dict(weights=GOOD, scales=ODD), "ALIGN")):
+        _refused(moe, getattr(moe, "MOE_ERR_" + code), moe.moe_expert_forward8, p, lay, moe.Experts(64, 64, **kw), GOOD, GOOD, GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward8, p, lay, x, GOOD, GOOD, GOOD, pre=GOOD)
+    _refused(moe, moe.MOE_ERR_INVALID, moe.moe_expert_forward8, p, _lay(moe, expert_offset=At(None)), x, GOOD, GOOD, GOOD)
+    gated = moe.Experts(64, 64, GOOD, act=moe.MOE_ACT_SWIGLU, scales=GOOD)
+    _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_expert_forward8, p, lay, gated, GOOD, GOOD, GOOD, pre=ODD)
+    moe.moe_expert_forward8(_p(moe, num_tokens=0), lay, moe.Experts(64, 64), None, None, None, stream=0)
+    for args in ((None, GOOD), (GOOD, None)):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_quant8_weights, p, x, *args)
+    for args in ((ODD, GOOD), (GOOD, ODD)):
+        _refused(moe, moe.MOE_ERR_ALIGN, moe.moe_quant8_weights, p, x, *args)
+
+
+def test_binding_refuses_tensors_of_int8_calls(moe, first_gpu):
+    import torch
+    bf, i8, f32, p = torch.bfloat16, torch.int8, torch.float32, _p(moe)
+    lay = _lay(moe, expert_count=On(torch.int32, 16), expert_offset=On(torch.int32, 17))
+    _tensors_refused(moe, [(bf, 512, 64), (i8, 512, 64), (f32, 512)], lambda *t: moe.moe_quant8_rows(p, *t, stream=0))
+    _tensors_refused(moe, [(bf, 16, 40, 64), (i8, 16, 40, 64), (f32, 16, 40)],
+                     lambda w, *t: moe.moe_quant8_weights(p, moe.Experts(64, 40, w), *t, stream=0))
+    _tensors_refused(moe, [(i8, 16, 80, 64), (f32, 16, 80), (i8, 512, 64), (f32, 512), (bf, 512, 40), (bf, 512, 80)],
+                     lambda w, s, *t: moe.moe_expert_forward8(p, lay, moe.Experts(64, 40, w, act=moe.MOE_ACT_SWIGLU, scales=s),
+                                                              *t[:3], pre=t[3], stream=0))
+    for bad in (dict(expert_count=On(torch.int32, 15)), dict(expert_offset=On(torch.int32, 16))):
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_expert_forward8(p, _lay(moe, **{**dict(expert_count=On(torch.int32, 16), expert_offset=On(torch.int32, 17)), **bad}),
+                                    moe.Experts(64, 40, On(i8, 16, 40, 64), scales=On(f32, 16, 40)), On(i8, 512, 64),
+                                    On(f32, 512), On(bf, 512, 40), stream=0)
+        assert ei.value.code == moe.MOE_ERR_INVALID
