@@ -58,6 +58,7 @@
 
 #include <cmath>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -70,29 +71,32 @@ namespace {
 
 __device__ unsigned int g_expert_faults;
 
-constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3;
-constexpr int kGroups = 4;             // of four warps that store
-constexpr int kTailWarp = 2 + 4 * kGroups;
+constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3, kForward8 = 4;
+template <int OP>
+constexpr int kGroups = OP == kForward8 ? 2 : 4;  // of four warps that store
+template <int OP>
+constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
+constexpr int kWideners = 8;           // warps that widen integers: four for either half of a stage
 template <int OP>                      // warp 0 copies, warp 1 multiplies; in the weights' gradient one more clears
-constexpr int kThreads = 32 * (kTailWarp + (OP == kBackWeights ? 1 : 0));
+constexpr int kThreads = 32 * (kTailWarp<OP> + (OP == kBackWeights ? 1 : OP == kForward8 ? kWideners : 0));
 constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // most columns of one product instruction
 constexpr int kFirst = 128;            // a wider tile is two products: this many columns, and the others
 template <int OP>
-constexpr int kTop = OP == kForward4 ? 448 : 512;  // columns of tensor memory for sums
+constexpr int kTop = OP == kForward4 ? 448 : OP == kForward8 ? 384 : 512;  // columns of tensor memory for sums
 constexpr int kRowBytes = 128;         // of a stage, along memory
 template <int OP>
-constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : kRowBytes / 2;  // its contraction
+constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : OP == kForward8 ? kRowBytes : kRowBytes / 2;  // its contraction
 constexpr int kBoxBytes = 64 * kRowBytes;
 constexpr int kBytesA = kHalf * kRowBytes;
 template <int OP>
-constexpr int kRingBytes = (OP == kForward4 ? 176 : 180) * 1024;
+constexpr int kRingBytes = (OP == kForward4 ? 176 : OP == kForward8 ? 195 : 180) * 1024;
 constexpr int kStages = 12;            // most stages in flight
 constexpr int kTurn = 16;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
 constexpr int kTurnBytes = 4 * kTurn * kTurnPitch;
 template <int OP>                      // 1024: alignment; in 4 bits also the experts' first scale blocks
-constexpr int kSmem = kRingBytes<OP> + kGroups * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
+constexpr int kSmem = kRingBytes<OP> + kGroups<OP> * kTurnBytes + 1024 + (OP == kForward4 ? 4 * (MOE_MAX_EXPERTS + 4) : 0);
 
 // 4-bit stages end with the scales of 256 codes: 1 KB (two scale blocks along a row) of the weights' 128 rows and of
 // every 128 receive rows the tile touches (tiles start at multiples of 64 rows: one of up to 256 touches two, of up to
@@ -101,9 +105,15 @@ constexpr int kScaleBlock = 512;
 constexpr int scale_bytes(int columns) { return (columns > 256 ? 4 : 3) * 2 * kScaleBlock; }
 constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
+// 8-bit integers are widened to fp16 (exactly) between copy and product, in pieces of 64 of the contraction: half of what a
+// stage holds.  The weights' pieces lie in tensor memory above the sums, the rows' in shared memory behind the stages.
+constexpr int kPieces = 4, kPiece = 64, kPieceColumns = kPiece / 2;
+static_assert(kTop<kForward8> + kPieces * kPieceColumns == 512);
+
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
-    uint64_t ready[kGroups], seen[kGroups];  // of a store group's block, by the parts of a tile
+    uint64_t ready[4], seen[4];        // of a store group's block, by the parts of a tile
+    uint64_t made[kPieces], used[kPieces];  // pieces of widened integers
     uint32_t tmem;
     int scratch[32];
     int base[MOE_MAX_EXPERTS + 1];
@@ -262,6 +272,57 @@ __device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]
     v[0] = swap ? b.x : a.x; v[1] = swap ? b.y : a.y; v[2] = swap ? b.z : a.z; v[3] = swap ? b.w : a.w;
     v[4] = swap ? a.x : b.x; v[5] = swap ? a.y : b.y; v[6] = swap ? a.z : b.z; v[7] = swap ? a.w : b.w;
 }
+__device__ __forceinline__ void load_scales(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// ---- 8-bit integers to fp16 ------------------------------------------------------
+
+// 4 integers to 4 fp16: a byte under the exponent of 1024 counts in ones, so the integer is that less 1024 + 128.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&lo), bias), y = __hsub2(*reinterpret_cast<__half2*>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+
+// Half `half` of a stage's 128 weight rows to a piece in tensor memory: a lane takes a row, 64 bytes of it.  (16-byte pieces
+// of a row lie swizzled by the row, so that 8 lanes cover all banks.)
+__device__ __forceinline__ void widen_weights(uint32_t stage, int half, uint32_t piece, int quarter, int lane) {
+    const int row = quarter * 32 + lane;
+    uint32_t v[kPieceColumns];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 w = lds_v4(stage + row * kRowBytes + (((4 * half + i) ^ (row & 7)) << 4));
+        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 x = widen4(b[j]);
+            v[8 * i + 2 * j] = x.x;
+            v[8 * i + 2 * j + 1] = x.y;
+        }
+    }
+    tc::st32(piece + ((uint32_t)(quarter * 32) << 16), v);
+}
+
+// The same of `rows` receive rows, to rows of 128 bytes in shared memory, swizzled likewise: 8 rows at a time, 8 lanes on
+// one 16-byte piece of each.
+__device__ __forceinline__ void widen_rows(uint32_t stage, int half, uint32_t piece, int rows, int warp, int lane) {
+    const int sub = lane & 7, chunk = lane >> 3;
+    for (int r0 = 8 * warp; r0 < rows; r0 += 32) {
+        const uint32_t row = (uint32_t)(r0 + sub) * kRowBytes;
+        const uint4 w = lds_v4(stage + row + (((4 * half + chunk) ^ sub) << 4));
+        const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(piece + row + (((2 * chunk) ^ sub) << 4)), "r"(a.x), "r"(a.y),
+                     "r"(b.x), "r"(b.y) : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(piece + row + (((2 * chunk + 1) ^ sub) << 4)), "r"(c.x),
+                     "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
+    }
+}
+
 // ---- pre-activations kept in 8 bits: e4m3 codes, a power of two (E8M0) for 32 columns ----
 
 // 8 of 32 columns on each of 4 lanes to codes; returns the scale byte: the least power of two with no value over 448 of
@@ -334,7 +395,7 @@ __device__ __forceinline__ void store_weights(const Plan& p, const Tile& t, cons
                                               uint32_t block, int cta, int group, int tid) {
     const int w0 = t.f0 + cta * kHalf;
     const uint32_t row = block + tid * 64, turn = (tid >> 1) & 3;
-    for (int c = group * 32; c < t.n; c += kGroups * 32) {
+    for (int c = group * 32; c < t.n; c += kGroups<kBackWeights> * 32) {
         uint32_t lo[16], hi[16];
         tc::ld16(sums + c, lo);
         tc::ld16(sums + c + 16, hi);
@@ -381,6 +442,13 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     const int64_t r0 = (int64_t)t.first + t.m0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
     const int count = t.n / kTurn;
+    constexpr bool k8 = OP == kForward8;
+    float sg[8], su[8];                                 // scales of this thread's features
+    if constexpr (k8) {
+        const float* scales = static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + f;
+        if (live) load_scales(scales, sg);
+        if (live && GLU) load_scales(scales + a.N, su);
+    }
     auto column = [&](int i) { return (up ? i : count - 1 - i) * kTurn; };
     bool told = false;
     auto tell = [&] {
@@ -391,7 +459,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     };
     uint32_t v[kTurn];
     if (group < count) tc::ld16(sums + column(group), v);
-    for (int b = group; b < count; b += kGroups) {
+    for (int b = group; b < count; b += kGroups<OP>) {
         const int c = column(b);
         if (!told && b >= shared) tell();
         tc::wait_ld();
@@ -411,7 +479,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
             if (!link.ok) break;
             link.phase ^= 1u;
         }
-        if (b + kGroups < count) tc::ld16(sums + column(b + kGroups), v);
+        if (b + kGroups<OP> < count) tc::ld16(sums + column(b + kGroups<OP>), v);
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
@@ -453,10 +521,19 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
             if (SPLIT) summed8(from, link, x);
             else turned8(from, swap, x);
             const int64_t at = (c + row) * pitch;
+            const float scale = k8 ? __ldg(static_cast<const float*>(a.row_scales) + r0 + c + row) : 1.0f;
+            if constexpr (k8) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = x[k] * sg[k] * scale;
+            }
             if (GLU) {
                 float u[8];
                 if (SPLIT) summed8(from + kHalf / 2, link, u);
                 else turned8(from + kHalf / 2, swap, u);
+                if constexpr (k8) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) u[k] = u[k] * su[k] * scale;
+                }
                 if (a.pre != nullptr) {
                     __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(a.pre) + (r0 + c + row) * a.W + f;
                     store8(pre, x);
@@ -508,39 +585,47 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
 
 // Whether the weights' 128 rows of a CTA come in one box.
 template <int OP, bool GLU>
-constexpr bool kOneBox = (OP == kForward || OP == kForward4) && !GLU;
+constexpr bool kOneBox = (OP == kForward || OP == kForward4 || OP == kForward8) && !GLU;
 
 // The weights (dout, in the weights' gradient) come through map_a, the rows through maps.
 template <int OP, bool GLU, bool SPLIT, bool KEPT>
 __global__ void __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
-    constexpr bool k4 = OP == kForward4, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
+    constexpr bool k4 = OP == kForward4, k8 = OP == kForward8, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
     const uint32_t stages = smem_u32(dynamic) + skip;
     float* turn = reinterpret_cast<float*>(dynamic + skip + kRingBytes<OP>);
-    int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + kGroups * kTurnBytes);  // [E + 1], in 4 bits
+    int* blocks = reinterpret_cast<int*>(dynamic + skip + kRingBytes<OP> + kGroups<OP> * kTurnBytes);  // [E + 1], in 4 bits
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)tc::rank_in_cluster(), cta = rank & 1, lead = rank & ~1;
     const uint16_t both = (uint16_t)(3u << lead);
     const int parts = SPLIT ? cut.parts : 1, part = SPLIT ? rank >> 1 : 0;
     const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty);  // 8 bytes a stage
+    const uint32_t made = smem_u32(sh.made), used = smem_u32(sh.used);    // 8 bytes a piece
+    const uint32_t pieces = stages + cut.stages * cut.bytes, piece_bytes = cut.columns / 2 * kRowBytes;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < cut.stages; ++i) {
-            mbar_init(full + 8 * i, 2);   // both CTAs' copies arrive on the first CTA's
-            mbar_init(empty + 8 * i, 1);
+            // both CTAs' copies arrive on the first CTA's; integers are widened by the CTA that copied them
+            mbar_init(full + 8 * i, k8 ? 1 : 2);
+            mbar_init(empty + 8 * i, k8 ? kWideners : 1);
             mbar_init(smem_u32(&sh.tail[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.done[i]), 1);
-            mbar_init(smem_u32(&sh.free[i]), 2 * 4 * kGroups);
-            mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups);
+            mbar_init(smem_u32(&sh.free[i]), 2 * 4 * kGroups<OP>);
+            mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups<OP>);
         }
+        if (k8)
+            for (int i = 0; i < kPieces; ++i) {
+                mbar_init(made + 8 * i, kWideners);  // half of them in either CTA
+                mbar_init(used + 8 * i, 1);
+            }
         if (SPLIT)
-            for (int i = 0; i < kGroups; ++i) {
+            for (int i = 0; i < kGroups<OP>; ++i) {
                 mbar_init(smem_u32(&sh.ready[i]), parts);
                 mbar_init(smem_u32(&sh.seen[i]), parts);
             }
@@ -574,7 +659,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 
     bool ok = true;
     if (warp == 0) {
-        const uint32_t full0 = tc::in_rank(full, lead);
+        const uint32_t full0 = tc::in_rank(full, k8 ? rank : lead);
         Ring ring;
         int flying = 0;                // stages issued, up to all of them
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
@@ -648,7 +733,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             }
         }
         // no copy of this pair is in flight when it ends: its readers have waited for them, unless a wait gave up
-        if (cta == 0)
+        if (cta == 0 || k8)
             for (; flying > 0; --flying) {
                 if (ring.stage-- == 0) {
                     ring.stage = cut.stages - 1;
@@ -659,6 +744,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     } else if (warp == 1 && cta == 0) {
         Ring ring;
         int n = 0, before = 0;         // tiles so far, columns of the one before
+        int piece = 0;
+        uint32_t piece_phase = 0;
         for (int64_t i = pair; i < p.tiles && ok; i += pairs, ++n) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const bool wide = !across_b && t.n > kColumns;
@@ -677,6 +764,24 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             before = t.n;
             tc::fence_after_sync();
             const int begin = begin_of(t), end = end_of(t);
+            if constexpr (k8) {
+                for (int k0 = begin; k0 < end; k0 += kPiece, piece = (piece + 1) % kPieces, piece_phase ^= piece == 0) {
+                    ok = warp_wait_cluster(made + 8 * piece, piece_phase);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
+                        const uint32_t wa = tmem + kTop<OP> + piece * kPieceColumns;
+                        const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes);
+                        const int count = min(kPiece, end - k0) / 16;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < count)
+                                tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, tc::instruction16_pair(t.n), k0 > begin || k > 0);
+                        tc::commit_pair(used + 8 * piece, both);
+                    }
+                    __syncwarp();
+                }
+            } else
             for (int k0 = begin; k0 < end; k0 += kStep<OP>) {
                 // a stage that the tail warps of both CTAs have cleared is theirs to hand over, any other the copies'
                 const bool cleared = OP == kBackWeights && t.length - k0 < kStep<OP> && (t.length & 15) != 0;
@@ -749,7 +854,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         if (tc::elect_one()) tc::commit_pair(smem_u32(&sh.last), both);
         __syncwarp();
         ok = warp_wait(smem_u32(&sh.last), 0) && ok;
-    } else if (warp >= 2 && warp < kTailWarp) {
+    } else if (warp >= 2 && warp < kTailWarp<OP>) {
         const int quarter = warp & 3, group = (warp - 2) >> 2;
         float* mine = turn + group * kTurn * kTurnPitch;
         int n = 0;
@@ -788,7 +893,49 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         }
         if (OP == kBackWeights && quarter * 32 + lane == 0) bulk_wait_all();
     }
-    if (OP == kBackWeights && warp == kTailWarp) {
+    if (k8 && warp >= kTailWarp<OP>) {
+        // Widens one half of every stage: this CTA's weights to its tensor memory and its rows to its shared memory, and
+        // hands the piece to the first CTA, which multiplies it.
+        const int half = (warp - kTailWarp<OP>) >> 2, quarter = warp & 3;
+        const uint32_t made0 = tc::in_rank(made, lead);
+        Ring ring;
+        int piece = 0;
+        uint32_t phase = 0;
+        auto next_piece = [&] { if (++piece == kPieces) { piece = 0; phase ^= 1u; } };
+        for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
+            const Tile t = tile_at<OP, GLU>(a, p, sh, i);
+            const int end = end_of(t);
+            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>) {
+                if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
+                    ok = false;
+                    break;
+                }
+                const bool two = end - k0 > kPiece;          // pieces of this stage
+                if (half == 1) next_piece();
+                if (half == 0 || two) {
+                    if (!warp_wait(used + 8 * piece, phase ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t sa = stages + ring.at;
+                    widen_weights(sa, half, tmem + kTop<OP> + piece * kPieceColumns, quarter, lane);
+                    widen_rows(sa + kBytesA, half, pieces + piece * piece_bytes, t.n / 2, quarter, lane);
+                    asm volatile("fence.proxy.async;" ::: "memory");  // also for the first CTA's products
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::arrive_cluster_smem(made0 + 8 * piece);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * ring.stage);
+                if (half == 0 || two) next_piece();
+                if (half == 0 && two) next_piece();
+                ring.next(cut);
+            }
+        }
+    }
+    if (OP == kBackWeights && warp == kTailWarp<OP>) {
         // Clears the rows past an expert's last in its last stage, in this CTA, and hands the stage on.  The copying warp
         // does not wait for it: doing so there cost a memory latency a tile (1024 rows of 32 experts spread by routing,
         // 2048 x 7168: 660 us against 604 us).
@@ -861,11 +1008,12 @@ Cut make_cut(const ExpertArgs& a) {
     Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
-        if (OP != kForward4 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
+        if (OP != kForward4 && OP != kForward8 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
         if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
-    cut.stages = kRingBytes<OP> / cut.bytes < kStages ? kRingBytes<OP> / cut.bytes : kStages;
+    const int ring = kRingBytes<OP> - (OP == kForward8 ? kPieces * cut.columns / 2 * kRowBytes : 0);
+    cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
     return cut;
 }
 
@@ -927,6 +1075,9 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
              tc::make_scale_map(&mb.weight_scales, a.weight_scales, a.E * ((a.N + per - 1) / per) * groups) &&
              tc::make_scale_map(&mb.row_scales, a.row_scales, (a.R / 128 + a.E) * groups);
         for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K / 2, a.R, 0, 8 << i);
+    } else if (OP == kForward8) {
+        ok = tc::make_map(&ma, a.weights, true, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
+        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K, a.R, 0, 8 << i);
     } else {
         ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
         for (int i = 0; i < kMaps; ++i)
@@ -948,7 +1099,9 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
         auto* split = pair_kernel<OP, GLU, true, KEPT>;
         e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
         if (e != cudaSuccess) return e;
-        const int steps = ((OP == kBackRows ? a.W : a.K) + kStep<OP> - 1) / kStep<OP>;
+        // (a stage of integers is two pieces, each a stage's worth of products)
+        constexpr int kWork = OP == kForward8 ? kPiece : kStep<OP>;
+        const int steps = ((OP == kBackRows ? a.W : a.K) + kWork - 1) / kWork;
         int64_t teams = pairs;
         cut.parts = parts_of(reinterpret_cast<const void*>(split), kThreads<OP>, kSmem<OP>, tiles, steps, pairs, &teams);
         if (cut.parts > 1) return start<OP>(split, a, cut, tiles, teams, ma, mb, s);
@@ -972,6 +1125,10 @@ cudaError_t launch_expert_backward_weights(const ExpertArgs& a, cudaStream_t s) 
 
 cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
     return a.glu ? launch<kForward4, true>(a, s) : launch<kForward4, false>(a, s);
+}
+
+cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s) {
+    return a.glu ? launch<kForward8, true>(a, s) : launch<kForward8, false>(a, s);
 }
 
 cudaError_t read_expert_faults(uint32_t* bits, cudaStream_t stream) {
