@@ -76,14 +76,14 @@ template <int OP>
 constexpr int kGroups = OP == kForward8 ? 2 : 4;  // of four warps that store
 template <int OP>
 constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
-constexpr int kWideners = 8;           // warps that widen integers: four for either half of a stage
+constexpr int kWideners = 16;          // warps that widen integers: four for either half of a stage, stages in turn
 template <int OP>                      // warp 0 copies, warp 1 multiplies; in the weights' gradient one more clears
 constexpr int kThreads = 32 * (kTailWarp<OP> + (OP == kBackWeights ? 1 : OP == kForward8 ? kWideners : 0));
 constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // most columns of one product instruction
 constexpr int kFirst = 128;            // a wider tile is two products: this many columns, and the others
 template <int OP>
-constexpr int kTop = OP == kForward4 ? 448 : OP == kForward8 ? 384 : 512;  // columns of tensor memory for sums
+constexpr int kTop = OP == kForward4 ? 448 : 512;  // columns of tensor memory for sums (of integers: cut.top)
 constexpr int kRowBytes = 128;         // of a stage, along memory
 template <int OP>
 constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : OP == kForward8 ? kRowBytes : kRowBytes / 2;  // its contraction
@@ -107,8 +107,7 @@ constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 // 8-bit integers are widened to fp16 (exactly) between copy and product, in pieces of 64 of the contraction: half of what a
 // stage holds.  The weights' pieces lie in tensor memory above the sums, the rows' in shared memory behind the stages.
-constexpr int kPieces = 4, kPiece = 64, kPieceColumns = kPiece / 2;
-static_assert(kTop<kForward8> + kPieces * kPieceColumns == 512);
+constexpr int kPieces = 8, kPiece = 64, kPieceColumns = kPiece / 2;  // (most in flight)
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
@@ -126,6 +125,7 @@ struct Shared {
 struct Cut {
     int columns, stages, bytes;
     int parts;                         // pairs that share a tile
+    int top, pieces;                   // of widened integers: where they start in tensor memory, how many there are
 };
 
 // Where in the ring of stages a thread is.
@@ -272,10 +272,16 @@ __device__ __forceinline__ void turned8(const float* p, bool swap, float (&v)[8]
     v[0] = swap ? b.x : a.x; v[1] = swap ? b.y : a.y; v[2] = swap ? b.z : a.z; v[3] = swap ? b.w : a.w;
     v[4] = swap ? a.x : b.x; v[5] = swap ? a.y : b.y; v[6] = swap ? a.z : b.z; v[7] = swap ? a.w : b.w;
 }
-__device__ __forceinline__ void load_scales(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 8 sums of integers times their scales; WEIGHTS: times the weights' too, first.
+template <bool WEIGHTS>
+__device__ __forceinline__ void scale8(float (&v)[8], float row, const float* weights) {
+    if (WEIGHTS) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(weights)), b = __ldg(reinterpret_cast<const float4*>(weights) + 1);
+        v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
+        v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= row;
 }
 
 // ---- 8-bit integers to fp16 ------------------------------------------------------
@@ -308,18 +314,24 @@ __device__ __forceinline__ void widen_weights(uint32_t stage, int half, uint32_t
     tc::st32(piece + ((uint32_t)(quarter * 32) << 16), v);
 }
 
+__device__ __forceinline__ void store_wide(uint4 w, uint32_t lo, uint32_t hi) {
+    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(lo), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(hi), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
+}
+
 // The same of `rows` receive rows, to rows of 128 bytes in shared memory, swizzled likewise: 8 rows at a time, 8 lanes on
 // one 16-byte piece of each.
 __device__ __forceinline__ void widen_rows(uint32_t stage, int half, uint32_t piece, int rows, int warp, int lane) {
     const int sub = lane & 7, chunk = lane >> 3;
-    for (int r0 = 8 * warp; r0 < rows; r0 += 32) {
-        const uint32_t row = (uint32_t)(r0 + sub) * kRowBytes;
-        const uint4 w = lds_v4(stage + row + (((4 * half + chunk) ^ sub) << 4));
-        const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(piece + row + (((2 * chunk) ^ sub) << 4)), "r"(a.x), "r"(a.y),
-                     "r"(b.x), "r"(b.y) : "memory");
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(piece + row + (((2 * chunk + 1) ^ sub) << 4)), "r"(c.x),
-                     "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
+    const uint32_t from = stage + sub * kRowBytes + (((4 * half + chunk) ^ sub) << 4), to = piece + sub * kRowBytes;
+    const uint32_t lo = to + (((2 * chunk) ^ sub) << 4), hi = to + (((2 * chunk + 1) ^ sub) << 4);
+    for (int r0 = 8 * warp; r0 < rows; r0 += 64) {
+        const bool more = r0 + 32 < rows;
+        const uint4 v = lds_v4(from + r0 * kRowBytes);
+        const uint4 w = more ? lds_v4(from + (r0 + 32) * kRowBytes) : make_uint4(0, 0, 0, 0);
+        store_wide(v, lo + r0 * kRowBytes, hi + r0 * kRowBytes);
+        if (more) store_wide(w, lo + (r0 + 32) * kRowBytes, hi + (r0 + 32) * kRowBytes);
     }
 }
 
@@ -443,11 +455,12 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
     const int count = t.n / kTurn;
     constexpr bool k8 = OP == kForward8;
-    float sg[8], su[8];                                 // scales of this thread's features
-    if constexpr (k8) {
-        const float* scales = static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + f;
-        if (live) load_scales(scales, sg);
-        if (live && GLU) load_scales(scales + a.N, su);
+    // Sums of integers are scaled where they are turned, by this thread's weight row; parts of a sum are added first, which
+    // is exact below 2^24, and scaled where a result row is written.
+    float scale = 1.0f;
+    if constexpr (k8 && !SPLIT) {
+        const int of = t.f0 + cta * kMine + tid % kMine;
+        if (of < p.features) scale = __ldg(static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + of + tid / kMine * a.N);
     }
     auto column = [&](int i) { return (up ? i : count - 1 - i) * kTurn; };
     bool told = false;
@@ -469,7 +482,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         }
         store_sync(group);  // the block before has been read
 #pragma unroll
-        for (int i = 0; i < kTurn; ++i) turn[i * kTurnPitch + tid] = __uint_as_float(v[i]);
+        for (int i = 0; i < kTurn; ++i) turn[i * kTurnPitch + tid] = k8 && !SPLIT ? __uint_as_float(v[i]) * scale : __uint_as_float(v[i]);
         store_sync(group);
         if (SPLIT) {
             if (tid < link.parts)
@@ -521,19 +534,14 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
             if (SPLIT) summed8(from, link, x);
             else turned8(from, swap, x);
             const int64_t at = (c + row) * pitch;
-            const float scale = k8 ? __ldg(static_cast<const float*>(a.row_scales) + r0 + c + row) : 1.0f;
-            if constexpr (k8) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = x[k] * sg[k] * scale;
-            }
+            const float row_scale = k8 ? __ldg(static_cast<const float*>(a.row_scales) + r0 + c + row) : 1.0f;
+            if constexpr (k8) scale8<SPLIT>(x, row_scale, static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + f);
             if (GLU) {
                 float u[8];
                 if (SPLIT) summed8(from + kHalf / 2, link, u);
                 else turned8(from + kHalf / 2, swap, u);
-                if constexpr (k8) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) u[k] = u[k] * su[k] * scale;
-                }
+                if constexpr (k8)
+                    scale8<SPLIT>(u, row_scale, static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + a.N + f);
                 if (a.pre != nullptr) {
                     __nv_bfloat16* pre = static_cast<__nv_bfloat16*>(a.pre) + (r0 + c + row) * a.W + f;
                     store8(pre, x);
@@ -611,7 +619,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int i = 0; i < cut.stages; ++i) {
             // both CTAs' copies arrive on the first CTA's; integers are widened by the CTA that copied them
             mbar_init(full + 8 * i, k8 ? 1 : 2);
-            mbar_init(empty + 8 * i, k8 ? kWideners : 1);
+            mbar_init(empty + 8 * i, k8 ? 8 : 1);
             mbar_init(smem_u32(&sh.tail[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -620,8 +628,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups<OP>);
         }
         if (k8)
-            for (int i = 0; i < kPieces; ++i) {
-                mbar_init(made + 8 * i, kWideners);  // half of them in either CTA
+            for (int i = 0; i < cut.pieces; ++i) {
+                mbar_init(made + 8 * i, 8);  // four warps in either CTA
                 mbar_init(used + 8 * i, 1);
             }
         if (SPLIT)
@@ -743,6 +751,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             }
     } else if (warp == 1 && cta == 0) {
         Ring ring;
+        const int top = k8 ? cut.top : kTop<OP>;
         int n = 0, before = 0;         // tiles so far, columns of the one before
         int piece = 0;
         uint32_t piece_phase = 0;
@@ -750,7 +759,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const bool wide = !across_b && t.n > kColumns;
             // tiles take the low and the high end of tensor memory in turn
-            const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
+            const uint32_t sums = tmem + (n & 1 ? top - t.n : 0);
             // the instruction of the tile and, for a wide one, of its other columns
             const int n0 = wide ? kFirst : t.n, n1 = max(t.n - kFirst, 16);
             const uint32_t instr = tc::instruction_pair(n0, across_a, across_b);
@@ -758,19 +767,19 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             // this end is free when the tile before the last is stored, and what the last one holds of it when its store
             // half has been there
             ok = warp_wait_cluster(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
-            if (ok && before + t.n > kTop<OP>)
+            if (ok && before + t.n > top)
                 ok = warp_wait_cluster(smem_u32(&sh.over[(n + 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
             if (!ok) break;
             before = t.n;
             tc::fence_after_sync();
             const int begin = begin_of(t), end = end_of(t);
             if constexpr (k8) {
-                for (int k0 = begin; k0 < end; k0 += kPiece, piece = (piece + 1) % kPieces, piece_phase ^= piece == 0) {
+                for (int k0 = begin; k0 < end; k0 += kPiece) {
                     ok = warp_wait_cluster(made + 8 * piece, piece_phase);
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (tc::elect_one()) {
-                        const uint32_t wa = tmem + kTop<OP> + piece * kPieceColumns;
+                        const uint32_t wa = tmem + cut.top + piece * kPieceColumns;
                         const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes);
                         const int count = min(kPiece, end - k0) / 16;
 #pragma unroll
@@ -780,6 +789,10 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         tc::commit_pair(used + 8 * piece, both);
                     }
                     __syncwarp();
+                    if (++piece == cut.pieces) {
+                        piece = 0;
+                        piece_phase ^= 1u;
+                    }
                 }
             } else
             for (int k0 = begin; k0 < end; k0 += kStep<OP>) {
@@ -864,7 +877,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
             // columns that the next tile's sums share with this one's, and with them its first blocks to store
             const Tile next = tile_at<OP, GLU>(a, p, sh, min(i + pairs, p.tiles - 1));
-            const int shared = i + pairs < p.tiles ? max(t.n + next.n - kTop<OP>, 0) / kTurn : 0;
+            const int shared = i + pairs < p.tiles ? max(t.n + next.n - (k8 ? cut.top : kTop<OP>), 0) / kTurn : 0;
             // One warp of a group watches the sums' barrier, the others sleep at the group's own: sixteen watching
             // warps would take issue slots from the two that feed the tensor core.  A group gives up together.
             const bool got = ((warp - 2) & 3) != 0 ||
@@ -875,7 +888,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0) + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t sums = tmem + (n & 1 ? (k8 ? cut.top : kTop<OP>) - t.n : 0) + ((uint32_t)(quarter * 32) << 16);
             if constexpr (OP == kBackWeights) {
                 store_weights(p, t, &maps.out, sums, smem_u32(turn) + group * 32 * kHalf * 2, cta, group, quarter * 32 + lane);
             } else {
@@ -894,44 +907,53 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         if (OP == kBackWeights && quarter * 32 + lane == 0) bulk_wait_all();
     }
     if (k8 && warp >= kTailWarp<OP>) {
-        // Widens one half of every stage: this CTA's weights to its tensor memory and its rows to its shared memory, and
-        // hands the piece to the first CTA, which multiplies it.
-        const int half = (warp - kTailWarp<OP>) >> 2, quarter = warp & 3;
+        // Widens one half of every other stage: this CTA's weights to its tensor memory and its rows to its shared memory,
+        // and hands the piece to the first CTA, which multiplies it.
+        const int group = (warp - kTailWarp<OP>) >> 2, half = group & 1, quarter = warp & 3;
         const uint32_t made0 = tc::in_rank(made, lead);
         Ring ring;
         int piece = 0;
         uint32_t phase = 0;
-        auto next_piece = [&] { if (++piece == kPieces) { piece = 0; phase ^= 1u; } };
+        bool mine = group < 2;
+        auto pass = [&](int pieces) {
+            piece += pieces;
+            if (piece >= cut.pieces) {
+                piece -= cut.pieces;
+                phase ^= 1u;
+            }
+        };
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const int end = end_of(t);
-            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>) {
-                if (!warp_wait(full + 8 * ring.stage, ring.phase)) {
-                    ok = false;
-                    break;
+            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = !mine, ring.next(cut)) {
+                const int count = end - k0 > kPiece ? 2 : 1;  // pieces of this stage
+                if (!mine) {
+                    pass(count);
+                    continue;
                 }
-                const bool two = end - k0 > kPiece;          // pieces of this stage
-                if (half == 1) next_piece();
-                if (half == 0 || two) {
-                    if (!warp_wait(used + 8 * piece, phase ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
+                ok = warp_wait(full + 8 * ring.stage, ring.phase);
+                if (!ok) break;
+                if (half < count) {
+                    pass(half);
+                    ok = warp_wait(used + 8 * piece, phase ^ 1u);
+                    if (!ok) break;
                     tc::fence_after_sync();
                     const uint32_t sa = stages + ring.at;
-                    widen_weights(sa, half, tmem + kTop<OP> + piece * kPieceColumns, quarter, lane);
+                    widen_weights(sa, half, tmem + cut.top + piece * kPieceColumns, quarter, lane);
                     widen_rows(sa + kBytesA, half, pieces + piece * piece_bytes, t.n / 2, quarter, lane);
-                    asm volatile("fence.proxy.async;" ::: "memory");  // also for the first CTA's products
+                    fence_proxy_async_smem();
                     tc::wait_st();
                     tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::arrive_cluster_smem(made0 + 8 * piece);
+                    if (lane == 0) {
+                        tc::arrive_cluster_smem(made0 + 8 * piece);
+                        mbar_arrive(empty + 8 * ring.stage);
+                    }
+                    pass(count - half);
+                } else {
+                    if (lane == 0) mbar_arrive(empty + 8 * ring.stage);
+                    pass(count);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty + 8 * ring.stage);
-                if (half == 0 || two) next_piece();
-                if (half == 0 && two) next_piece();
-                ring.next(cut);
             }
         }
     }
@@ -1005,14 +1027,18 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
-    Cut cut{kColumns, 0, 0, 1};
+    Cut cut{kColumns, 0, 0, 1, 0, 0};
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
         if (OP != kForward4 && OP != kForward8 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
         if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
-    const int ring = kRingBytes<OP> - (OP == kForward8 ? kPieces * cut.columns / 2 * kRowBytes : 0);
+    if (OP == kForward8) {
+        cut.top = cut.columns == 64 ? 256 : cut.columns == 128 ? 256 : 384;
+        cut.pieces = (512 - cut.top) / kPieceColumns;
+    }
+    const int ring = kRingBytes<OP> - cut.pieces * cut.columns / 2 * kRowBytes;
     cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
     return cut;
 }
