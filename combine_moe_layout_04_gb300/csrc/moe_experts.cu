@@ -774,14 +774,16 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             tc::fence_after_sync();
             const int begin = begin_of(t), end = end_of(t);
             if constexpr (k8) {
-                for (int k0 = begin; k0 < end; k0 += kPiece) {
+                // (two pieces to every stage; the second of a last one may be empty)
+                const int stop = begin + (end - begin + kStep<OP> - 1) / kStep<OP> * kStep<OP>;
+                for (int k0 = begin; k0 < stop; k0 += kPiece) {
                     ok = warp_wait_cluster(made + 8 * piece, piece_phase);
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (tc::elect_one()) {
                         const uint32_t wa = tmem + cut.top + piece * kPieceColumns;
                         const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes);
-                        const int count = min(kPiece, end - k0) / 16;
+                        const int count = min(kPiece, max(end - k0, 0)) / 16;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (k < count)
@@ -908,51 +910,41 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     }
     if (k8 && warp >= kTailWarp<OP>) {
         // Widens one half of every other stage: this CTA's weights to its tensor memory and its rows to its shared memory,
-        // and hands the piece to the first CTA, which multiplies it.
+        // and hands the piece to the first CTA, which multiplies it.  A barrier's parity tells one phase from the next
+        // alone, so a group must see every phase of the barriers it waits on: the stages are even in number and
+        // the pieces a multiple of four, two to every stage, so that each is always the same group's.
         const int group = (warp - kTailWarp<OP>) >> 2, half = group & 1, quarter = warp & 3;
         const uint32_t made0 = tc::in_rank(made, lead);
         Ring ring;
-        int piece = 0;
+        int piece = half;
         uint32_t phase = 0;
         bool mine = group < 2;
-        auto pass = [&](int pieces) {
-            piece += pieces;
-            if (piece >= cut.pieces) {
-                piece -= cut.pieces;
-                phase ^= 1u;
-            }
-        };
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const int end = end_of(t);
             for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = !mine, ring.next(cut)) {
-                const int count = end - k0 > kPiece ? 2 : 1;  // pieces of this stage
-                if (!mine) {
-                    pass(count);
-                    continue;
-                }
-                ok = warp_wait(full + 8 * ring.stage, ring.phase);
-                if (!ok) break;
-                if (half < count) {
-                    pass(half);
-                    ok = warp_wait(used + 8 * piece, phase ^ 1u);
+                if (mine) {
+                    ok = warp_wait(full + 8 * ring.stage, ring.phase) && warp_wait(used + 8 * piece, phase ^ 1u);
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint32_t sa = stages + ring.at;
-                    widen_weights(sa, half, tmem + cut.top + piece * kPieceColumns, quarter, lane);
-                    widen_rows(sa + kBytesA, half, pieces + piece * piece_bytes, t.n / 2, quarter, lane);
-                    fence_proxy_async_smem();
-                    tc::wait_st();
-                    tc::fence_before_sync();
+                    if (k0 + half * kPiece < end) {
+                        tc::fence_after_sync();
+                        const uint32_t sa = stages + ring.at;
+                        widen_weights(sa, half, tmem + cut.top + piece * kPieceColumns, quarter, lane);
+                        widen_rows(sa + kBytesA, half, pieces + piece * piece_bytes, t.n / 2, quarter, lane);
+                        fence_proxy_async_smem();
+                        tc::wait_st();
+                        tc::fence_before_sync();
+                    }
                     __syncwarp();
                     if (lane == 0) {
                         tc::arrive_cluster_smem(made0 + 8 * piece);
                         mbar_arrive(empty + 8 * ring.stage);
                     }
-                    pass(count - half);
-                } else {
-                    if (lane == 0) mbar_arrive(empty + 8 * ring.stage);
-                    pass(count);
+                }
+                piece += 2;
+                if (piece >= cut.pieces) {
+                    piece -= cut.pieces;
+                    phase ^= 1u;
                 }
             }
         }
@@ -1035,11 +1027,12 @@ Cut make_cut(const ExpertArgs& a) {
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
     if (OP == kForward8) {
-        cut.top = cut.columns == 64 ? 256 : cut.columns == 128 ? 256 : 384;
+        cut.top = cut.columns == 64 ? 256 : 384;
         cut.pieces = (512 - cut.top) / kPieceColumns;
     }
     const int ring = kRingBytes<OP> - cut.pieces * cut.columns / 2 * kRowBytes;
     cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
+    if (OP == kForward8) cut.stages &= ~1;
     return cut;
 }
 

@@ -155,6 +155,7 @@ COUNTS = {
     "a little over a tile": [257, 272, 300, 0, 320, 321, 255, 290],
     "a tile and a half": [384, 360, 385, 350, 400, 0, 391],
     "some dozens": [40, 64, 65, 33, 50, 0, 17],
+    "about a hundred": [90, 104, 128, 129, 72, 0, 100],
     "few each": [2, 1, 0, 3, 1, 1, 2, 0, 0, 1, 4, 1, 0, 1, 2, 1],
 }
 WIDTHS = [(16, 8), (64, 128), (80, 136), (208, 264), (1024, 512), (528, 1016), (128, 8), (4112, 72)]
