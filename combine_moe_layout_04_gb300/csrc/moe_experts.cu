@@ -105,14 +105,14 @@ constexpr int kScaleBlock = 512;
 constexpr int scale_bytes(int columns) { return (columns > 256 ? 4 : 3) * 2 * kScaleBlock; }
 constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
-// 8-bit integers are widened to fp16 (exactly) between copy and product, in pieces of 64 of the contraction: half of what a
-// stage holds.  The weights' pieces lie in tensor memory above the sums, the rows' in shared memory behind the stages.
+// 8-bit integers are widened to fp16 (exactly) between copy and product, in pieces of 64 of the contraction: a stage holds
+// two.  The weights' pieces lie in tensor memory above the sums, the rows' in shared memory behind the stages.
 constexpr int kPieces = 8, kPiece = 64, kPieceColumns = kPiece / 2;  // (most in flight)
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
     uint64_t ready[4], seen[4];        // of a store group's block, by the parts of a tile
-    uint64_t made[kPieces], used[kPieces];  // pieces of widened integers
+    uint64_t made[kPieces / 2], used[kPieces];  // pieces of widened integers, two made together
     uint32_t tmem;
     int scratch[32];
     int base[MOE_MAX_EXPERTS + 1];
@@ -629,7 +629,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         }
         if (k8)
             for (int i = 0; i < cut.pieces; ++i) {
-                mbar_init(made + 8 * i, 8);  // four warps in either CTA
+                if (i % 2 == 0) mbar_init(made + 4 * i, 16);  // eight warps in either CTA
                 mbar_init(used + 8 * i, 1);
             }
         if (SPLIT)
@@ -774,24 +774,34 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             tc::fence_after_sync();
             const int begin = begin_of(t), end = end_of(t);
             if constexpr (k8) {
-                // (two pieces to every stage; the second of a last one may be empty)
-                const int stop = begin + (end - begin + kStep<OP> - 1) / kStep<OP> * kStep<OP>;
-                for (int k0 = begin; k0 < stop; k0 += kPiece) {
-                    ok = warp_wait_cluster(made + 8 * piece, piece_phase);
+                // a stage at a time: both its pieces are waited for at once, and given back one by one
+                const uint32_t instr8 = tc::instruction16_pair(t.n);
+                for (int k0 = begin; k0 < end; k0 += kStep<OP>) {
+                    ok = warp_wait_cluster(made + 4 * piece, piece_phase);
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (tc::elect_one()) {
                         const uint32_t wa = tmem + cut.top + piece * kPieceColumns;
-                        const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes);
-                        const int count = min(kPiece, max(end - k0, 0)) / 16;
+                        const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes), rb1 = rb + (piece_bytes >> 4);
+                        if (end - k0 >= kStep<OP>) {       // without tests between the instructions
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < count)
-                                tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, tc::instruction16_pair(t.n), k0 > begin || k > 0);
-                        tc::commit_pair(used + 8 * piece, both);
+                            for (int k = 0; k < 4; ++k) tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, instr8, k0 > begin || k > 0);
+                            tc::commit_pair(used + 8 * piece, both);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tc::mma_tmem_pair(sums, wa + kPieceColumns + k * 8, rb1 + k * 2, instr8, true);
+                        } else {
+                            const int count = (end - k0) / 16;
+                            for (int k = 0; k < min(count, 4); ++k)
+                                tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, instr8, k0 > begin || k > 0);
+                            tc::commit_pair(used + 8 * piece, both);
+                            for (int k = 4; k < count; ++k)
+                                tc::mma_tmem_pair(sums, wa + k * 8, rb1 + (k - 4) * 2, instr8, true);
+                        }
+                        tc::commit_pair(used + 8 * (piece + 1), both);
                     }
                     __syncwarp();
-                    if (++piece == cut.pieces) {
+                    piece += 2;
+                    if (piece == cut.pieces) {
                         piece = 0;
                         piece_phase ^= 1u;
                     }
@@ -937,7 +947,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        tc::arrive_cluster_smem(made0 + 8 * piece);
+                        tc::arrive_cluster_smem(made0 + 8 * (piece >> 1));
                         mbar_arrive(empty + 8 * ring.stage);
                     }
                 }
