@@ -73,7 +73,7 @@ __device__ unsigned int g_expert_faults;
 
 constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3, kForward8 = 4;
 template <int OP>
-constexpr int kGroups = OP == kForward8 ? 2 : 4;  // of four warps that store
+constexpr int kGroups = OP == kForward8 ? 1 : 4;  // of four warps that store
 template <int OP>
 constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
 constexpr int kWideners = 16;          // warps that widen integers: four for either half of a stage, stages in turn
@@ -83,7 +83,7 @@ constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // most columns of one product instruction
 constexpr int kFirst = 128;            // a wider tile is two products: this many columns, and the others
 template <int OP>
-constexpr int kTop = OP == kForward4 ? 448 : 512;  // columns of tensor memory for sums (of integers: cut.top)
+constexpr int kTop = OP == kForward4 ? 448 : OP == kForward8 ? 384 : 512;  // columns of tensor memory for sums
 constexpr int kRowBytes = 128;         // of a stage, along memory
 template <int OP>
 constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : OP == kForward8 ? kRowBytes : kRowBytes / 2;  // its contraction
@@ -107,7 +107,8 @@ constexpr uint32_t kScalesA = kTop<kForward4>, kScalesB = kScalesA + 8;
 
 // 8-bit integers are widened to fp16 (exactly) between copy and product, in pieces of 64 of the contraction: a stage holds
 // two.  The weights' pieces lie in tensor memory above the sums, the rows' in shared memory behind the stages.
-constexpr int kPieces = 8, kPiece = 64, kPieceColumns = kPiece / 2;  // (most in flight)
+constexpr int kPieces = 4, kPiece = 64, kPieceColumns = kPiece / 2;
+static_assert(kTop<kForward8> + kPieces * kPieceColumns == 512 && kPieces % 4 == 0);
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], done[2], free[2], over[2], last, tail[kStages];
@@ -125,7 +126,6 @@ struct Shared {
 struct Cut {
     int columns, stages, bytes;
     int parts;                         // pairs that share a tile
-    int top, pieces;                   // of widened integers: where they start in tensor memory, how many there are
 };
 
 // Where in the ring of stages a thread is.
@@ -295,14 +295,27 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// Half `half` of a stage's 128 weight rows to a piece in tensor memory: a lane takes a row, 64 bytes of it.  (16-byte pieces
-// of a row lie swizzled by the row, so that 8 lanes cover all banks.)
-__device__ __forceinline__ void widen_weights(uint32_t stage, int half, uint32_t piece, int quarter, int lane) {
-    const int row = quarter * 32 + lane;
+__device__ __forceinline__ void store_wide(uint4 w, uint32_t lo, uint32_t hi) {
+    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(lo), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(hi), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
+}
+
+// Half `half` of a stage to a piece: of its 128 weight rows a lane takes 64 bytes of one, to tensor memory; of its `rows`
+// receive rows 8 lanes take a 16-byte part of 8 rows at a time, to rows of 128 bytes in shared memory.  16-byte parts of a
+// row lie swizzled by the row, here and there, so that 8 lanes cover all banks.  The first rows are loaded ahead: with few
+// rows only one warp of the four has any, and the others would wait for its second round of latencies.
+__device__ __forceinline__ void widen(uint32_t stage, int half, int rows, uint32_t weights, uint32_t piece, int quarter, int lane) {
+    const int row = quarter * 32 + lane, sub = lane & 7, chunk = lane >> 3;
+    const uint32_t from = stage + kBytesA + sub * kRowBytes + (((4 * half + chunk) ^ sub) << 4), to = piece + sub * kRowBytes;
+    const uint32_t lo = to + (((2 * chunk) ^ sub) << 4), hi = to + (((2 * chunk + 1) ^ sub) << 4);
+    const int r1 = 8 * (3 - quarter);
+    uint4 ahead = make_uint4(0, 0, 0, 0);
+    if (r1 < rows) ahead = lds_v4(from + r1 * kRowBytes);
     uint32_t v[kPieceColumns];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 w = lds_v4(stage + row * kRowBytes + (((4 * half + i) ^ (row & 7)) << 4));
+        const uint4 w = lds_v4(stage + row * kRowBytes + (((4 * half + i) ^ sub) << 4));
         const uint32_t b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -311,27 +324,11 @@ __device__ __forceinline__ void widen_weights(uint32_t stage, int half, uint32_t
             v[8 * i + 2 * j + 1] = x.y;
         }
     }
-    tc::st32(piece + ((uint32_t)(quarter * 32) << 16), v);
-}
-
-__device__ __forceinline__ void store_wide(uint4 w, uint32_t lo, uint32_t hi) {
-    const uint2 a = widen4(w.x), b = widen4(w.y), c = widen4(w.z), d = widen4(w.w);
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(lo), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(hi), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
-}
-
-// The same of `rows` receive rows, to rows of 128 bytes in shared memory, swizzled likewise: 8 rows at a time, 8 lanes on
-// one 16-byte piece of each.
-__device__ __forceinline__ void widen_rows(uint32_t stage, int half, uint32_t piece, int rows, int warp, int lane) {
-    const int sub = lane & 7, chunk = lane >> 3;
-    const uint32_t from = stage + sub * kRowBytes + (((4 * half + chunk) ^ sub) << 4), to = piece + sub * kRowBytes;
-    const uint32_t lo = to + (((2 * chunk) ^ sub) << 4), hi = to + (((2 * chunk + 1) ^ sub) << 4);
-    for (int r0 = 8 * warp; r0 < rows; r0 += 64) {
-        const bool more = r0 + 32 < rows;
-        const uint4 v = lds_v4(from + r0 * kRowBytes);
-        const uint4 w = more ? lds_v4(from + (r0 + 32) * kRowBytes) : make_uint4(0, 0, 0, 0);
-        store_wide(v, lo + r0 * kRowBytes, hi + r0 * kRowBytes);
-        if (more) store_wide(w, lo + (r0 + 32) * kRowBytes, hi + (r0 + 32) * kRowBytes);
+    tc::st32(weights + ((uint32_t)(quarter * 32) << 16), v);
+    for (int r0 = r1; r0 < rows; r0 += 32) {
+        const uint4 x = ahead;
+        if (r0 + 32 < rows) ahead = lds_v4(from + (r0 + 32) * kRowBytes);
+        store_wide(x, lo + r0 * kRowBytes, hi + r0 * kRowBytes);
     }
 }
 
@@ -471,10 +468,11 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         told = true;
     };
     uint32_t v[kTurn];
-    if (group < count) tc::ld16(sums + column(group), v);
+    if (!k8 && group < count) tc::ld16(sums + column(group), v);
     for (int b = group; b < count; b += kGroups<OP>) {
         const int c = column(b);
         if (!told && b >= shared) tell();
+        if (k8) tc::ld16(sums + c, v);  // (here the registers that fetching ahead takes cost more than it gives: 115 and 112 us)
         tc::wait_ld();
         if (SPLIT) {
             // the block before has been read by all parts
@@ -492,7 +490,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
             if (!link.ok) break;
             link.phase ^= 1u;
         }
-        if (b + kGroups<OP> < count) tc::ld16(sums + column(b + kGroups<OP>), v);
+        if (!k8 && b + kGroups<OP> < count) tc::ld16(sums + column(b + kGroups<OP>), v);
 #pragma unroll
         for (int i = 0; i < kTurn; i += kAtOnce) {
             const int row = i + tid / kEights;
@@ -628,7 +626,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             mbar_init(smem_u32(&sh.over[i]), 2 * 4 * kGroups<OP>);
         }
         if (k8)
-            for (int i = 0; i < cut.pieces; ++i) {
+            for (int i = 0; i < kPieces; ++i) {
                 if (i % 2 == 0) mbar_init(made + 4 * i, 16);  // eight warps in either CTA
                 mbar_init(used + 8 * i, 1);
             }
@@ -751,7 +749,6 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             }
     } else if (warp == 1 && cta == 0) {
         Ring ring;
-        const int top = k8 ? cut.top : kTop<OP>;
         int n = 0, before = 0;         // tiles so far, columns of the one before
         int piece = 0;
         uint32_t piece_phase = 0;
@@ -759,7 +756,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const bool wide = !across_b && t.n > kColumns;
             // tiles take the low and the high end of tensor memory in turn
-            const uint32_t sums = tmem + (n & 1 ? top - t.n : 0);
+            const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0);
             // the instruction of the tile and, for a wide one, of its other columns
             const int n0 = wide ? kFirst : t.n, n1 = max(t.n - kFirst, 16);
             const uint32_t instr = tc::instruction_pair(n0, across_a, across_b);
@@ -767,7 +764,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
             // this end is free when the tile before the last is stored, and what the last one holds of it when its store
             // half has been there
             ok = warp_wait_cluster(smem_u32(&sh.free[n & 1]), (uint32_t)((n >> 1) & 1) ^ 1u);
-            if (ok && before + t.n > top)
+            if (ok && before + t.n > kTop<OP>)
                 ok = warp_wait_cluster(smem_u32(&sh.over[(n + 1) & 1]), (uint32_t)(((n - 1) >> 1) & 1));
             if (!ok) break;
             before = t.n;
@@ -781,7 +778,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (tc::elect_one()) {
-                        const uint32_t wa = tmem + cut.top + piece * kPieceColumns;
+                        const uint32_t wa = tmem + kTop<OP> + piece * kPieceColumns;
                         const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes), rb1 = rb + (piece_bytes >> 4);
                         if (end - k0 >= kStep<OP>) {       // without tests between the instructions
 #pragma unroll
@@ -801,7 +798,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     }
                     __syncwarp();
                     piece += 2;
-                    if (piece == cut.pieces) {
+                    if (piece == kPieces) {
                         piece = 0;
                         piece_phase ^= 1u;
                     }
@@ -889,7 +886,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         for (int64_t i = pair; i < p.tiles; i += pairs, ++n) {
             // columns that the next tile's sums share with this one's, and with them its first blocks to store
             const Tile next = tile_at<OP, GLU>(a, p, sh, min(i + pairs, p.tiles - 1));
-            const int shared = i + pairs < p.tiles ? max(t.n + next.n - (k8 ? cut.top : kTop<OP>), 0) / kTurn : 0;
+            const int shared = i + pairs < p.tiles ? max(t.n + next.n - kTop<OP>, 0) / kTurn : 0;
             // One warp of a group watches the sums' barrier, the others sleep at the group's own: sixteen watching
             // warps would take issue slots from the two that feed the tensor core.  A group gives up together.
             const bool got = ((warp - 2) & 3) != 0 ||
@@ -900,7 +897,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                 break;
             }
             tc::fence_after_sync();
-            const uint32_t sums = tmem + (n & 1 ? (k8 ? cut.top : kTop<OP>) - t.n : 0) + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t sums = tmem + (n & 1 ? kTop<OP> - t.n : 0) + ((uint32_t)(quarter * 32) << 16);
             if constexpr (OP == kBackWeights) {
                 store_weights(p, t, &maps.out, sums, smem_u32(turn) + group * 32 * kHalf * 2, cta, group, quarter * 32 + lane);
             } else {
@@ -939,8 +936,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     if (k0 + half * kPiece < end) {
                         tc::fence_after_sync();
                         const uint32_t sa = stages + ring.at;
-                        widen_weights(sa, half, tmem + cut.top + piece * kPieceColumns, quarter, lane);
-                        widen_rows(sa + kBytesA, half, pieces + piece * piece_bytes, t.n / 2, quarter, lane);
+                        widen(sa, half, t.n / 2, tmem + kTop<OP> + piece * kPieceColumns, pieces + piece * piece_bytes, quarter, lane);
                         fence_proxy_async_smem();
                         tc::wait_st();
                         tc::fence_before_sync();
@@ -952,8 +948,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     }
                 }
                 piece += 2;
-                if (piece >= cut.pieces) {
-                    piece -= cut.pieces;
+                if (piece >= kPieces) {
+                    piece -= kPieces;
                     phase ^= 1u;
                 }
             }
@@ -1029,20 +1025,16 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
-    Cut cut{kColumns, 0, 0, 1, 0, 0};
+    Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
         cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
         if (OP != kForward4 && OP != kForward8 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
         if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
-    if (OP == kForward8) {
-        cut.top = cut.columns == 64 ? 256 : 384;
-        cut.pieces = (512 - cut.top) / kPieceColumns;
-    }
-    const int ring = kRingBytes<OP> - cut.pieces * cut.columns / 2 * kRowBytes;
+    const int ring = kRingBytes<OP> - (OP == kForward8 ? kPieces * cut.columns / 2 * kRowBytes : 0);
     cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
-    if (OP == kForward8) cut.stages &= ~1;
+    if (OP == kForward8) cut.stages &= ~1;  // (see the widening warps)
     return cut;
 }
 
