@@ -53,6 +53,16 @@
 // scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
 // between the products (333 us then; 32768 rows of 32 experts, 7168 -> 2 x 2048).
 //
+// 8-bit integers.  The tensor core here has no products of them, and fp16 holds them exactly, so sixteen more warps of a CTA
+// widen what the copies bring, weights to tensor memory (a lane a row) and rows to shared memory, and the products take A
+// from the one and B from the other.  Weights in tensor memory, because shared memory would be written and read 32 KB a
+// stage more; sums have 384 of its columns then.  A decode reads half the bytes of bf16 weights (16 tokens, top-8 of 128, 7168 -> 2 x 2048:
+// 411 us, 5.9 TB/s, and 665); a prefill is at the same power limit (4096 tokens, top-8 of 32: 1185 us, 1.62 PFLOP/s).  What the
+// steps there measured (decode, prefill; us): 64 x 64 tiles on the CUDA cores 5245, 32670; eight widening warps 919, 1860;
+// sixteen, stages in turn 627, 1220; the multiplying warp waiting for a stage, not for half of one 517, 1230; one store group, so that a thread
+// has 88 registers and not 72, 424, 1190; four pieces in flight, not eight 411, 1185.  The copies alone take 361 and 458, all
+// but the widening 490 and 991.
+//
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
 
@@ -1022,12 +1032,16 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 //    three 0.987 of four or five [1.004], and those between 1.017 [1.018].  170 rows (16 experts) take 129 us cut at 128 and 97 at 256.
 //    The stages in flight count: 384 columns take 330 us with four and 353 with three (1024 rows), 256 columns 129 with five
 //    and 142 with four (256 rows).
+//  * In 8-bit integers a wide tile pays twice, since its weights are widened for all of its rows at once (8 and 32 experts,
+//    six widths, 128 against 256 columns): 40 to 90 rows take 0.98 of the time, 120 rows 1.07, 230 to 1024 rows 1.2 to 1.36
+//    from 2048 of contraction on, 1.02 at 512 and 1024.  64 columns take 1.00 at 40 rows and 1.19 at 60 (1 row: the same),
+//    192, whose sums lie beside the next tile's, 0.98 up to 1424 of contraction and 1.08 from 2048 on.
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
     Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
-        cut.columns = most <= 64 ? 64 : most <= 128 ? 128 : 256;
+        cut.columns = most <= 64 && OP != kForward8 ? 64 : most <= 128 ? 128 : 256;
         if (OP != kForward4 && OP != kForward8 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
         if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }

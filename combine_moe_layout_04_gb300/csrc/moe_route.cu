@@ -276,10 +276,31 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
         const unsigned other = __shfl_sync(kFull, mine, g * wide);
         before += other > mine || (other == mine && g < group);
     }
-    if (before >= a.kept)
+    int chosen;
+    constexpr int kHalf = V / 2;
+    if (kHalf > 0 && 2 * a.kept <= a.groups) {
+        // The lanes of as many groups that go take the upper half of the keys of those that stay: half as many a lane to
+        // sort and to move.
+        __shared__ int with_rank[kRouteThreads / 32][MOE_MAX_ROUTE_GROUPS];
+        int* groups = with_rank[threadIdx.x >> 5];
+        if (sub == 0 && group < a.groups) groups[before] = group;
+        __syncwarp();
+        const bool stays = before < a.kept && group < a.groups, takes = before >= a.kept && before < 2 * a.kept && group < a.groups;
+        const int from = takes ? groups[before - a.kept] : group;
+        unsigned few[kHalf > 0 ? kHalf : 1], few_id[kHalf > 0 ? kHalf : 1];
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = kTaken;
-    const int chosen = take_largest<V>(key, id, a.k, lane);
+        for (int i = 0; i < kHalf; ++i) {
+            const unsigned theirs = __shfl_sync(kFull, key[kHalf + i], from * wide + sub);
+            few[i] = stays ? key[i] : takes ? theirs : kTaken;
+            few_id[i] = from * size + (i + (takes ? kHalf : 0)) * wide + sub;
+        }
+        chosen = take_largest<(kHalf > 0 ? kHalf : 1)>(few, few_id, a.k, lane);
+    } else {
+        if (before >= a.kept)
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = kTaken;
+        chosen = take_largest<V>(key, id, a.k, lane);
+    }
     const bool on = lane < a.k;
     const float logit = on ? widen(row[chosen]) : -INFINITY;
     float rest;
