@@ -50,6 +50,7 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
 MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_MAX_EXPERT_ROWS = 2 ** 31 - 512
+MOE_MAX_ROUTE_GROUPS = 32
 MOE_LAYOUT_AUTO, MOE_LAYOUT_SPLIT, MOE_LAYOUT_FUSED, MOE_LAYOUT_TWO_KERNELS = 0, 1, 2, 3
 
 # Header word names in index order (include/moe_layout.h, MOE_ST_*).

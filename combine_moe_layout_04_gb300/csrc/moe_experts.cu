@@ -81,26 +81,29 @@ namespace {
 
 __device__ unsigned int g_expert_faults;
 
-constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3, kForward8 = 4;
+constexpr int kForward = 0, kBackRows = 1, kBackWeights = 2, kForward4 = 3, kForward8 = 4, kShort8 = 5;
+template <int OP>                      // integers: a long contraction, or one that the store half would not keep up with
+constexpr bool kIntegers = OP == kForward8 || OP == kShort8;
 template <int OP>
-constexpr int kGroups = OP == kForward8 ? 1 : 4;  // of four warps that store
+constexpr int kGroups = OP == kForward8 ? 1 : OP == kShort8 ? 3 : 4;  // of four warps that store
 template <int OP>
 constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
-constexpr int kWideners = 16;          // warps that widen integers: four for either half of a stage, stages in turn
+template <int OP>                      // warps that widen integers: four for either half of a stage, or twice that, stages in turn
+constexpr int kWideners = OP == kForward8 ? 16 : 8;
 template <int OP>                      // warp 0 copies, warp 1 multiplies; in the weights' gradient one more clears
-constexpr int kThreads = 32 * (kTailWarp<OP> + (OP == kBackWeights ? 1 : OP == kForward8 ? kWideners : 0));
+constexpr int kThreads = 32 * (kTailWarp<OP> + (OP == kBackWeights ? 1 : kIntegers<OP> ? kWideners<OP> : 0));
 constexpr int kHalf = 128;             // rows of the sums in one CTA
 constexpr int kColumns = 256;          // most columns of one product instruction
 constexpr int kFirst = 128;            // a wider tile is two products: this many columns, and the others
 template <int OP>
-constexpr int kTop = OP == kForward4 ? 448 : OP == kForward8 ? 384 : 512;  // columns of tensor memory for sums
+constexpr int kTop = OP == kForward4 ? 448 : kIntegers<OP> ? 384 : 512;  // columns of tensor memory for sums
 constexpr int kRowBytes = 128;         // of a stage, along memory
 template <int OP>
-constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : OP == kForward8 ? kRowBytes : kRowBytes / 2;  // its contraction
+constexpr int kStep = OP == kForward4 ? 2 * kRowBytes : kIntegers<OP> ? kRowBytes : kRowBytes / 2;  // its contraction
 constexpr int kBoxBytes = 64 * kRowBytes;
 constexpr int kBytesA = kHalf * kRowBytes;
 template <int OP>
-constexpr int kRingBytes = (OP == kForward4 ? 176 : OP == kForward8 ? 195 : 180) * 1024;
+constexpr int kRingBytes = (OP == kForward4 ? 176 : OP == kForward8 ? 195 : OP == kShort8 ? 178 : 180) * 1024;
 constexpr int kStages = 12;            // most stages in flight
 constexpr int kTurn = 16;              // columns turned at a time
 constexpr int kTurnPitch = kHalf + 4;  // floats: rows of the turned block start 16 bytes apart in the banks
@@ -461,7 +464,7 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     const int64_t r0 = (int64_t)t.first + t.m0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r0 * pitch + f;
     const int count = t.n / kTurn;
-    constexpr bool k8 = OP == kForward8;
+    constexpr bool k8 = kIntegers<OP>;
     // Sums of integers are scaled where they are turned, by this thread's weight row; parts of a sum are added first, which
     // is exact below 2^24, and scaled where a result row is written.
     float scale = 1.0f;
@@ -601,14 +604,14 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
 
 // Whether the weights' 128 rows of a CTA come in one box.
 template <int OP, bool GLU>
-constexpr bool kOneBox = (OP == kForward || OP == kForward4 || OP == kForward8) && !GLU;
+constexpr bool kOneBox = (OP == kForward || OP == kForward4 || kIntegers<OP>) && !GLU;
 
 // The weights (dout, in the weights' gradient) come through map_a, the rows through maps.
 template <int OP, bool GLU, bool SPLIT, bool KEPT>
 __global__ void __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
-    constexpr bool k4 = OP == kForward4, k8 = OP == kForward8, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
+    constexpr bool k4 = OP == kForward4, k8 = kIntegers<OP>, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
@@ -926,7 +929,7 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         if (OP == kBackWeights && quarter * 32 + lane == 0) bulk_wait_all();
     }
     if (k8 && warp >= kTailWarp<OP>) {
-        // Widens one half of every other stage: this CTA's weights to its tensor memory and its rows to its shared memory,
+        // Widens one half of every (other) stage: this CTA's weights to its tensor memory and its rows to its shared memory,
         // and hands the piece to the first CTA, which multiplies it.  A barrier's parity tells one phase from the next
         // alone, so a group must see every phase of the barriers it waits on: the stages are even in number and
         // the pieces a multiple of four, two to every stage, so that each is always the same group's.
@@ -935,11 +938,12 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
         Ring ring;
         int piece = half;
         uint32_t phase = 0;
+        constexpr bool kInTurn = kWideners<OP> > 8;
         bool mine = group < 2;
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const int end = end_of(t);
-            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = !mine, ring.next(cut)) {
+            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = mine != kInTurn, ring.next(cut)) {
                 if (mine) {
                     ok = warp_wait(full + 8 * ring.stage, ring.phase) && warp_wait(used + 8 * piece, phase ^ 1u);
                     if (!ok) break;
@@ -1041,14 +1045,14 @@ Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
     Cut cut{kColumns, 0, 0, 1};
     if (OP != kBackWeights) {
-        cut.columns = most <= 64 && OP != kForward8 ? 64 : most <= 128 ? 128 : 256;
-        if (OP != kForward4 && OP != kForward8 && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
+        cut.columns = most <= 64 && !kIntegers<OP> ? 64 : most <= 128 ? 128 : 256;
+        if (OP != kForward4 && !kIntegers<OP> && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
         if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
     }
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
-    const int ring = kRingBytes<OP> - (OP == kForward8 ? kPieces * cut.columns / 2 * kRowBytes : 0);
+    const int ring = kRingBytes<OP> - (kIntegers<OP> ? kPieces * cut.columns / 2 * kRowBytes : 0);
     cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
-    if (OP == kForward8) cut.stages &= ~1;  // (see the widening warps)
+    if (kIntegers<OP>) cut.stages &= ~1;  // (see the widening warps)
     return cut;
 }
 
@@ -1110,7 +1114,7 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
              tc::make_scale_map(&mb.weight_scales, a.weight_scales, a.E * ((a.N + per - 1) / per) * groups) &&
              tc::make_scale_map(&mb.row_scales, a.row_scales, (a.R / 128 + a.E) * groups);
         for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K / 2, a.R, 0, 8 << i);
-    } else if (OP == kForward8) {
+    } else if (kIntegers<OP>) {
         ok = tc::make_map(&ma, a.weights, true, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
         for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K, a.R, 0, 8 << i);
     } else {
@@ -1130,12 +1134,12 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     auto* whole = pair_kernel<OP, GLU, false, KEPT>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(whole), kSmem<OP>);
     if (e != cudaSuccess) return e;
-    if constexpr (OP != kBackWeights) {
+    if constexpr (OP != kBackWeights && OP != kShort8) {
         auto* split = pair_kernel<OP, GLU, true, KEPT>;
         e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
         if (e != cudaSuccess) return e;
         // (a stage of integers is two pieces, each a stage's worth of products)
-        constexpr int kWork = OP == kForward8 ? kPiece : kStep<OP>;
+        constexpr int kWork = kIntegers<OP> ? kPiece : kStep<OP>;
         const int steps = ((OP == kBackRows ? a.W : a.K) + kWork - 1) / kWork;
         int64_t teams = pairs;
         cut.parts = parts_of(reinterpret_cast<const void*>(split), kThreads<OP>, kSmem<OP>, tiles, steps, pairs, &teams);
@@ -1162,7 +1166,14 @@ cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
     return a.glu ? launch<kForward4, true>(a, s) : launch<kForward4, false>(a, s);
 }
 
+// Few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the widening warps are
+// faster (32 experts, 1024 rows; 1024 features: 256 of contraction 79.2 -> 43.0 us, 512 82.5 -> 49.0, 1024 91.6 -> 76.5; 1424 ->
+// 2568: 241.7 and 239.9; 3584 -> 2 x 2048: 651 and 703; four groups: 39.6, 50.2, 79.3).  With few rows the weights are (16 rows, 1024 ->
+// 2048: 21.0 and 24.8 us).
+constexpr int kLeastLong = 1200;
+static_assert(kLeastLong <= kLeastShared * kPiece);  // (no tile of the short ones is shared)
 cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s) {
+    if (a.K < kLeastLong && make_cut<kShort8>(a).columns > 128) return a.glu ? launch<kShort8, true>(a, s) : launch<kShort8, false>(a, s);
     return a.glu ? launch<kForward8, true>(a, s) : launch<kForward8, false>(a, s);
 }
 
