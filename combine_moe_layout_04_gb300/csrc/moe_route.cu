@@ -186,12 +186,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
 // that a group's two largest keys meet in a few exchanges.  A warp ranks the groups by comparing every
 // group's value with every other's, and takes the k largest keys of those that stay.
 
-constexpr unsigned kMasked = 0x007fffffu;  // the key of -infinity
-
-// The float of a key; -infinity for a NaN's and for none.
+// key_of without NaN, which counts as -infinity here, and without -0, which no sum of a score and a bias is.
+__device__ __forceinline__ unsigned short_key_of(float v) {
+    const unsigned u = __float_as_uint(fmaxf(v, -INFINITY));
+    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+// The float of such a key; -infinity for none.
 __device__ __forceinline__ float value_of(unsigned key) {
-    if (key <= kMasked) return -INFINITY;
-    return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
+    return key == kTaken ? -INFINITY : __uint_as_float(key ^ (~(unsigned)((int)key >> 31) | 0x80000000u));
 }
 
 // Sum of one value a lane and V each, rounded once: every addition's error is kept and added at the end.  Keys are made
@@ -212,6 +214,35 @@ __device__ __forceinline__ float sum_once(const float (&v)[V]) {
         add(x, more);
     }
     return s + err;
+}
+
+// take_largest among the groups that stay, their keys spread over PARTS times as many lanes, those of groups that go: fewer
+// keys a lane to sort and to move.  before: how many groups come before this lane's.
+template <int V, int PARTS>
+__device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&key)[V], int group, int sub, int wide, int before,
+                                           int lane) {
+    constexpr int kFew = V / PARTS;
+    __shared__ int with_rank[kRouteThreads / 32][MOE_MAX_ROUTE_GROUPS];
+    int* ranked = with_rank[threadIdx.x >> 5];
+    if (sub == 0 && group < a.groups) ranked[before] = group;
+    __syncwarp();
+    const int part = before / a.kept;                        // of the keys of the group with rank before % kept
+    const bool takes = group < a.groups && part < PARTS;
+    const int from = takes ? ranked[before - part * a.kept] : 0;
+    unsigned few[kFew], id[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+        unsigned mine = kTaken;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            // (a lane of a group that stays keeps the first part of its own)
+            const unsigned theirs = q == 0 ? key[i] : __shfl_sync(kFull, key[q * kFew + i], from * wide + sub);
+            if (q == part) mine = theirs;
+        }
+        few[i] = takes ? mine : kTaken;
+        id[i] = from * (a.E / a.groups) + (part * kFew + i) * wide + sub;
+    }
+    return take_largest<kFew>(few, id, a.k, lane);
 }
 
 template <typename T, int V>
@@ -251,12 +282,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
     unsigned first = kTaken, second = kTaken;                // the two largest keys of this lane, then of its group
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if ((int)id[i] >= a.E) {
-            key[i] = kTaken;
-        } else {
-            const float k = score[i] == 0.0f ? -INFINITY : a.bias != nullptr ? score[i] + a.bias[id[i]] : score[i];
-            key[i] = key_of(k);
-        }
+        const float with_bias = a.bias != nullptr && (int)id[i] < a.E ? score[i] + a.bias[id[i]] : score[i];
+        key[i] = short_key_of(score[i] == 0.0f ? -INFINITY : with_bias);
+        if ((int)id[i] >= a.E) key[i] = kTaken;
         second = max(second, min(first, key[i]));
         first = max(first, key[i]);
     }
@@ -270,31 +298,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
         const float more = value_of(second);
         if (more != -INFINITY) value += more;
     }
-    const unsigned mine = key_of(value);
-    int before = 0;                                          // groups that come before this one
-    for (int g = 0; g < a.groups; ++g) {
-        const unsigned other = __shfl_sync(kFull, mine, g * wide);
-        before += other > mine || (other == mine && g < group);
-    }
+    const unsigned mine = short_key_of(value);
+    int before = 0;                                          // groups that come before this one: equal ones by index
+#pragma unroll 4
+    for (int g = 0; g < a.groups; ++g) before += __shfl_sync(kFull, mine, g * wide) + (g < group) > mine;
     int chosen;
-    constexpr int kHalf = V / 2;
-    if (kHalf > 0 && 2 * a.kept <= a.groups) {
-        // The lanes of as many groups that go take the upper half of the keys of those that stay: half as many a lane to
-        // sort and to move.
-        __shared__ int with_rank[kRouteThreads / 32][MOE_MAX_ROUTE_GROUPS];
-        int* groups = with_rank[threadIdx.x >> 5];
-        if (sub == 0 && group < a.groups) groups[before] = group;
-        __syncwarp();
-        const bool stays = before < a.kept && group < a.groups, takes = before >= a.kept && before < 2 * a.kept && group < a.groups;
-        const int from = takes ? groups[before - a.kept] : group;
-        unsigned few[kHalf > 0 ? kHalf : 1], few_id[kHalf > 0 ? kHalf : 1];
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) {
-            const unsigned theirs = __shfl_sync(kFull, key[kHalf + i], from * wide + sub);
-            few[i] = stays ? key[i] : takes ? theirs : kTaken;
-            few_id[i] = from * size + (i + (takes ? kHalf : 0)) * wide + sub;
-        }
-        chosen = take_largest<(kHalf > 0 ? kHalf : 1)>(few, few_id, a.k, lane);
+    if (V >= 4 && 4 * a.kept <= a.groups) {
+        chosen = take_spread<V, V >= 4 ? 4 : 1>(a, key, group, sub, wide, before, lane);
+    } else if (V >= 2 && 2 * a.kept <= a.groups) {
+        chosen = take_spread<V, V >= 2 ? 2 : 1>(a, key, group, sub, wide, before, lane);
     } else {
         if (before >= a.kept)
 #pragma unroll

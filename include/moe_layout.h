@@ -502,13 +502,13 @@ typedef struct moe_grouping {
  *   score = softmax over all E logits, or 1 / (1 + exp(-logit)), in fp32, with the
  *     softmax's sum rounded once from a sum of twice that precision;
  *   key = score, or score + bias (one fp32 addition); a score of 0 (a logit of
- *     -infinity, or too low for its exponential) has key -infinity whatever its bias;
+ *     -infinity, or too low for its exponential) has key -infinity whatever its bias,
+ *     and so has a NaN;
  *   value of a group: its largest key, or that plus the second largest unless that is
- *     -infinity; a NaN key counts as -infinity here.
+ *     -infinity.
  * The kept groups are those with the largest values, equal values by the lower
  * index.  ids[t] = the k experts of kept groups with the largest key, in falling
- * order, equal keys by the lower index, a NaN key after every number: in range and
- * distinct.  gates, arguments and types as for moe_route; moe_route_backward takes
+ * order, equal keys by the lower index: in range and distinct whatever the logits.  gates, arguments and types as for moe_route; moe_route_backward takes
  * the ids as they are (the choice itself has no gradient). */
 int moe_route_groups(const moe_problem* problem, const moe_routing* routing, const moe_grouping* grouping,
                      const void* logits, const float* bias, int32_t* ids, float* gates, moe_stream_t stream);

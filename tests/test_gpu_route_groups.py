@@ -34,8 +34,8 @@ def _scores(x, score):
 
 
 def _order(v):
-    """Indexes in falling order, NaN after -infinity, equal values by index."""
-    return np.lexsort((np.broadcast_to(np.arange(v.shape[1]), v.shape), np.where(np.isnan(v), 0, -v), np.isnan(v)), axis=1)
+    """Indexes in falling order, equal values by index."""
+    return np.lexsort((np.broadcast_to(np.arange(v.shape[1]), v.shape), -v), axis=1)
 
 
 def _reference(x, bias, G, kept, top, k, score):
@@ -48,8 +48,8 @@ def _reference(x, bias, G, kept, top, k, score):
         with np.errstate(all="ignore"):
             s32 = np.float32(1) / (np.float32(1) + np.exp(-x.astype(np.float64)).astype(np.float32))
     key = (s32 if bias is None else s32 + bias).astype(np.float64)
-    key = np.where(s32 == 0, -np.inf, key)
-    best = -np.sort(-np.where(np.isnan(key), -np.inf, key).reshape(T, G, E // G), axis=2)
+    key = np.where((s32 == 0) | np.isnan(key), -np.inf, key)
+    best = -np.sort(-key.reshape(T, G, E // G), axis=2)
     value = best[..., 0].copy()
     if top == 2 and E > G:
         value = value + np.where(np.isneginf(best[..., 1]), 0, best[..., 1])
@@ -59,7 +59,6 @@ def _reference(x, bias, G, kept, top, k, score):
     on = np.repeat(on, E // G, axis=1)
 
     def near(v, n, ties):
-        v = np.where(np.isnan(v), -np.inf, v)
         v = -np.sort(-v, axis=1)[:, : n + 1]
         with np.errstate(all="ignore"):
             d = v[:, :-1] - v[:, 1:]
@@ -68,7 +67,7 @@ def _reference(x, bias, G, kept, top, k, score):
     size = np.nan_to_num(s).max(axis=1) + (0 if bias is None else float(np.abs(np.nan_to_num(bias)).max()))
     gap = np.minimum(near(value, kept, False), near(np.where(on, key64, -np.inf), k, True)) / np.maximum(size, 1e-300)
     # an expert of a group that stays comes before any other, whatever its key
-    order = np.lexsort((np.broadcast_to(np.arange(E), (T, E)), np.where(np.isnan(key), 0, -key), np.isnan(key), ~on), axis=1)
+    order = np.lexsort((np.broadcast_to(np.arange(E), (T, E)), -key, ~on), axis=1)
     return order[:, :k], gap
 
 
