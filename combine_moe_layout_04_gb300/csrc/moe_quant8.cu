@@ -5,6 +5,9 @@
 // A row is read once: its threads keep it in registers, 16 columns (32 bytes) a lane at a time and up to four times,
 // while they find its largest magnitude.  A warp takes rows of up to 2048 columns, a block of 128 threads up to
 // 8192, one of 512 up to 32768; longer rows are read twice.
+//
+// HBM-bound: 2 bytes in and 1 out a column, 32768 rows of 7168 in 99 us (7.1 TB/s; a block of 256 threads reading every row twice,
+// the second time out of L2, took 113), 11994 rows of 1424 in 6.9 (14.3), 128 rows of 7168 in 4.9 us of host time.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
