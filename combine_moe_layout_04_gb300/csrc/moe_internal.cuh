@@ -197,6 +197,7 @@ struct RouteArgs {
     bool renorm, bf16;
     float scale;
     int groups, kept, top;   // choice limited to groups of experts
+    int size, bits;          // experts of a group, logarithm of its lanes (the launcher's)
 };
 
 // ---- inline PTX helpers --------------------------------------------------

@@ -226,15 +226,16 @@ __device__ __forceinline__ float sum_once(const float (&v)[V]) {
 // take_largest among the groups that stay, their keys spread over PARTS times as many lanes, those of groups that go: fewer
 // keys a lane to sort and to move.  before: how many groups come before this lane's.
 template <int V, int PARTS>
-__device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&key)[V], int group, int sub, int wide, int before,
-                                           int lane) {
+__device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&key)[V], int group, int sub, int before, int lane) {
     constexpr int kFew = V / PARTS;
     __shared__ int with_rank[kRouteThreads / 32][MOE_MAX_ROUTE_GROUPS];
     int* ranked = with_rank[threadIdx.x >> 5];
     if (sub == 0 && group < a.groups) ranked[before] = group;
     __syncwarp();
-    const int part = before / a.kept;                        // of the keys of the group with rank before % kept
-    const bool takes = group < a.groups && part < PARTS;
+    int part = 0;                                            // of the keys of the group with rank before - part * kept
+#pragma unroll
+    for (int q = 1; q < PARTS; ++q) part += before >= q * a.kept;
+    const bool takes = group < a.groups && before < PARTS * a.kept;
     const int from = takes ? ranked[before - part * a.kept] : 0;
     unsigned few[kFew], id[kFew];
 #pragma unroll
@@ -243,11 +244,11 @@ __device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
             // (a lane of a group that stays keeps the first part of its own)
-            const unsigned theirs = q == 0 ? key[i] : __shfl_sync(kFull, key[q * kFew + i], from * wide + sub);
+            const unsigned theirs = q == 0 ? key[i] : __shfl_sync(kFull, key[q * kFew + i], (from << a.bits) + sub);
             if (q == part) mine = theirs;
         }
         few[i] = takes ? mine : kTaken;
-        id[i] = from * (a.E / a.groups) + (part * kFew + i) * wide + sub;
+        id[i] = from * a.size + ((part * kFew + i) << a.bits) + sub;
     }
     return take_largest<kFew>(few, id, a.k, lane);
 }
@@ -259,15 +260,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
     pdl_wait();
     pdl_launch_dependents();
     if (t >= a.T) return;
-    const int size = a.E / a.groups;                         // experts of a group
-    const int wide = 1 << (31 - __clz(32 / a.groups));       // lanes of a group
-    const int group = lane / wide, sub = lane % wide;
+    const int size = a.size, wide = 1 << a.bits;             // experts and lanes of a group
+    const int group = lane >> a.bits, sub = lane & (wide - 1);
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
     float l[V], score[V];
     unsigned key[V], id[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = i * wide + sub;
+        const int at = (i << a.bits) + sub;
         const bool live = group < a.groups && at < size;
         id[i] = live ? group * size + at : a.E + i;
         l[i] = live ? widen(row[id[i]]) : -INFINITY;
@@ -308,12 +308,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
     const unsigned mine = short_key_of(value);
     int before = 0;                                          // groups that come before this one: equal ones by index
 #pragma unroll 4
-    for (int g = 0; g < a.groups; ++g) before += __shfl_sync(kFull, mine, g * wide) + (g < group) > mine;
+    for (int g = 0; g < a.groups; ++g) before += __shfl_sync(kFull, mine, g << a.bits) + (g < group) > mine;
     int chosen;
     if (V >= 4 && 4 * a.kept <= a.groups) {
-        chosen = take_spread<V, V >= 4 ? 4 : 1>(a, key, group, sub, wide, before, lane);
+        chosen = take_spread<V, V >= 4 ? 4 : 1>(a, key, group, sub, before, lane);
     } else if (V >= 2 && 2 * a.kept <= a.groups) {
-        chosen = take_spread<V, V >= 2 ? 2 : 1>(a, key, group, sub, wide, before, lane);
+        chosen = take_spread<V, V >= 2 ? 2 : 1>(a, key, group, sub, before, lane);
     } else {
         if (before >= a.kept)
 #pragma unroll
@@ -413,9 +413,7 @@ cudaError_t launch_grouped(const RouteArgs& a, cudaStream_t s) {
 // By the experts of a lane: those of a group over its lanes (up to 60, where a group has one lane).
 template <typename T>
 cudaError_t pick_grouped(const RouteArgs& a, cudaStream_t s) {
-    int wide = 1;
-    while (2 * wide * a.groups <= 32) wide *= 2;
-    const int each = (a.E / a.groups + wide - 1) / wide;
+    const int each = (a.size + (1 << a.bits) - 1) >> a.bits;
     if (each <= 1) return launch_grouped<T, 1>(a, s);
     if (each <= 2) return launch_grouped<T, 2>(a, s);
     if (each <= 4) return launch_grouped<T, 4>(a, s);
@@ -427,7 +425,10 @@ cudaError_t pick_grouped(const RouteArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_route_groups(const RouteArgs& a, cudaStream_t s) {
+cudaError_t launch_route_groups(const RouteArgs& args, cudaStream_t s) {
+    RouteArgs a = args;
+    a.size = a.E / a.groups;
+    for (a.bits = 0; (2 << a.bits) * a.groups <= 32;) ++a.bits;
     return a.bf16 ? pick_grouped<__nv_bfloat16>(a, s) : pick_grouped<float>(a, s);
 }
 
