@@ -197,7 +197,8 @@ struct RouteArgs {
     bool renorm, bf16;
     float scale;
     int groups, kept, top;   // choice limited to groups of experts
-    int size, bits;          // experts of a group, logarithm of its lanes (the launcher's)
+    int size, bits;          // experts of a group, logarithm of its lanes (the launcher's, as the next)
+    bool fours;              // logits and bias can be loaded four at a time
 };
 
 // ---- inline PTX helpers --------------------------------------------------

@@ -223,6 +223,22 @@ __device__ __forceinline__ float sum_once(const float (&v)[V]) {
     return s + err;
 }
 
+// Which expert of its group is value j of a lane: four neighbours a lane in turn, so that they come in one load, or, with
+// less than four values a lane, one.
+template <int V>
+__device__ __forceinline__ int place(int j, int bits, int sub) {
+    return V >= 4 ? ((j >> 2) << (bits + 2)) + (sub << 2) + (j & 3) : (j << bits) + sub;
+}
+__device__ __forceinline__ void load4(const float* p, float* v) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+
 // take_largest among the groups that stay, their keys spread over PARTS times as many lanes, those of groups that go: fewer
 // keys a lane to sort and to move.  before: how many groups come before this lane's.
 template <int V, int PARTS>
@@ -248,7 +264,7 @@ __device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&
             if (q == part) mine = theirs;
         }
         few[i] = takes ? mine : kTaken;
-        id[i] = from * a.size + ((part * kFew + i) << a.bits) + sub;
+        id[i] = from * a.size + place<V>(part * kFew + i, a.bits, sub);
     }
     return take_largest<kFew>(few, id, a.k, lane);
 }
@@ -263,14 +279,29 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
     const int size = a.size, wide = 1 << a.bits;             // experts and lanes of a group
     const int group = lane >> a.bits, sub = lane & (wide - 1);
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
-    float l[V], score[V];
+    float l[V], score[V], bias[V];
     unsigned key[V], id[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int at = (i << a.bits) + sub;
-        const bool live = group < a.groups && at < size;
-        id[i] = live ? group * size + at : a.E + i;
-        l[i] = live ? widen(row[id[i]]) : -INFINITY;
+        const int at = place<V>(i, a.bits, sub);
+        id[i] = group < a.groups && at < size ? group * size + at : a.E + i;
+        l[i] = -INFINITY;
+        bias[i] = 0.0f;
+    }
+    if (V >= 4 && a.fours) {
+#pragma unroll
+        for (int i = 0; i + 3 < V; i += 4) {
+            if ((int)id[i] >= a.E) continue;
+            load4(row + id[i], l + i);
+            if (a.bias != nullptr) load4(a.bias + id[i], bias + i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if ((int)id[i] >= a.E) continue;
+            l[i] = widen(row[id[i]]);
+            if (a.bias != nullptr) bias[i] = a.bias[id[i]];
+        }
     }
     if (a.score == MOE_SCORE_SOFTMAX) {
         float top = -INFINITY;
@@ -289,8 +320,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
     unsigned first = kTaken, second = kTaken;                // the two largest keys of this lane, then of its group
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float with_bias = a.bias != nullptr && (int)id[i] < a.E ? score[i] + a.bias[id[i]] : score[i];
-        key[i] = short_key_of(score[i] == 0.0f ? -INFINITY : with_bias);
+        key[i] = short_key_of(score[i] == 0.0f ? -INFINITY : score[i] + bias[i]);  // (no bias: + 0 changes no score)
         if ((int)id[i] >= a.E) key[i] = kTaken;
         second = max(second, min(first, key[i]));
         first = max(first, key[i]);
@@ -413,7 +443,8 @@ cudaError_t launch_grouped(const RouteArgs& a, cudaStream_t s) {
 // By the experts of a lane: those of a group over its lanes (up to 60, where a group has one lane).
 template <typename T>
 cudaError_t pick_grouped(const RouteArgs& a, cudaStream_t s) {
-    const int each = (a.size + (1 << a.bits) - 1) >> a.bits;
+    int each = (a.size + (1 << a.bits) - 1) >> a.bits;
+    if (each > 2) each = (a.size + (4 << a.bits) - 1) / (4 << a.bits) * 4;  // in fours
     if (each <= 1) return launch_grouped<T, 1>(a, s);
     if (each <= 2) return launch_grouped<T, 2>(a, s);
     if (each <= 4) return launch_grouped<T, 4>(a, s);
@@ -429,6 +460,8 @@ cudaError_t launch_route_groups(const RouteArgs& args, cudaStream_t s) {
     RouteArgs a = args;
     a.size = a.E / a.groups;
     for (a.bits = 0; (2 << a.bits) * a.groups <= 32;) ++a.bits;
+    a.fours = a.size % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0 &&
+              reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     return a.bf16 ? pick_grouped<__nv_bfloat16>(a, s) : pick_grouped<float>(a, s);
 }
 

@@ -271,3 +271,22 @@ def test_streams_graphs_and_two_calls_at_once(moe):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0][0], want[1][0]) and torch.equal(out[0][1], want[1][1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_least_alignment_gives_the_same(moe, dtype):
+    """Logits and bias that start on their type's own size alone: the same bits as aligned ones."""
+    import torch
+    T, E = 65, 160
+    kind = torch.float32 if dtype == "f32" else torch.bfloat16
+    g = torch.Generator().manual_seed(9)
+    logits, bias = torch.randn((T, E), generator=g).to(kind).cuda(), (0.1 * torch.randn(E, generator=g)).cuda()
+    raw, raw_bias = torch.empty(T * E + 8, dtype=kind, device="cuda"), torch.empty(E + 4, device="cuda")
+    want = _run(moe, logits, bias, 8, 3, 2, 6, "sigmoid")[2:]
+    for shift in (1, 2, 3):
+        x, b = raw[shift:shift + T * E].view(T, E), raw_bias[shift:shift + E]
+        x.copy_(logits)
+        b.copy_(bias)
+        for lo, bi in ((x, bias), (logits, b), (x, b)):
+            got = _run(moe, lo, bi, 8, 3, 2, 6, "sigmoid")[2:]
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
