@@ -90,6 +90,8 @@ template <int OP>
 constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
 template <int OP>                      // warps that widen integers: four for either half of a stage, or twice that, stages in turn
 constexpr int kWideners = OP == kForward8 ? 16 : 8;
+template <int OP>
+constexpr bool kInTurn = kWideners<OP> > 8;
 template <int OP>                      // warp 0 copies, warp 1 multiplies; in the weights' gradient one more clears
 constexpr int kThreads = 32 * (kTailWarp<OP> + (OP == kBackWeights ? 1 : kIntegers<OP> ? kWideners<OP> : 0));
 constexpr int kHalf = 128;             // rows of the sums in one CTA
@@ -938,19 +940,19 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     if (k8 && warp >= kTailWarp<OP>) {
         // Widens one half of every (other) stage: this CTA's weights to its tensor memory and its rows to its shared memory,
         // and hands the piece to the first CTA, which multiplies it.  A barrier's parity tells one phase from the next
-        // alone, so a group must see every phase of the barriers it waits on: the stages are even in number and
-        // the pieces a multiple of four, two to every stage, so that each is always the same group's.
+        // alone, so a group must see every phase of the barriers it waits on.  Where two sets of groups take stages in turn
+        // the stages are even in number and the pieces a multiple of four, two to every stage, so that each is always the same
+        // group's.
         const int group = (warp - kTailWarp<OP>) >> 2, half = group & 1, quarter = warp & 3;
         const uint32_t made0 = tc::in_rank(made, lead);
         Ring ring;
         int piece = half;
         uint32_t phase = 0;
-        constexpr bool kInTurn = kWideners<OP> > 8;
         bool mine = group < 2;
         for (int64_t i = pair; i < p.tiles && ok; i += pairs) {
             const Tile t = tile_at<OP, GLU>(a, p, sh, i);
             const int end = end_of(t);
-            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = mine != kInTurn, ring.next(cut)) {
+            for (int k0 = begin_of(t); k0 < end; k0 += kStep<OP>, mine = mine != kInTurn<OP>, ring.next(cut)) {
                 if (mine) {
                     ok = warp_wait(full + 8 * ring.stage, ring.phase) && warp_wait(used + 8 * piece, phase ^ 1u);
                     if (!ok) break;
@@ -1059,7 +1061,7 @@ Cut make_cut(const ExpertArgs& a) {
     cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
     const int ring = kRingBytes<OP> - (kIntegers<OP> ? kPieces * cut.columns / 2 * kRowBytes : 0);
     cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
-    if (kIntegers<OP>) cut.stages &= ~1;  // (see the widening warps)
+    if (kIntegers<OP> && kInTurn<OP>) cut.stages &= ~1;  // (see the widening warps)
     return cut;
 }
 

@@ -28,10 +28,10 @@ def test_groups_keep_their_barriers():
     four give every barrier to one set."""
     text = _text()
     assert "static_assert(kTop<kForward8> + kPieces * kPieceColumns == 512 && kPieces % 4 == 0)" in text
-    assert "if (kIntegers<OP>) cut.stages &= ~1;" in text
-    for ring, columns in ((195 * 1024, 128), (195 * 1024, 256), (178 * 1024, 128), (178 * 1024, 256)):
-        stages = (ring - 4 * columns // 2 * 128) // (128 * 128 + columns // 2 * 128) & ~1
-        assert stages >= 2
+    assert "if (kIntegers<OP> && kInTurn<OP>) cut.stages &= ~1;" in text
+    for columns in (128, 256):
+        stages = (195 * 1024 - 4 * columns // 2 * 128) // (128 * 128 + columns // 2 * 128) & ~1
+        assert stages >= 4
         owner = {}
         for use in range(8 * stages):
             for kind, slot in (("stage", use % stages), ("piece", 2 * use % 4), ("piece", (2 * use + 1) % 4)):
