@@ -1175,12 +1175,12 @@ cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
     return a.glu ? launch<kForward4, true>(a, s) : launch<kForward4, false>(a, s);
 }
 
-// Few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the widening warps are
-// faster (32 experts, 1024 rows; 1024 features: 256 of contraction 79.2 -> 43.0 us, 512 82.5 -> 49.0, 1024 91.6 -> 76.5; 1424 ->
-// 2568: 241.7 and 239.9; 3584 -> 2 x 2048: 651 and 703; four groups: 39.6, 50.2, 79.3).  With few rows the weights are (16 rows, 1024 ->
-// 2048: 21.0 and 24.8 us).
-constexpr int kLeastLong = 1200;
-static_assert(kLeastLong <= kLeastShared * kPiece);  // (no tile of the short ones is shared)
+// Few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the widening
+// warps are faster (8 and 40 experts, 130 to 1024 rows: 1024 of contraction takes 0.83 of the time, 1200 0.87, 1424 to 1792 0.95; 32
+// experts of 1024 rows, 512 -> 1024: 82.5 -> 50 us; with two stages in flight for three 3584 -> 2 x 2048 took 703 and not 651; four
+// groups: 0.99 to 1.03 of three).  With few rows the weights are what counts (16 rows, 1024 -> 2048: 21.0 and 24.8 us).
+// So up to the contraction from which on tiles may be shared, which these never are.
+constexpr int kLeastLong = kLeastShared * kPiece;
 cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s) {
     if (a.K < kLeastLong && make_cut<kShort8>(a).columns > 128) return a.glu ? launch<kShort8, true>(a, s) : launch<kShort8, false>(a, s);
     return a.glu ? launch<kForward8, true>(a, s) : launch<kForward8, false>(a, s);
