@@ -56,12 +56,12 @@
 // 8-bit integers.  The tensor core here has no products of them, and fp16 holds them exactly, so sixteen more warps of a CTA
 // widen what the copies bring, weights to tensor memory (a lane a row) and rows to shared memory, and the products take A
 // from the one and B from the other.  Weights in tensor memory, because shared memory would be written and read 32 KB a
-// stage more; sums have 384 of its columns then.  A decode reads half the bytes of bf16 weights (16 tokens, top-8 of 128, 7168 -> 2 x 2048:
-// 411 us, 5.9 TB/s, and 665); a prefill is at the same power limit (4096 tokens, top-8 of 32: 1185 us, 1.62 PFLOP/s).  What the
-// steps there measured (decode, prefill; us): 64 x 64 tiles on the CUDA cores 5245, 32670; eight widening warps 919, 1860;
-// sixteen, stages in turn 627, 1220; the multiplying warp waiting for a stage, not for half of one 517, 1230; one store group, so that a thread
-// has 88 registers and not 72, 424, 1190; four pieces in flight, not eight 411, 1185.  The copies alone take 361 and 458, all
-// but the widening 490 and 991.
+// stage more; sums have 384 of its columns then.  A decode reads half the bytes of bf16 weights (16 tokens, top-8 of 128,
+// 7168 -> 2 x 2048: 405 us, 6.0 TB/s, and 714 in the same run); a prefill is at the same power limit (4096 tokens, top-8 of
+// 32: 1180 us, 1.63 PFLOP/s).  What the steps there measured (decode, prefill; us): 64 x 64 tiles on the CUDA cores 5245,
+// 32670; eight widening warps 919, 1860; sixteen, stages in turn 627, 1220; the multiplying warp waiting for a stage, not for
+// half of one 517, 1230; one store group, so that a thread has 88 registers and not 72, 424, 1190; four pieces in flight, not
+// eight 411, 1185.  The copies alone take 361 and 458, all but the widening 388 and 983.
 //
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
 // own copies and products, frees its tensor memory and returns.
@@ -88,7 +88,7 @@ template <int OP>
 constexpr int kGroups = OP == kForward8 ? 1 : OP == kShort8 ? 3 : 4;  // of four warps that store
 template <int OP>
 constexpr int kTailWarp = 2 + 4 * kGroups<OP>;
-template <int OP>                      // warps that widen integers: four for either half of a stage, or twice that, stages in turn
+template <int OP>                      // warps that widen integers: four for either half of a stage, or eight, stages in turn
 constexpr int kWideners = OP == kForward8 ? 16 : 8;
 template <int OP>
 constexpr bool kInTurn = kWideners<OP> > 8;
@@ -320,7 +320,8 @@ __device__ __forceinline__ void store_wide(uint4 w, uint32_t lo, uint32_t hi) {
 // receive rows 8 lanes take a 16-byte part of 8 rows at a time, to rows of 128 bytes in shared memory.  16-byte parts of a
 // row lie swizzled by the row, here and there, so that 8 lanes cover all banks.  The first rows are loaded ahead: with few
 // rows only one warp of the four has any, and the others would wait for its second round of latencies.
-__device__ __forceinline__ void widen(uint32_t stage, int half, int rows, uint32_t weights, uint32_t piece, int quarter, int lane) {
+__device__ __forceinline__ void widen(uint32_t stage, int half, int rows, uint32_t weights, uint32_t piece, int quarter,
+                                      int lane) {
     const int row = quarter * 32 + lane, sub = lane & 7, chunk = lane >> 3;
     const uint32_t from = stage + kBytesA + sub * kRowBytes + (((4 * half + chunk) ^ sub) << 4), to = piece + sub * kRowBytes;
     const uint32_t lo = to + (((2 * chunk) ^ sub) << 4), hi = to + (((2 * chunk + 1) ^ sub) << 4);
@@ -349,12 +350,12 @@ __device__ __forceinline__ void widen(uint32_t stage, int half, int rows, uint32
 
 // ---- pre-activations kept in 8 bits: e4m3 codes, a power of two (E8M0) for 32 columns ----
 //
-// Where a result row is written its 32 columns lie on four neighbouring lanes, so a scale takes two exchanges.  Powers of two, so that
-// the code's rounding is the only one, 32 columns because that is what one CTA's store half has beside each other at any
-// tile, and the least power that saturates nothing: a value is off by half a step however its 32 columns are spread.
-// 4096 tokens, top-8 of 32, 7168 -> 2 x 2048: 1238 us in a long run, 1234 with pre in bf16, 1225 without (half the
-// bytes of pre, but its arithmetic: 281.7 us for 8192 rows, 258.8 without pre).  Back, 2048 <- 7168: 661 us, 659 from bf16, and 681 with
-// the activation made anew, 134 MB (20 us at the copy rate).
+// Where a result row is written its 32 columns lie on four neighbouring lanes, so a scale takes two exchanges.  Powers of
+// two, so that the code's rounding is the only one, 32 columns because that is what one CTA's store half has beside each
+// other at any tile, and the least power that saturates nothing: a value is off by half a step however its 32 columns are
+// spread.  4096 tokens, top-8 of 32, 7168 -> 2 x 2048: 1238 us in a long run, 1234 with pre in bf16, 1225 without (half the
+// bytes of pre, but its arithmetic: 281.7 us for 8192 rows, 258.8 without pre).  Back, 2048 <- 7168: 661 us, 659 from bf16,
+// and 681 with the activation made anew, 134 MB (20 us at the copy rate).
 
 // 8 of 32 columns on each of 4 lanes to codes; returns the scale byte: the least power of two with no value over 448 of
 // it (448 = 1.75 * 2^8, so a mantissa over 1.75 takes the next).  All lanes of the warp call it.
@@ -479,7 +480,8 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
     float scale = 1.0f;
     if constexpr (k8 && !SPLIT) {
         const int of = t.f0 + cta * kMine + tid % kMine;
-        if (of < p.features) scale = __ldg(static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W + of + tid / kMine * a.N);
+        const float* scales = static_cast<const float*>(a.weight_scales) + (int64_t)t.e * a.W;
+        if (of < p.features) scale = __ldg(scales + of + tid / kMine * a.N);
     }
     auto column = [&](int i) { return (up ? i : count - 1 - i) * kTurn; };
     bool told = false;
@@ -502,7 +504,8 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
         }
         store_sync(group);  // the block before has been read
 #pragma unroll
-        for (int i = 0; i < kTurn; ++i) turn[i * kTurnPitch + tid] = k8 && !SPLIT ? __uint_as_float(v[i]) * scale : __uint_as_float(v[i]);
+        for (int i = 0; i < kTurn; ++i)
+            turn[i * kTurnPitch + tid] = k8 && !SPLIT ? __uint_as_float(v[i]) * scale : __uint_as_float(v[i]);
         store_sync(group);
         if (SPLIT) {
             if (tid < link.parts)
@@ -620,7 +623,8 @@ template <int OP, bool GLU, bool SPLIT, bool KEPT>
 __global__ void __launch_bounds__(kThreads<OP>, 1)
 pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ Maps maps) {
-    constexpr bool k4 = OP == kForward4, k8 = kIntegers<OP>, across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
+    constexpr bool k4 = OP == kForward4, k8 = kIntegers<OP>;
+    constexpr bool across_a = OP == kBackRows || OP == kBackWeights, across_b = OP == kBackWeights;
     extern __shared__ uint8_t dynamic[];
     __shared__ Shared sh;
     const uint32_t skip = (1024u - (smem_u32(dynamic) & 1023u)) & 1023u;
@@ -804,10 +808,12 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                         const uint64_t rb = tc::at(tc::kAlongK, pieces + piece * piece_bytes), rb1 = rb + (piece_bytes >> 4);
                         if (end - k0 >= kStep<OP>) {       // without tests between the instructions
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, instr8, k0 > begin || k > 0);
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_tmem_pair(sums, wa + k * 8, rb + k * 2, instr8, k0 > begin || k > 0);
                             tc::commit_pair(used + 8 * piece, both);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tc::mma_tmem_pair(sums, wa + kPieceColumns + k * 8, rb1 + k * 2, instr8, true);
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_tmem_pair(sums, wa + kPieceColumns + k * 8, rb1 + k * 2, instr8, true);
                         } else {
                             const int count = (end - k0) / 16;
                             for (int k = 0; k < min(count, 4); ++k)
@@ -959,7 +965,8 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
                     if (k0 + half * kPiece < end) {
                         tc::fence_after_sync();
                         const uint32_t sa = stages + ring.at;
-                        widen(sa, half, t.n / 2, tmem + kTop<OP> + piece * kPieceColumns, pieces + piece * piece_bytes, quarter, lane);
+                        widen(sa, half, t.n / 2, tmem + kTop<OP> + piece * kPieceColumns, pieces + piece * piece_bytes,
+                              quarter, lane);
                         fence_proxy_async_smem();
                         tc::wait_st();
                         tc::fence_before_sync();
@@ -1176,13 +1183,14 @@ cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
 }
 
 // Few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the widening
-// warps are faster (8 and 40 experts, 130 to 1024 rows: 1024 of contraction takes 0.83 of the time, 1200 0.87, 1424 to 1792 0.95; 32
-// experts of 1024 rows, 512 -> 1024: 82.5 -> 50 us; with two stages in flight for three 3584 -> 2 x 2048 took 703 and not 651; four
-// groups: 0.99 to 1.03 of three).  With few rows the weights are what counts (16 rows, 1024 -> 2048: 21.0 and 24.8 us).
+// warps are faster (8 and 40 experts, 130 to 1024 rows: 1024 of contraction takes 0.83 of the time, 1200 0.87, 1424 to 1792
+// 0.95; 32 experts of 1024 rows, 512 -> 1024: 82.5 -> 50 us; with two stages in flight for three 3584 -> 2 x 2048 took 703
+// and not 651; four groups: 0.99 to 1.03 of three).  With few rows the weights are what counts (16 rows, 1024 -> 2048: 21.0 and 24.8 us).
 // So up to the contraction from which on tiles may be shared, which these never are.
 constexpr int kLeastLong = kLeastShared * kPiece;
 cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s) {
-    if (a.K < kLeastLong && make_cut<kShort8>(a).columns > 128) return a.glu ? launch<kShort8, true>(a, s) : launch<kShort8, false>(a, s);
+    if (a.K < kLeastLong && make_cut<kShort8>(a).columns > 128)
+        return a.glu ? launch<kShort8, true>(a, s) : launch<kShort8, false>(a, s);
     return a.glu ? launch<kForward8, true>(a, s) : launch<kForward8, false>(a, s);
 }
 

@@ -8,10 +8,12 @@ namespace moe {
 
 // Tries until it succeeds, giving up after limit_ns (or somewhat later: the clock
 // is read only once in 1024 tries, because reading it costs more than a stage of a
-// product lasts).
+// product lasts).  The first try stands before the loop and its counter (integer products of few rows: 412 -> 405 us).
 template <typename F>
 __device__ __forceinline__ bool within(uint64_t limit_ns, F attempt) {
+    if (attempt()) return true;
     uint64_t t0 = 0;
+#pragma unroll 1
     for (uint32_t it = 1;; ++it) {
         if (attempt()) return true;
         if ((it & 1023u) == 0u) {

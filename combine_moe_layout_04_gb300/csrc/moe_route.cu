@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
 // Keys are scores, so that a bias moves them on the scale of the scores; they decide, so their value must not hang on an
 // order of additions: the softmax's sum is rounded once (sum_once), all else is one fp32 operation after another.
 //
-// Instructions bound it, as above: 16384 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid and bias, 15.4 us (floor 2.8;
-// moe_route, which needs no score before its choice, 12.6), 128 experts, top-8 of 3 of 8, softmax, 12.0, 512, 4 of 16 groups, 26.1, one
-// token 2.8.  What it cost otherwise: 22 us with the keys of groups that stay left on their own lanes (512 experts: 38), 17.6 with lanes
-// and groups divided on the device, 16.2 with a load for every logit (512: 35).
+// Instructions bound it, as above: 16384 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid and bias, 15.4 us (floor
+// 2.8; moe_route, which needs no score before its choice, 12.6), 128 experts, top-8 of 3 of 8, softmax, 12.0, 512, 4 of 16
+// groups, 26.1, one token 2.8.  What it cost otherwise: 22 us with the keys of groups that stay left on their own lanes (512
+// experts: 38), 17.6 with lanes and groups divided on the device, 16.2 with a load for every logit (512: 35).
 
 // key_of without NaN, which counts as -infinity here, and without -0, which no sum of a score and a bias is.
 __device__ __forceinline__ unsigned short_key_of(float v) {
@@ -243,7 +243,8 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
 // take_largest among the groups that stay, their keys spread over PARTS times as many lanes, those of groups that go: fewer
 // keys a lane to sort and to move.  before: how many groups come before this lane's.
 template <int V, int PARTS>
-__device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&key)[V], int group, int sub, int before, int lane) {
+__device__ __forceinline__ int take_spread(const RouteArgs& a, const unsigned (&key)[V], int group, int sub, int before,
+                                           int lane) {
     constexpr int kFew = V / PARTS;
     __shared__ int with_rank[kRouteThreads / 32][MOE_MAX_ROUTE_GROUPS];
     int* ranked = with_rank[threadIdx.x >> 5];
