@@ -53,7 +53,7 @@
 // scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
 // between the products (333 us then; 32768 rows of 32 experts, 7168 -> 2 x 2048).
 //
-// 8-bit integers.  The tensor core here has no products of them, and fp16 holds them exactly, so sixteen more warps of a CTA
+// 8-bit integers.  The chip multiplies them far slower than fp16, which holds them exactly, so sixteen more warps of a CTA
 // widen what the copies bring, weights to tensor memory (a lane a row) and rows to shared memory, and the products take A
 // from the one and B from the other.  Weights in tensor memory, because shared memory would be written and read 32 KB a
 // stage more; sums have 384 of its columns then.  A decode reads half the bytes of bf16 weights (16 tokens, top-8 of 128,
