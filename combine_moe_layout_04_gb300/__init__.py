@@ -595,11 +595,28 @@ def moe_route(problem: Problem, routing: Routing, logits, ids, gates, bias=None,
         _take(where, gates, "float32", p.num_tokens, p.topk), _stream(stream)), where)
 
 
+class _ChoiceStructs(dict):
+    """References to the C structs of a routing and a grouping by their values (1 us of host time a call less than
+    making them; the library only reads them, and nobody else gets hold of them)."""
+
+    def __missing__(self, key):
+        made = ctypes.byref(_RoutingC(key[0], bool(key[1]), key[2], key[3])), ctypes.byref(_GroupingC(*key[4:], 0))
+        if len(self) >= 64:
+            self.clear()
+        self[key] = made
+        return made
+
+
+_CHOICE = _ChoiceStructs()
+
+
 def moe_route_groups(problem: Problem, routing: Routing, grouping: Grouping, logits, ids, gates, bias=None, stream=None):
     """moe_route with every token's choice limited to `grouping.kept` groups of experts; keys are scores (+ bias)."""
     p, where = problem, "moe_route_groups"
+    kind = MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32
+    choice = _CHOICE[routing.score, routing.renormalise, routing.scale, kind, grouping.groups, grouping.kept, grouping.top]
     _check((_lib or load_library()).moe_route_groups(
-        ctypes.byref(p.c()), ctypes.byref(routing.c(logits)), ctypes.byref(grouping.c()),
+        ctypes.byref(p.c()), *choice,
         _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
         _take(where, bias, "float32", p.num_experts), _take(where, ids, "int32", p.num_tokens, p.topk),
         _take(where, gates, "float32", p.num_tokens, p.topk), _stream(stream)), where)

@@ -59,6 +59,25 @@ def test_route_groups_refusals(moe):
     moe.moe_route_groups(_p(moe, num_tokens=0), r, good, None, None, None, stream=0)
 
 
+def test_choice_structs_follow_their_values(moe):
+    """The structs of a routing and a grouping are kept by value: changed fields give others, and the store stays small."""
+    r, g = moe.Routing(scale=1.5), moe.Grouping(4, 2)
+    moe._CHOICE.clear()
+    p = _p(moe, num_tokens=0)
+    moe.moe_route_groups(p, r, g, None, None, None, stream=0)
+    (key, (rc, gc)), = moe._CHOICE.items()
+    assert bytes(rc._obj) == bytes(r.c(None)) and bytes(gc._obj) == bytes(g.c())
+    r.score, g.kept = moe.MOE_SCORE_SIGMOID, 3
+    moe.moe_route_groups(p, r, g, None, None, None, stream=0)
+    assert len(moe._CHOICE) == 2
+    r.score, g.top = 7, 2                                              # refused each time, also from the store
+    for _ in range(2):
+        _refused(moe, moe.MOE_ERR_INVALID, moe.moe_route_groups, _p(moe), r, g, GOOD, GOOD, GOOD)
+    for i in range(200):
+        moe.moe_route_groups(p, moe.Routing(scale=float(i)), moe.Grouping(4, 2), None, None, None, stream=0)
+    assert len(moe._CHOICE) <= 64
+
+
 def _tensors_refused(moe, tensors, call):
     """Every tensor in turn on the host, on another GPU, of another type, with gaps or of another shape."""
     import torch
