@@ -190,9 +190,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
 // order of additions: the softmax's sum is rounded once (sum_once), all else is one fp32 operation after another.
 //
 // Instructions bound it, as above: 16384 tokens of 256 experts, top-8 of 4 of 8 groups, sigmoid and bias, 15.4 us (floor
-// 2.8; moe_route, which needs no score before its choice, 12.6), 128 experts, top-8 of 3 of 8, softmax, 12.0, 512, 4 of 16
-// groups, 26.1, one token 2.8.  What it cost otherwise: 22 us with the keys of groups that stay left on their own lanes (512
-// experts: 38), 17.6 with lanes and groups divided on the device, 16.2 with a load for every logit (512: 35).
+// 2.8; moe_route, which needs no score before its choice, 12.6), 128 experts, top-8 of 3 of 8, softmax, 12.0, 160 experts 15.2,
+// 512, 4 of 16 groups, 26.1, one token 2.8.  What it cost otherwise: 22 us with the keys of groups that stay left on their own lanes (512
+// experts: 38), 17.6 with lanes and groups divided on the device, 16.2 with a load for every logit (512: 35), 19.7 for 160 experts with
+// eight values a lane for five.
 
 // key_of without NaN, which counts as -infinity here, and without -0, which no sum of a score and a bias is.
 __device__ __forceinline__ unsigned short_key_of(float v) {
@@ -224,11 +225,11 @@ __device__ __forceinline__ float sum_once(const float (&v)[V]) {
     return s + err;
 }
 
-// Which expert of its group is value j of a lane: four neighbours a lane in turn, so that they come in one load, or, with
-// less than four values a lane, one.
+// Which expert of its group is value j of a lane: four neighbours a lane in turn, so that they come in one load, or, where
+// the values are no fours, one.
 template <int V>
 __device__ __forceinline__ int place(int j, int bits, int sub) {
-    return V >= 4 ? ((j >> 2) << (bits + 2)) + (sub << 2) + (j & 3) : (j << bits) + sub;
+    return V % 4 == 0 ? ((j >> 2) << (bits + 2)) + (sub << 2) + (j & 3) : (j << bits) + sub;
 }
 __device__ __forceinline__ void load4(const float* p, float* v) {
     const float4 x = *reinterpret_cast<const float4*>(p);
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
         l[i] = -INFINITY;
         bias[i] = 0.0f;
     }
-    if (V >= 4 && a.fours) {
+    if (V % 4 == 0 && a.fours) {
 #pragma unroll
         for (int i = 0; i + 3 < V; i += 4) {
             if ((int)id[i] >= a.E) continue;
@@ -342,8 +343,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_groups_kernel(RouteArgs a
 #pragma unroll 4
     for (int g = 0; g < a.groups; ++g) before += __shfl_sync(kFull, mine, g << a.bits) + (g < group) > mine;
     int chosen;
-    if (V >= 4 && 4 * a.kept <= a.groups) {
-        chosen = take_spread<V, V >= 4 ? 4 : 1>(a, key, group, sub, before, lane);
+    if (V % 4 == 0 && 4 * a.kept <= a.groups) {
+        chosen = take_spread<V, V % 4 == 0 ? 4 : 1>(a, key, group, sub, before, lane);
     } else if (V >= 2 && 2 * a.kept <= a.groups) {
         chosen = take_spread<V, V >= 2 ? 2 : 1>(a, key, group, sub, before, lane);
     } else {
@@ -445,12 +446,13 @@ cudaError_t launch_grouped(const RouteArgs& a, cudaStream_t s) {
 // By the experts of a lane: those of a group over its lanes (up to 60, where a group has one lane).
 template <typename T>
 cudaError_t pick_grouped(const RouteArgs& a, cudaStream_t s) {
-    int each = (a.size + (1 << a.bits) - 1) >> a.bits;
-    if (each > 2) each = (a.size + (4 << a.bits) - 1) / (4 << a.bits) * 4;  // in fours
-    if (each <= 1) return launch_grouped<T, 1>(a, s);
-    if (each <= 2) return launch_grouped<T, 2>(a, s);
+    const int ones = (a.size + (1 << a.bits) - 1) >> a.bits, each = (a.size + (4 << a.bits) - 1) / (4 << a.bits) * 4;
+    if (ones <= 1) return launch_grouped<T, 1>(a, s);
+    if (ones <= 2) return launch_grouped<T, 2>(a, s);
     if (each <= 4) return launch_grouped<T, 4>(a, s);
+    if (ones == 5 || ones == 6) return launch_grouped<T, 6>(a, s);  // (in fours they would be eight)
     if (each <= 8) return launch_grouped<T, 8>(a, s);
+    if (each <= 12) return launch_grouped<T, 12>(a, s);
     if (each <= 16) return launch_grouped<T, 16>(a, s);
     if (each <= 32) return launch_grouped<T, 32>(a, s);
     return launch_grouped<T, 64>(a, s);

@@ -120,7 +120,7 @@ def _check(moe, logits, bias, G, kept, top, k, score, renorm=True, scale=1.0, ex
 CASES = [  # T, E, G, kept, k
     (1, 256, 8, 4, 8), (1, 1, 1, 1, 1), (5, 2, 2, 1, 1), (130, 60, 5, 2, 3), (67, 32, 32, 32, 32), (33, 64, 32, 3, 6),
     (500, 160, 8, 3, 6), (1025, 128, 4, 1, 8), (259, 384, 8, 4, 8), (77, 192, 6, 5, 4), (19, 1000, 20, 7, 32),
-    (9, 1023, 31, 2, 17), (21, 1023, 11, 4, 9), (5, 1024, 1, 1, 16), (300, 512, 16, 4, 8), (40, 96, 3, 1, 32)]
+    (9, 1023, 31, 2, 17), (31, 192, 8, 2, 8), (45, 176, 8, 8, 9), (60, 384, 8, 2, 6), (12, 768, 16, 3, 8), (21, 1023, 11, 4, 9), (5, 1024, 1, 1, 16), (300, 512, 16, 4, 8), (40, 96, 3, 1, 32)]
 
 
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
