@@ -1116,30 +1116,38 @@ cudaError_t start(K* kern, const ExpertArgs& a, const Cut& cut, int64_t tiles, i
     return cudaLaunchKernelEx(&cfg, kern, a, cut, ma, mb);
 }
 
-template <int OP, bool GLU, bool KEPT = false>
-cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
-    CUtensorMap ma;
-    Maps mb{};
+template <int OP, bool GLU>
+bool make_maps(const ExpertArgs& a, CUtensorMap* ma, Maps* mb) {
     bool ok;
     if (OP == kBackWeights) {
-        ok = tc::make_map(&ma, a.dout, false, a.W, a.R, 0, 64) && tc::make_map(&mb.rows[0], a.rows, false, a.K, a.R, 0, 64) &&
-             tc::make_map(&mb.out, a.out, false, a.K, a.W, a.E, kHalf, 64);
+        ok = tc::make_map(ma, a.dout, false, a.W, a.R, 0, 64) && tc::make_map(&mb->rows[0], a.rows, false, a.K, a.R, 0, 64) &&
+             tc::make_map(&mb->out, a.out, false, a.K, a.W, a.E, kHalf, 64);
     } else if (OP == kForward4) {
         const int64_t groups = (a.K + 127) / 128, per = GLU ? 64 : 128;
-        ok = tc::make_map(&ma, a.weights, true, a.K / 2, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64) &&
-             tc::make_scale_map(&mb.weight_scales, a.weight_scales, a.E * ((a.N + per - 1) / per) * groups) &&
-             tc::make_scale_map(&mb.row_scales, a.row_scales, (a.R / 128 + a.E) * groups);
-        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K / 2, a.R, 0, 8 << i);
+        ok = tc::make_map(ma, a.weights, true, a.K / 2, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64) &&
+             tc::make_scale_map(&mb->weight_scales, a.weight_scales, a.E * ((a.N + per - 1) / per) * groups) &&
+             tc::make_scale_map(&mb->row_scales, a.row_scales, (a.R / 128 + a.E) * groups);
+        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb->rows[i], a.rows, true, a.K / 2, a.R, 0, 8 << i);
     } else if (kIntegers<OP>) {
-        ok = tc::make_map(&ma, a.weights, true, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
-        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb.rows[i], a.rows, true, a.K, a.R, 0, 8 << i);
+        ok = tc::make_map(ma, a.weights, true, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
+        for (int i = 0; i < kMaps; ++i) ok = ok && tc::make_map(&mb->rows[i], a.rows, true, a.K, a.R, 0, 8 << i);
     } else {
-        ok = tc::make_map(&ma, a.weights, false, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
+        ok = tc::make_map(ma, a.weights, false, a.K, a.W, a.E, kOneBox<OP, GLU> ? kHalf : 64);
         for (int i = 0; i < kMaps; ++i)
-            ok = ok && tc::make_map(&mb.rows[i], OP == kForward ? a.rows : a.dout, false, OP == kForward ? a.K : a.W, a.R,
+            ok = ok && tc::make_map(&mb->rows[i], OP == kForward ? a.rows : a.dout, false, OP == kForward ? a.K : a.W, a.R,
                                     0, 8 << i);
     }
-    if (!ok) return cudaErrorInvalidValue;
+    return ok;
+}
+
+// Integers, few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the
+// widening warps are faster (130 to 1024 rows of 8 and 32 or 40 experts: 1024 of contraction takes 0.83 of the time, 1424 0.92,
+// 2048 0.93, 2816 0.99, 3584 1.02, 7168 1.04; 32 experts of 1024 rows, 512 -> 1024: 82.5 -> 50 us; four groups take 0.99 to
+// 1.04 of three).  With few rows the weights are what counts (16 rows, 1024 -> 2048: 21.0 and 24.8 us).
+constexpr int kLeastLong = 3200;
+
+template <int OP, bool GLU, bool KEPT = false>
+cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     Cut cut = make_cut<OP>(a);
     // no more pairs than there can be tiles
     const int64_t features = OP == kBackWeights ? a.W : OP == kBackRows ? a.K : a.N, wide = GLU ? kHalf : 2 * kHalf;
@@ -1147,21 +1155,26 @@ cudaError_t launch(const ExpertArgs& a, cudaStream_t s) {
     const int64_t tiles = across * (OP == kBackWeights ? (int64_t)a.E * ((a.K + kColumns - 1) / kColumns)
                                                        : a.R / cut.columns + (int64_t)(a.E < a.R ? a.E : a.R));
     const int64_t pairs = device_sm_count() / 2;
-    auto* whole = pair_kernel<OP, GLU, false, KEPT>;
-    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(whole), kSmem<OP>);
-    if (e != cudaSuccess) return e;
+    int64_t teams = pairs;
+    auto* kern = pair_kernel<OP, GLU, false, KEPT>;
     if constexpr (OP != kBackWeights && OP != kShort8) {
         auto* split = pair_kernel<OP, GLU, true, KEPT>;
-        e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
+        const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(split), kSmem<OP>);
         if (e != cudaSuccess) return e;
         // (a stage of integers is two pieces, each a stage's worth of products)
         constexpr int kWork = kIntegers<OP> ? kPiece : kStep<OP>;
         const int steps = ((OP == kBackRows ? a.W : a.K) + kWork - 1) / kWork;
-        int64_t teams = pairs;
         cut.parts = parts_of(reinterpret_cast<const void*>(split), kThreads<OP>, kSmem<OP>, tiles, steps, pairs, &teams);
-        if (cut.parts > 1) return start<OP>(split, a, cut, tiles, teams, ma, mb, s);
+        if (cut.parts > 1) kern = split;
     }
-    return start<OP>(whole, a, cut, tiles, pairs, ma, mb, s);
+    if constexpr (OP == kForward8)
+        if (cut.parts == 1 && a.K < kLeastLong && cut.columns > 128) return launch<kShort8, GLU>(a, s);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmem<OP>);
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma;
+    Maps mb{};
+    if (!make_maps<OP, GLU>(a, &ma, &mb)) return cudaErrorInvalidValue;
+    return start<OP>(kern, a, cut, tiles, teams, ma, mb, s);
 }
 
 }  // namespace
@@ -1182,15 +1195,7 @@ cudaError_t launch_expert_forward4(const ExpertArgs& a, cudaStream_t s) {
     return a.glu ? launch<kForward4, true>(a, s) : launch<kForward4, false>(a, s);
 }
 
-// Few stages a tile and many columns: the store half is what a tile takes, and three groups of it with half the widening
-// warps are faster (8 and 40 experts, 130 to 1024 rows: 1024 of contraction takes 0.83 of the time, 1200 0.87, 1424 to 1792
-// 0.95; 32 experts of 1024 rows, 512 -> 1024: 82.5 -> 50 us; with two stages in flight for three 3584 -> 2 x 2048 took 703
-// and not 651; four groups: 0.99 to 1.03 of three).  With few rows the weights are what counts (16 rows, 1024 -> 2048: 21.0 and 24.8 us).
-// So up to the contraction from which on tiles may be shared, which these never are.
-constexpr int kLeastLong = kLeastShared * kPiece;
 cudaError_t launch_expert_forward8(const ExpertArgs& a, cudaStream_t s) {
-    if (a.K < kLeastLong && make_cut<kShort8>(a).columns > 128)
-        return a.glu ? launch<kShort8, true>(a, s) : launch<kShort8, false>(a, s);
     return a.glu ? launch<kForward8, true>(a, s) : launch<kForward8, false>(a, s);
 }
 
