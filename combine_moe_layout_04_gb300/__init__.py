@@ -596,14 +596,25 @@ def moe_route(problem: Problem, routing: Routing, logits, ids, gates, bias=None,
 
 
 class _ChoiceStructs(dict):
-    """References to the C structs of a routing and a grouping by their values (1 us of host time a call less than
-    making them; the library only reads them, and nobody else gets hold of them)."""
+    """References to the C structs of a routing and a grouping by their values (0.3 us of host time a call less than
+    making them; the library only reads them, and nobody else gets hold of them).  Values of Python's own types alone
+    are a key: a tensor or an array can change in place.  Neither is a scale of zero, which hides its sign."""
+    TYPES = (int, bool, float, int, int, int, int)
 
-    def __missing__(self, key):
-        made = ctypes.byref(_RoutingC(key[0], bool(key[1]), key[2], key[3])), ctypes.byref(_GroupingC(*key[4:], 0))
-        if len(self) >= 64:
-            self.clear()
-        self[key] = made
+    def of(self, *values):
+        return self[values] if tuple(map(type, values)) == self.TYPES else self.made(values)
+
+    @staticmethod
+    def made(values):
+        return (ctypes.byref(_RoutingC(values[0], bool(values[1]), values[2], values[3])),
+                ctypes.byref(_GroupingC(*values[4:], 0)))
+
+    def __missing__(self, values):
+        made = self.made(values)
+        if values[2] != 0:
+            if len(self) >= 64:
+                self.clear()
+            self[values] = made
         return made
 
 
@@ -614,7 +625,7 @@ def moe_route_groups(problem: Problem, routing: Routing, grouping: Grouping, log
     """moe_route with every token's choice limited to `grouping.kept` groups of experts; keys are scores (+ bias)."""
     p, where = problem, "moe_route_groups"
     kind = MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32
-    choice = _CHOICE[routing.score, routing.renormalise, routing.scale, kind, grouping.groups, grouping.kept, grouping.top]
+    choice = _CHOICE.of(routing.score, routing.renormalise, routing.scale, kind, grouping.groups, grouping.kept, grouping.top)
     _check((_lib or load_library()).moe_route_groups(
         ctypes.byref(p.c()), *choice,
         _take(where, logits, "float32|bfloat16", p.num_tokens, p.num_experts),
