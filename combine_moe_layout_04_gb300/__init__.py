@@ -314,12 +314,14 @@ class Problem:
         now = _PROBLEM_FIELDS(self)
         if now[8] is None and now[9] is None and now[10] is None:
             # a struct of sizes alone is kept with the fields it was made from and what it then held: it serves again
-            # while the fields are the same, whoever set them, and nobody has edited it
+            # while the fields are the same, whoever set them, and nobody has edited it; fields that can change in place
+            # (a count held in a tensor) would stay the same to a comparison, so then nothing is kept
             kept = self.__dict__.get("_kept")
             if kept is not None and kept[0] == now and bytes(kept[1]) == kept[2]:
                 return kept[1]
             pc = _ProblemC(*now)
-            self.__dict__["_kept"] = (now, pc, bytes(pc))
+            if all(type(value) is int for value in now[:8]):
+                self.__dict__["_kept"] = (now, pc, bytes(pc))
             return pc
         # the struct keeps its tuning alive for as long as it is referenced
         pc = _ProblemC(*now[:8], _ptr(now[8]), _ptr(now[9]), None)
