@@ -426,13 +426,13 @@ class Experts:
 
 
 class _Kinds(dict):
-    """The torch types of names joined by "|", looked up once."""
+    """The torch types of names joined by "|" (of those that this torch has), looked up once."""
 
     def __missing__(self, kinds: str):
         import torch
         if _raw_stream is None:
             _look_up()
-        found = self[kinds] = tuple(getattr(torch, n) for n in kinds.split("|"))
+        found = self[kinds] = tuple(getattr(torch, n) for n in kinds.split("|") if hasattr(torch, n))
         return found
 
 
@@ -442,12 +442,11 @@ _KINDS = _Kinds()
 def _take(where: str, t, kinds: str, *shape):
     """Address of a tensor argument that has to be dense, on the current GPU, of
     one of these types and (where given) of this shape."""
-    try:
-        if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous() and (
-                t.is_cuda if _one_gpu else _on_current_gpu(t)):
-            return t.data_ptr()
-    except AttributeError:  # NULL, or an object with nothing but an address
+    if getattr(t, "dtype", None) is None:  # NULL, or an object with nothing but an address
         return None if t is None else t.data_ptr()
+    if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous() and (
+            t.is_cuda if _one_gpu else _on_current_gpu(t)):
+        return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {kinds} tensor {list(shape) or ''} on the current GPU is wanted, not "
                                     f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
 
