@@ -660,11 +660,10 @@ def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy,
 
 def _take_ints(where: str, t, name: str, size: int):
     """Address of a layout's array: dense int32 on the current GPU, `size` long at least."""
-    try:
-        if t.numel() >= size and t.dtype is _KINDS["int32"][0] and t.is_contiguous() and (
-                t.is_cuda if _one_gpu else _on_current_gpu(t)):
-            return t.data_ptr()
-    except AttributeError:  # an object with nothing but an address
+    if getattr(t, "dtype", None) is None:  # an object with nothing but an address
+        return t.data_ptr()
+    if t.numel() >= size and t.dtype is _KINDS["int32"][0] and t.is_contiguous() and (
+            t.is_cuda if _one_gpu else _on_current_gpu(t)):
         return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID, f"{where}: the layout's {name} has to be dense int32 on the current GPU, {size} values "
                                     f"or more, not {t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")

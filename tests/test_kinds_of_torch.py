@@ -43,3 +43,16 @@ def test_a_failing_check_is_not_an_address(moe, first_gpu, monkeypatch):
     monkeypatch.setattr(moe, "_get_device", lost)
     with pytest.raises(AttributeError):
         moe.moe_quant8_rows(_p(moe, num_tokens=0), On(torch.bfloat16, 0, 64), On(torch.int8, 0, 64), On(torch.float32, 0), stream=0)
+
+
+def test_a_failing_check_is_not_an_array_of_the_layout(moe, first_gpu, monkeypatch):
+    import torch
+
+    def lost():
+        raise AttributeError("no such thing")
+    monkeypatch.setattr(moe, "_get_device", lost)
+    for lay in (_lay(moe, expert_count=On(torch.int32, 16)), _lay(moe, expert_offset=On(torch.int32, 17))):
+        with pytest.raises(AttributeError):
+            moe.moe_expert_forward(_p(moe, num_tokens=0), lay, moe.Experts(64, 64), None, None, stream=0)
+    with pytest.raises(AttributeError):
+        moe.moe_combine_backward(_p(moe, num_tokens=0), _lay(moe, pos=On(torch.int32, 0)), None, None, None, None, None, stream=0)
