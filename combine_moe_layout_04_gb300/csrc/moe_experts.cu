@@ -1030,6 +1030,29 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     if (warp == 1) tc::dealloc_pair(tmem, 512);
 }
 
+// Tiles of this many columns: as many stages as the ring holds, beside the pieces of widened integers.
+template <int OP>
+constexpr int pieces_bytes(int columns) { return kIntegers<OP> ? kPieces * columns / 2 * kRowBytes : 0; }
+template <int OP>
+constexpr Cut cut_at(int columns) {
+    Cut cut{columns, 0, 0, 1};
+    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
+    const int ring = kRingBytes<OP> - pieces_bytes<OP>(columns);
+    cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
+    if (kIntegers<OP> && kInTurn<OP>) cut.stages &= ~1;  // (see the widening warps)
+    return cut;
+}
+// Two stages at least, an even number of them where groups take them in turn, and all of it inside the ring.
+template <int OP>
+constexpr bool holds(int columns) {
+    const Cut cut = cut_at<OP>(columns);
+    return cut.stages >= 2 && !(kInTurn<OP> && cut.stages % 2) && cut.stages * cut.bytes + pieces_bytes<OP>(columns) <= kRingBytes<OP>;
+}
+static_assert(holds<kForward>(64) && holds<kForward>(128) && holds<kForward>(256) && holds<kForward>(320) && holds<kForward>(384));
+static_assert(holds<kBackRows>(64) && holds<kBackRows>(128) && holds<kBackRows>(256) && holds<kBackRows>(320) && holds<kBackRows>(384));
+static_assert(holds<kForward4>(64) && holds<kForward4>(128) && holds<kForward4>(256) && holds<kForward4>(384));
+static_assert(holds<kForward8>(128) && holds<kForward8>(256) && holds<kShort8>(256) && holds<kBackWeights>(kColumns));
+
 // The cut of a launch, from the mean rows of an expert (all the host knows of them); routing spreads an expert's rows by
 // about the square root of their mean, and 3.5 of that hold almost all experts.  The bounds above 256 rows were each timed
 // on both sides for three to four widths, 8 and 32 experts, even routing and one whose experts' shares fall as rank^-0.4 (in brackets).
@@ -1059,17 +1082,13 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
 template <int OP>
 Cut make_cut(const ExpertArgs& a) {
     const double mean = (double)a.R / a.E, most = mean + 3.5 * std::sqrt(mean);
-    Cut cut{kColumns, 0, 0, 1};
+    int columns = kColumns;
     if (OP != kBackWeights) {
-        cut.columns = most <= 64 && !kIntegers<OP> ? 64 : most <= 128 ? 128 : 256;
-        if (OP != kForward4 && !kIntegers<OP> && most > 256 && mean < 900) cut.columns = mean > 310 && mean <= 365 ? 384 : 320;
-        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) cut.columns = 384;
+        columns = most <= 64 && !kIntegers<OP> ? 64 : most <= 128 ? 128 : 256;
+        if (OP != kForward4 && !kIntegers<OP> && most > 256 && mean < 900) columns = mean > 310 && mean <= 365 ? 384 : 320;
+        if (OP == kForward4 && most > 256 && (mean <= 365 || (mean > 768 && mean <= 1152))) columns = 384;
     }
-    cut.bytes = kBytesA + cut.columns / 2 * kRowBytes + (OP == kForward4 ? scale_bytes(cut.columns) : 0);
-    const int ring = kRingBytes<OP> - (kIntegers<OP> ? kPieces * cut.columns / 2 * kRowBytes : 0);
-    cut.stages = ring / cut.bytes < kStages ? ring / cut.bytes : kStages;
-    if (kIntegers<OP> && kInTurn<OP>) cut.stages &= ~1;  // (see the widening warps)
-    return cut;
+    return cut_at<OP>(columns);
 }
 
 // Pairs that share a tile: the fewest rounds of tiles times stages of a round.  Sharing costs a round about as long as 14
