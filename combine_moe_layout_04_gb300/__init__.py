@@ -443,9 +443,10 @@ _KINDS = _Kinds()
 def _take(where: str, t, kinds: str, *shape):
     """Address of a tensor argument that has to be dense, on the current GPU, of
     one of these types and (where given) of this shape."""
-    if getattr(t, "dtype", None) is None:  # NULL, or an object with nothing but an address
+    kind = getattr(t, "dtype", None)
+    if kind is None:  # NULL, or an object with nothing but an address
         return None if t is None else t.data_ptr()
-    if t.dtype in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous() and (
+    if kind in _KINDS[kinds] and (t.shape == shape or not shape) and t.is_contiguous() and (
             t.is_cuda if _one_gpu else _on_current_gpu(t)):
         return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID, f"{where}: a dense {kinds} tensor {list(shape) or ''} on the current GPU is wanted, not "
@@ -663,9 +664,10 @@ def moe_combine_backward(problem: Problem, layout: Layout, dout, y, weights, dy,
 
 def _take_ints(where: str, t, name: str, size: int):
     """Address of a layout's array: dense int32 on the current GPU, `size` long at least."""
-    if getattr(t, "dtype", None) is None:  # an object with nothing but an address
+    kind = getattr(t, "dtype", None)
+    if kind is None:  # an object with nothing but an address
         return t.data_ptr()
-    if t.numel() >= size and t.dtype is _KINDS["int32"][0] and t.is_contiguous() and (
+    if t.numel() >= size and kind is _KINDS["int32"][0] and t.is_contiguous() and (
             t.is_cuda if _one_gpu else _on_current_gpu(t)):
         return t.data_ptr()
     raise MoeError(MOE_ERR_INVALID, f"{where}: the layout's {name} has to be dense int32 on the current GPU, {size} values "
