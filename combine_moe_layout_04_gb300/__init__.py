@@ -71,8 +71,9 @@ EXPORTED = ("moe_workspace_bytes", "moe_layout", "moe_stats_words", "moe_stats",
             "moe_relay_layout", "moe_dispatch_relay", "moe_combine_relay",
             "moe_expert_groups", "moe_dispatch_group", "moe_combine_group",
             "moe_route", "moe_route_groups", "moe_route_backward", "moe_expert_forward", "moe_expert_backward_rows",
-            "moe_expert_backward_weights", "moe_expert_forward_kept", "moe_expert_backward_kept", "moe_combine_backward", "moe_quant4_row_scale_bytes",
-            "moe_quant4_weight_scale_bytes", "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4",
+            "moe_expert_backward_weights", "moe_expert_forward_kept", "moe_expert_backward_kept",
+            "moe_combine_backward", "moe_quant4_row_scale_bytes", "moe_quant4_weight_scale_bytes",
+            "moe_quant4_rows", "moe_quant4_weights", "moe_expert_forward4",
             "moe_quant8_rows", "moe_quant8_weights", "moe_expert_forward8")
 
 
@@ -410,8 +411,8 @@ class Grouping:
 class Experts:
     """The experts of a layer (moe_experts in include/moe_layout.h): weights
     bf16 [E, W, in_cols], 4-bit codes [E, W, in_cols / 2] with their scale
-    blocks, or int8 [E, W, in_cols] with fp32 scales [E, W]; W = out_cols, or 2 * out_cols (gate rows, then up rows) with
-    MOE_ACT_SWIGLU."""
+    blocks, or int8 [E, W, in_cols] with fp32 scales [E, W]; W = out_cols, or
+    2 * out_cols (gate rows, then up rows) with MOE_ACT_SWIGLU."""
     in_cols: int
     out_cols: int
     weights: object = None

@@ -53,14 +53,15 @@
 // scales to tensor memory one stage early, by the same warp (406 us) or by one of its own (368 us), measured slower than
 // between the products (333 us then; 32768 rows of 32 experts, 7168 -> 2 x 2048).
 //
-// 8-bit integers.  The chip multiplies them far slower than fp16, which holds them exactly, so sixteen more warps of a CTA
-// widen what the copies bring, weights to tensor memory (a lane a row) and rows to shared memory, and the products take A
-// from the one and B from the other.  Weights in tensor memory, because shared memory would be written and read 32 KB a
+// 8-bit integers.  The chip multiplies them far slower than fp16, which holds them exactly, so other warps of a CTA widen
+// what the copies bring, weights to tensor memory (a lane a row) and rows to shared memory, and the products take A
+// from the one and B from the other.  Beside the copying and the multiplying warp a CTA has one group of four that store and
+// sixteen that widen, twenty-two warps; where a contraction is short and tiles are wide, three groups and eight, also twenty-two.  Weights in tensor memory, because shared memory would be written and read 32 KB a
 // stage more; sums have 384 of its columns then.  A decode reads half the bytes of bf16 weights (16 tokens, top-8 of 128,
 // 7168 -> 2 x 2048: 405 us, 6.0 TB/s, and 714 in the same run); a prefill is at the same power limit (4096 tokens, top-8 of
 // 32: 1180 us, 1.63 PFLOP/s).  What the steps there measured (decode, prefill; us): 64 x 64 tiles on the CUDA cores 5245,
 // 32670; eight widening warps 919, 1860; sixteen, stages in turn 627, 1220; the multiplying warp waiting for a stage, not for
-// half of one 517, 1230; one store group, so that a thread has 88 registers and not 72, 424, 1190; four pieces in flight, not
+// half of one 517, 1230; one store group, so that a thread has 80 registers and not 72, 424, 1190; four pieces in flight, not
 // eight 411, 1185.  The copies alone take 361 and 458, all but the widening 388 and 983.
 //
 // Every wait is bounded.  A CTA whose wait gives up records a fault, waits for its
@@ -301,7 +302,8 @@ __device__ __forceinline__ void scale8(float (&v)[8], float row, const float* we
 
 // ---- 8-bit integers to fp16 ------------------------------------------------------
 
-// 4 integers to 4 fp16: a byte under the exponent of 1024 counts in ones, so the integer is that less 1024 + 128.
+// 4 integers to 4 fp16: a byte under the exponent of 1024 counts in ones, so the integer is that less 1024 + 128 (the method
+// of Kim, Henry, Fahim and Hassan Awadalla, "Who Says Elephants Can't Run", 2022, here with signed bytes in order).
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
     const uint32_t u = w ^ 0x80808080u;
     const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
@@ -536,13 +538,13 @@ __device__ __forceinline__ void store_tile(const ExpertArgs& a, const Plan& p, c
                         turned8(from + kHalf / 2, swap, u);
                     }
                 }
-                uint2 gate, up;
-                const uint32_t gate_scale = keep8(x, &gate), up_scale = keep8(u, &up);
+                uint2 gate8, up8;
+                const uint32_t gate_scale = keep8(x, &gate8), up_scale = keep8(u, &up8);
                 if (!mine) continue;
                 const int64_t r = r0 + c + row;
                 uint8_t* codes = static_cast<uint8_t*>(a.kept) + r * a.W + f;
-                *reinterpret_cast<uint2*>(codes) = gate;
-                *reinterpret_cast<uint2*>(codes + a.N) = up;
+                *reinterpret_cast<uint2*>(codes) = gate8;
+                *reinterpret_cast<uint2*>(codes + a.N) = up8;
                 if ((tid & 3) == 0) {
                     uint8_t* scales = static_cast<uint8_t*>(a.kept_scales) + r * 2 * groups + (f >> 5);
                     scales[0] = (uint8_t)gate_scale;

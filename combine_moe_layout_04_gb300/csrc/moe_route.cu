@@ -205,8 +205,9 @@ __device__ __forceinline__ float value_of(unsigned key) {
     return key == kTaken ? -INFINITY : __uint_as_float(key ^ (~(unsigned)((int)key >> 31) | 0x80000000u));
 }
 
-// Sum of one value a lane and V each, rounded once: every addition's error is kept and added at the end.  Keys are made
-// of it, and with the bias they must not depend on an order of additions.
+// Sum of one value a lane and V each, rounded once: every addition's error (exact by Knuth's sum of two floats, "Seminumerical
+// Algorithms", 4.2.2) is kept and added at the end.  Keys are made of it, and with the bias they must not
+// depend on an order of additions.
 template <int V>
 __device__ __forceinline__ float sum_once(const float (&v)[V]) {
     float s = 0.0f, err = 0.0f;

@@ -508,8 +508,9 @@ typedef struct moe_grouping {
  *     -infinity.
  * The kept groups are those with the largest values, equal values by the lower
  * index.  ids[t] = the k experts of kept groups with the largest key, in falling
- * order, equal keys by the lower index: in range and distinct whatever the logits.  gates, arguments and types as for moe_route; moe_route_backward takes
- * the ids as they are (the choice itself has no gradient). */
+ * order, equal keys by the lower index: in range and distinct whatever the logits.
+ * gates, arguments and types as for moe_route; moe_route_backward takes the ids as
+ * they are (the choice itself has no gradient). */
 int moe_route_groups(const moe_problem* problem, const moe_routing* routing, const moe_grouping* grouping,
                      const void* logits, const float* bias, int32_t* ids, float* gates, moe_stream_t stream);
 
@@ -537,12 +538,13 @@ int moe_route_backward(const moe_problem* problem, const moe_routing* routing, c
  *   act: MOE_ACT_NONE, or MOE_ACT_SWIGLU: the weights hold a gate half and an
  *     up half, and a result is silu(gate) * up, silu(g) = g / (1 + exp(-g));
  *   weights: bf16 [E, W, in_cols] (codes [E, W, in_cols / 2] for the 4-bit
- *     calls), W = out_cols or, with MOE_ACT_SWIGLU, 2 * out_cols: first the
- *     gate rows, then the up rows;
- *   scales: the 4-bit weights' scale blocks, else NULL.
+ *     forward, int8 [E, W, in_cols] for the integers'), W = out_cols or, with
+ *     MOE_ACT_SWIGLU, 2 * out_cols: first the gate rows, then the up rows;
+ *   scales: the 4-bit weights' scale blocks, or the integers' fp32 [E, W]; not
+ *     read by any other call.
  * in_cols and out_cols: multiples of 8 in [8, 2^20]; in_cols a multiple of 32
- * for the 4-bit calls.  E * W < 2^31; T*k <= MOE_MAX_EXPERT_ROWS, in these calls
- * and the 4-bit ones below.  Every array 16-byte aligned; no output
+ * for the 4-bit calls, of 16 for the integers'.  E * W < 2^31; T*k <=
+ * MOE_MAX_EXPERT_ROWS, in these calls and those below.  Every array 16-byte aligned; no output
  * overlaps an input or another output, in these calls and those below.
  * Products are summed in fp32, in an order that the sizes, the counts of rows and
  * the device fix, and rounded once to bf16. */
