@@ -1027,6 +1027,11 @@ pair_kernel(const ExpertArgs a, const Cut cut, const __grid_constant__ CUtensorM
     // Not before: blocks of the next kernel that came early would crowd on the SMs that this one leaves free (1014 rows
     // quantised and multiplied in 4 bits, 1216 -> 2 x 864: 21.0 us, and 15.7 us this way).
     pdl_launch_dependents();
+    // Commits arrive on barriers of both CTAs, and the cluster's meeting does not wait for them: this CTA ends when the last
+    // one, behind all others, has arrived here too (the first CTA has waited for its own).
+    if (warp == 1 && cta == 1 && !warp_wait(smem_u32(&sh.last), 0) && lane == 0)
+        atomicOr(&g_expert_faults, MOE_FAULT_WAIT_TIMEOUT);
+    __syncwarp();
     tc::cluster_sync();
     tc::fence_after_sync();
     if (warp == 1) tc::dealloc_pair(tmem, 512);
