@@ -391,8 +391,7 @@ class Routing:
     scale: float = 1.0
 
     def c(self, logits) -> _RoutingC:
-        return _RoutingC(self.score, bool(self.renormalise), self.scale,
-                         MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32)
+        return _RoutingC(self.score, bool(self.renormalise), self.scale, _logits_kind(logits))
 
 
 @dataclass
@@ -439,6 +438,11 @@ class _Kinds(dict):
 
 
 _KINDS = _Kinds()
+
+
+def _logits_kind(logits) -> int:
+    kind = getattr(logits, "dtype", None)
+    return MOE_LOGITS_BF16 if kind is not None and kind in _KINDS["bfloat16"] else MOE_LOGITS_F32
 
 
 def _take(where: str, t, kinds: str, *shape):
@@ -626,8 +630,7 @@ _CHOICE = _ChoiceStructs()
 def moe_route_groups(problem: Problem, routing: Routing, grouping: Grouping, logits, ids, gates, bias=None, stream=None):
     """moe_route with every token's choice limited to `grouping.kept` groups of experts; keys are scores (+ bias)."""
     p, where = problem, "moe_route_groups"
-    kind = MOE_LOGITS_BF16 if getattr(logits, "itemsize", 4) == 2 else MOE_LOGITS_F32
-    values = routing.score, routing.renormalise, routing.scale, kind, grouping.groups, grouping.kept, grouping.top
+    values = routing.score, routing.renormalise, routing.scale, _logits_kind(logits), grouping.groups, grouping.kept, grouping.top
     try:
         choice = _CHOICE[_CHOICE_VALUES.pack(*values)]
     except (struct.error, OverflowError):  # no numbers, or past 32 bits: as the structs of the other calls take them
